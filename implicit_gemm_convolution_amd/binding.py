@@ -27,12 +27,27 @@ IGC_EOVERFLOW = -3
 IGC_EHIP = -4
 IGC_ENODEV = -5
 
+# Element types and activations of the feed-forward operators.
+IGC_F16 = 0
+IGC_BF16 = 1
+IGC_F32 = 2
+IGC_ACT_NONE = 0
+IGC_ACT_RELU = 1
+IGC_ACT_GELU = 2
+IGC_ACT_GELU_TANH = 3
+IGC_ACT_SILU = 4
+IGC_ACT_SIGMOID = 5
+IGC_WS_HEADER = 8192  # workspace bytes that are zero between calls
+
 # Every symbol include/igc.h declares.
 EXPORTED = ("gemm_f16f32", "gemm_u8i8_zp", "conv2d_implicit_gemm", "conv2d_u8i8_zp",
             "gemm_f16f32_workspace_size", "gemm_u8i8_zp_workspace_size",
             "conv2d_implicit_gemm_workspace_size", "conv2d_u8i8_zp_workspace_size",
             "gemm_f16f32_noalloc", "conv2d_implicit_gemm_nhwcnc", "conv2d_implicit_gemm_nhwcnc_workspace_size",
             "u8i8_colsum",
+            "linear_forward", "linear_forward_workspace_size", "linear_backward", "linear_backward_workspace_size",
+            "glu_forward", "glu_forward_workspace_size", "glu_backward", "glu_backward_workspace_size",
+            "grad_clip", "grad_clip_workspace_size",
             "igc_status_string", "igc_last_error", "igc_device_check", "igc_set_tuning")
 
 
@@ -58,6 +73,41 @@ class Epilogue(ctypes.Structure):
         ("ws_bytes", ctypes.c_size_t),
         ("colsum_B", ctypes.c_void_p),
     ]
+
+
+def _fields(text):
+    """Structure fields from "name:kind" words: i int, p pointer, f float, z size_t."""
+    kinds = {"i": ctypes.c_int, "p": ctypes.c_void_p, "f": ctypes.c_float, "z": ctypes.c_size_t}
+    return [(w.split(":")[0], kinds[w.split(":")[1]]) for w in text.split()]
+
+
+class LinearForward(ctypes.Structure):
+    """igc_linear_forward."""
+    _fields_ = _fields("M:i N:i K:i type:i act:i y_type:i X:p ldx:i W:p ldw:i bias:p R:p ldr:i Y:p ldy:i Z:p ldz:i "
+                       "workspace:p ws_bytes:z")
+
+
+class LinearBackward(ctypes.Structure):
+    """igc_linear_backward."""
+    _fields_ = _fields("M:i N:i K:i type:i act:i dY:p lddy:i Z:p ldz:i X:p ldx:i W:p ldw:i dX:p lddx:i dW:p lddw:i "
+                       "dbias:p workspace:p ws_bytes:z")
+
+
+class GluForward(ctypes.Structure):
+    """igc_glu_forward."""
+    _fields_ = _fields("M:i N:i K:i type:i act:i X:p ldx:i Wg:p ldwg:i Wu:p ldwu:i bias_g:p bias_u:p H:p ldh:i "
+                       "G:p ldg:i U:p ldu:i workspace:p ws_bytes:z")
+
+
+class GluBackward(ctypes.Structure):
+    """igc_glu_backward."""
+    _fields_ = _fields("M:i N:i K:i type:i act:i dH:p lddh:i G:p ldg:i U:p ldu:i X:p ldx:i Wg:p ldwg:i Wu:p ldwu:i "
+                       "dX:p lddx:i dWg:p lddwg:i dWu:p lddwu:i dbias_g:p dbias_u:p workspace:p ws_bytes:z")
+
+
+class GradClip(ctypes.Structure):
+    """igc_grad_clip."""
+    _fields_ = _fields("count:i grads:p outs:p sizes:p types:p max_norm:f norm:p workspace:p ws_bytes:z")
 
 
 _lib = None
@@ -100,6 +150,12 @@ def load() -> ctypes.CDLL:
         getattr(L, name).restype = i
     L.u8i8_colsum.argtypes = [i, i, p, i, p, p]
     L.u8i8_colsum.restype = i
+    for name, desc in (("linear_forward", LinearForward), ("linear_backward", LinearBackward),
+                       ("glu_forward", GluForward), ("glu_backward", GluBackward), ("grad_clip", GradClip)):
+        getattr(L, name).argtypes = [ctypes.POINTER(desc), p]
+        getattr(L, name).restype = i
+        getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(desc), pz]
+        getattr(L, name + "_workspace_size").restype = i
     L.igc_set_tuning.argtypes = [i, i]
     L.igc_set_tuning.restype = i
     L.igc_status_string.argtypes = [i]
@@ -256,3 +312,139 @@ def conv2d_u8i8_zp(Nb, H, W, C, Kout, R, S, stride_h, stride_w, pad_h, pad_w, x,
     st = load().conv2d_u8i8_zp(Nb, H, W, C, Kout, R, S, stride_h, stride_w, pad_h, pad_w, _addr(x), zA,
                                _addr(w), zB, ctypes.byref(ep), _stream(stream))
     return _check(st, "conv2d_u8i8_zp") if check else st
+
+
+# ---------------------------------------------------------------------------
+# The feed-forward operators.  Each <entry>_workspace_size takes the entry's
+# arguments (but for workspace and stream) and returns the bytes that the
+# call needs.
+# ---------------------------------------------------------------------------
+def _linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, type, act, y_type, bias, R, ldr, Z, ldz, workspace, ws_bytes):
+    return LinearForward(M, N, K, type, act, type if y_type is None else y_type, _addr(X), ldx, _addr(W), ldw, _addr(bias),
+                         _addr(R), ldr, _addr(Y), ldy, _addr(Z), ldz, _addr(workspace), _ws_bytes(workspace, ws_bytes))
+
+
+def linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, *, type=IGC_BF16, act=IGC_ACT_NONE, y_type=None, bias=None, R=None, ldr=0,
+                   Z=None, ldz=0, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """Z = X W^T + bias; Y = act(Z) + R (y_type None: the operands' type)."""
+    d = _linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, type, act, y_type, bias, R, ldr, Z, ldz, workspace, ws_bytes)
+    st = load().linear_forward(d, _stream(stream))
+    return _check(st, "linear_forward") if check else st
+
+
+def linear_forward_workspace_size(M, N, K, X, ldx, W, ldw, Y, ldy, *, type=IGC_BF16, act=IGC_ACT_NONE, y_type=None, bias=None,
+                                  R=None, ldr=0, Z=None, ldz=0) -> int:
+    return _ws_query("linear_forward_workspace_size",
+                     _linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, type, act, y_type, bias, R, ldr, Z, ldz, None, 0))
+
+
+def _linear_backward(M, N, K, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias, type, act, workspace, ws_bytes):
+    return LinearBackward(M, N, K, type, act, _addr(dY), lddy, _addr(Z), ldz, _addr(X), ldx, _addr(W), ldw, _addr(dX), lddx,
+                          _addr(dW), lddw, _addr(dbias), _addr(workspace), _ws_bytes(workspace, ws_bytes))
+
+
+def linear_backward(M, N, K, dY, lddy, *, Z=None, ldz=0, X=None, ldx=0, W=None, ldw=0, dX=None, lddx=0, dW=None, lddw=0,
+                    dbias=None, type=IGC_BF16, act=IGC_ACT_NONE, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """D = dY act'(Z); dX = D W; dW = D^T X; dbias = column sums of D (any subset)."""
+    d = _linear_backward(M, N, K, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias, type, act, workspace, ws_bytes)
+    st = load().linear_backward(d, _stream(stream))
+    return _check(st, "linear_backward") if check else st
+
+
+def linear_backward_workspace_size(M, N, K, dY, lddy, *, Z=None, ldz=0, X=None, ldx=0, W=None, ldw=0, dX=None, lddx=0, dW=None,
+                                   lddw=0, dbias=None, type=IGC_BF16, act=IGC_ACT_NONE) -> int:
+    return _ws_query("linear_backward_workspace_size",
+                     _linear_backward(M, N, K, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias, type, act, None, 0))
+
+
+def _glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, bias_g, bias_u, G, ldg, U, ldu, type, act, workspace, ws_bytes):
+    return GluForward(M, N, K, type, act, _addr(X), ldx, _addr(Wg), ldwg, _addr(Wu), ldwu, _addr(bias_g), _addr(bias_u),
+                      _addr(H), ldh, _addr(G), ldg, _addr(U), ldu, _addr(workspace), _ws_bytes(workspace, ws_bytes))
+
+
+def glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, *, bias_g=None, bias_u=None, G=None, ldg=0, U=None, ldu=0,
+                type=IGC_BF16, act=IGC_ACT_SILU, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """G = X Wg^T + bias_g; U = X Wu^T + bias_u; H = act(G) U."""
+    d = _glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, bias_g, bias_u, G, ldg, U, ldu, type, act, workspace, ws_bytes)
+    st = load().glu_forward(d, _stream(stream))
+    return _check(st, "glu_forward") if check else st
+
+
+def glu_forward_workspace_size(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, *, bias_g=None, bias_u=None, G=None, ldg=0, U=None,
+                               ldu=0, type=IGC_BF16, act=IGC_ACT_SILU) -> int:
+    return _ws_query("glu_forward_workspace_size",
+                     _glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, bias_g, bias_u, G, ldg, U, ldu, type, act, None, 0))
+
+
+def _glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg, dWu, lddwu, dbias_g,
+                  dbias_u, type, act, workspace, ws_bytes):
+    return GluBackward(M, N, K, type, act, _addr(dH), lddh, _addr(G), ldg, _addr(U), ldu, _addr(X), ldx, _addr(Wg), ldwg,
+                       _addr(Wu), ldwu, _addr(dX), lddx, _addr(dWg), lddwg, _addr(dWu), lddwu, _addr(dbias_g), _addr(dbias_u),
+                       _addr(workspace), _ws_bytes(workspace, ws_bytes))
+
+
+def glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, *, X=None, ldx=0, Wg=None, ldwg=0, Wu=None, ldwu=0, dX=None, lddx=0,
+                 dWg=None, lddwg=0, dWu=None, lddwu=0, dbias_g=None, dbias_u=None, type=IGC_BF16, act=IGC_ACT_SILU,
+                 stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """dU = dH act(G), dG = dH U act'(G); dX = dG Wg + dU Wu; dW* = d*^T X; dbias_* = column sums (any subset)."""
+    d = _glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg, dWu, lddwu, dbias_g,
+                      dbias_u, type, act, workspace, ws_bytes)
+    st = load().glu_backward(d, _stream(stream))
+    return _check(st, "glu_backward") if check else st
+
+
+def glu_backward_workspace_size(M, N, K, dH, lddh, G, ldg, U, ldu, *, X=None, ldx=0, Wg=None, ldwg=0, Wu=None, ldwu=0, dX=None,
+                                lddx=0, dWg=None, lddwg=0, dWu=None, lddwu=0, dbias_g=None, dbias_u=None, type=IGC_BF16,
+                                act=IGC_ACT_SILU) -> int:
+    return _ws_query("glu_backward_workspace_size",
+                     _glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg, dWu,
+                                   lddwu, dbias_g, dbias_u, type, act, None, 0))
+
+
+_DTYPES = {"torch.float16": IGC_F16, "torch.bfloat16": IGC_BF16, "torch.float32": IGC_F32}
+
+
+def _tensor_type(t) -> int:
+    try:
+        return _DTYPES[str(t.dtype)]
+    except KeyError:
+        raise TypeError(f"grad_clip takes float16, bfloat16 and float32 tensors, not {t.dtype}") from None
+
+
+def _grad_clip(grads, max_norm, norm, out, workspace, ws_bytes):
+    n = len(grads)
+    if out is not None and len(out) != n:
+        raise ValueError(f"{n} gradients but {len(out)} outputs")
+    for pair in (grads, out or ()):
+        for t in pair:
+            if not t.is_contiguous():
+                raise ValueError("grad_clip takes contiguous tensors")
+    types = [_tensor_type(t) for t in grads]
+    sizes = [t.numel() for t in grads]
+    if out is not None:
+        for g, o in zip(grads, out):
+            if o.dtype != g.dtype or o.numel() != g.numel():
+                raise ValueError("an output differs from its gradient in type or size")
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
+    outs = None if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
+    sizes, types = (ctypes.c_longlong * n)(*sizes), (ctypes.c_int * n)(*types)
+    a = ctypes.addressof
+    d = GradClip(n, a(ptrs), None if outs is None else a(outs), a(sizes), a(types), float(max_norm), _addr(norm),
+                 _addr(workspace), _ws_bytes(workspace, ws_bytes))
+    return d, (ptrs, outs, sizes, types)  # (the arrays live until the call returns)
+
+
+def grad_clip(grads, max_norm, norm, *, out=None, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """norm = the global norm of `grads` (contiguous fp16 / bf16 / fp32 tensors); out = grads * min(1, max_norm / (norm + 1e-6)),
+    in place without `out`."""
+    d, keep = _grad_clip(grads, max_norm, norm, out, workspace, ws_bytes)
+    st = load().grad_clip(d, _stream(stream))
+    del keep
+    return _check(st, "grad_clip") if check else st
+
+
+def grad_clip_workspace_size(grads, max_norm, norm, *, out=None) -> int:
+    d, keep = _grad_clip(grads, max_norm, norm, out, None, 0)
+    size = _ws_query("grad_clip_workspace_size", d)
+    del keep
+    return size

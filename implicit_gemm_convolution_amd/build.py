@@ -1,8 +1,9 @@
 """Build libigc.so (the HIP kernels and the C ABI) in-tree with hipcc for gfx950.
 
-The C ABI (csrc/igc.hip) and the kernel instantiations (csrc/igc_launch.hip,
-compiled once per kernel kind with -DIGC_LAUNCH_UNIT=<n>) are separate
-objects compiled in parallel, then linked into one shared library.
+The C ABI (csrc/igc.hip, csrc/ffn.hip) and the kernel instantiations
+(csrc/igc_launch.hip and csrc/ffn_launch.hip, compiled once per kernel kind
+with -DIGC_LAUNCH_UNIT=<n> and -DIGC_FFN_UNIT=<n>) are separate objects
+compiled in parallel, then linked into one shared library.
 """
 from __future__ import annotations
 
@@ -20,7 +21,10 @@ LIB_PATH = os.path.join(PKG, "libigc.so")
 ABI_SOURCE = os.path.join(CSRC, "igc.hip")
 LAUNCH_SOURCE = os.path.join(CSRC, "igc_launch.hip")
 LAUNCH_UNITS = 38  # the (kind, variant) pairs of IGC_LAUNCH_KINDS in igc_host.hpp
-SOURCES = [ABI_SOURCE, LAUNCH_SOURCE]
+FFN_SOURCE = os.path.join(CSRC, "ffn.hip")
+FFN_LAUNCH_SOURCE = os.path.join(CSRC, "ffn_launch.hip")
+FFN_LAUNCH_UNITS = 8  # the (type, layout) pairs of IGC_FFN_KINDS in ffn_host.hpp
+SOURCES = [ABI_SOURCE, LAUNCH_SOURCE, FFN_SOURCE, FFN_LAUNCH_SOURCE]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 HIP_FLAGS = [
@@ -42,6 +46,9 @@ def _units():
     yield ABI_SOURCE, [], "igc.o"
     for n in range(LAUNCH_UNITS):
         yield LAUNCH_SOURCE, [f"-DIGC_LAUNCH_UNIT={n}"], f"igc_launch_{n}.o"
+    yield FFN_SOURCE, [], "ffn.o"
+    for n in range(FFN_LAUNCH_UNITS):
+        yield FFN_LAUNCH_SOURCE, [f"-DIGC_FFN_UNIT={n}"], f"ffn_launch_{n}.o"
 
 
 def _jobs() -> int:

@@ -1,0 +1,667 @@
+// ffn_kernels.hpp -- the feed-forward operators on gfx950: 16-bit (fp16 or
+// bf16) matrix products with fused epilogues, the element-wise part of their
+// backward passes, and gradient clipping.
+//
+//   linear   Z = X W^T + b;  Y = act(Z) + R
+//   glu      G = X Wg^T + bg;  U = X Wu^T + bu;  H = act(G) * U
+//   back     D = dY act'(Z);  dX = D W;  dW = D^T X;  db = sum over rows of D
+//            dG = dH U act'(G), dU = dH act(G);  dX = dG Wg + dU Wu; ...
+//   clip     norm = sqrt(sum g^2);  out = g min(1, max_norm / (norm + 1e-6))
+//
+// Every product accumulates in fp32 on the 16x16x32 matrix instructions, and
+// bias, activation and residual are applied to the fp32 sums: one rounding,
+// at the store.  The backward products take D rounded to the operands' type,
+// as the matrix cores do: each term is then off by at most half a step of
+// that type, independently of the others, so a sum over r terms is off by
+// less than its own final rounding once r is more than a few.  db sums the
+// unrounded fp32 values.
+#pragma once
+
+#include "igc_kernels.hpp"
+
+namespace igc_ffn {
+
+using igc::CHUNK_BYTES;
+using igc::Rsrc;
+using igc::f32x4;
+using igc::lds_barrier;
+using igc::lds_read16;
+using igc::lds_write16;
+using igc::make_rsrc;
+using igc::static_for;
+using igc::swz;
+using igc::wait_vmcnt_lgkm0;
+using igc::wave_id;
+
+// ---------------------------------------------------------------------------
+// Element types.
+// ---------------------------------------------------------------------------
+enum Type : int { T_F16 = 0, T_BF16 = 1, T_F32 = 2 };
+enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4, ACT_SIGMOID = 5 };
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <bool BF>
+__device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
+  if constexpr (BF) {
+    a = __builtin_bit_cast(float, v << 16);
+    b = __builtin_bit_cast(float, v & 0xffff0000u);
+  } else {
+    const f16x2 h = __builtin_bit_cast(f16x2, v);
+    a = (float)h[0];
+    b = (float)h[1];
+  }
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {  // round to nearest even
+  if constexpr (BF) {
+    bf16x2 h;
+    h[0] = (__bf16)a;
+    h[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    f16x2 h;
+    h[0] = (_Float16)a;
+    h[1] = (_Float16)b;
+    return __builtin_bit_cast(uint32_t, h);
+  }
+}
+template <bool BF>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  unpack2<BF>(v.x, f[0], f[1]);
+  unpack2<BF>(v.y, f[2], f[3]);
+  unpack2<BF>(v.z, f[4], f[5]);
+  unpack2<BF>(v.w, f[6], f[7]);
+}
+template <bool BF>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2<BF>(f[0], f[1]), pack2<BF>(f[2], f[3]), pack2<BF>(f[4], f[5]), pack2<BF>(f[6], f[7]));
+}
+
+// Eight 16-bit elements from any 2-byte aligned address; elements past
+// `valid` read as zero and are not touched.  (The GPU takes 16-byte loads at
+// any address.)
+__device__ __forceinline__ uint4 load8(const uint8_t* p, int valid) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (valid >= 8) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (valid > 0) {
+    const uint16_t* const q = reinterpret_cast<const uint16_t*>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < valid) w[e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+__device__ __forceinline__ void store8(uint8_t* p, const uint4& v, int valid) {
+  if (valid >= 8) {
+    __builtin_memcpy(p, &v, 16);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint16_t* const q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < valid) q[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Activations, in fp32.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+// 1 / (1 + exp(-z)); exp overflowing to infinity gives 0
+__device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_f(-z)); }
+// The normal distribution function of z and e = exp(-z^2 / 2):
+// erfc(x) = exp(-x^2) t P(t), t = 1 / (1 + x/2), x = |z| / sqrt 2, with P a
+// least-squares fit of exp(x^2) erfc(x) / t (relative error 4e-8 before
+// rounding; about 4e-7 evaluated in fp32), so that the negative tail keeps
+// its relative accuracy.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float x = __builtin_fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, x, 1.0f));
+  e = exp_f(-0.5f * z * z);
+  float q = -0.05781668414637441f;
+  q = __builtin_fmaf(q, t, 0.27839578762714456f);
+  q = __builtin_fmaf(q, t, -0.47423681396851763f);
+  q = __builtin_fmaf(q, t, 0.26300854998394246f);
+  q = __builtin_fmaf(q, t, -0.01606377351405429f);
+  q = __builtin_fmaf(q, t, 0.1981216336858939f);
+  q = __builtin_fmaf(q, t, 0.2442873611701233f);
+  q = __builtin_fmaf(q, t, 0.2822075600438619f);
+  q = __builtin_fmaf(q, t, 0.28209634074354567f);
+  const float tail = 0.5f * e * t * q;  // erfc(x) / 2
+  return z > 0.0f ? 1.0f - tail : tail;
+}
+constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// f(z) and, with SLOPE, f'(z).  (gelu_tanh: (1 + tanh a) / 2 = sigmoid(2a).)
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ void act_one(float z, float& f, float& d) {
+  if constexpr (ACT == ACT_NONE) {
+    f = z;
+    if constexpr (SLOPE) d = 1.0f;
+  } else if constexpr (ACT == ACT_RELU) {
+    f = z < 0.0f ? 0.0f : z;  // (NaN stays NaN)
+    if constexpr (SLOPE) d = z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == ACT_GELU) {
+    float e;
+    const float c = normal_cdf(z, e);
+    f = z * c;
+    if constexpr (SLOPE) d = __builtin_fmaf(z * 0.39894228040143268f, e, c);
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    const float z2 = z * z;
+    const float s = sigmoid_f(2.0f * kGeluC * z * __builtin_fmaf(kGeluA, z2, 1.0f));
+    f = z * s;
+    if constexpr (SLOPE) d = s + f * (1.0f - s) * (2.0f * kGeluC) * __builtin_fmaf(3.0f * kGeluA, z2, 1.0f);
+  } else {
+    const float s = sigmoid_f(z);
+    if constexpr (ACT == ACT_SILU) {
+      f = z * s;
+      if constexpr (SLOPE) d = __builtin_fmaf(f, 1.0f - s, s);
+    } else {
+      f = s;
+      if constexpr (SLOPE) d = s * (1.0f - s);
+    }
+  }
+}
+template <int ACT, bool SLOPE, int N>
+__device__ __forceinline__ void act_all(const float (&z)[N], float (&f)[N], float (&d)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) act_one<ACT, SLOPE>(z[i], f[i], d[i]);
+}
+// the activation is a wave-uniform value: one scalar branch per N elements
+template <bool SLOPE, int N>
+__device__ __forceinline__ void act_n(int act, const float (&z)[N], float (&f)[N], float (&d)[N]) {
+  switch (act) {
+    case ACT_RELU: return act_all<ACT_RELU, SLOPE>(z, f, d);
+    case ACT_GELU: return act_all<ACT_GELU, SLOPE>(z, f, d);
+    case ACT_GELU_TANH: return act_all<ACT_GELU_TANH, SLOPE>(z, f, d);
+    case ACT_SILU: return act_all<ACT_SILU, SLOPE>(z, f, d);
+    case ACT_SIGMOID: return act_all<ACT_SIGMOID, SLOPE>(z, f, d);
+    default: return act_all<ACT_NONE, SLOPE>(z, f, d);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The matrix products.
+// ---------------------------------------------------------------------------
+// How the operands lie in memory.  ROW: the reduction runs along a row (one
+// row per output row or column).  COL: the reduction runs down the rows.
+//   FWD   out[m][n] = sum_k X[m][k] W[n][k]             A ROW, B ROW
+//   GLU   the same with two B operands, side by side    A ROW, B ROW
+//   DX    out[m][k] = sum_n D[m][n] W[n][k]             A ROW, B COL
+//   DW    out[n][k] = sum_m D[m][n] X[m][k]             A COL, B COL
+enum Mode : int { M_FWD = 0, M_GLU = 1, M_DX = 2, M_DW = 3 };
+
+struct GemmArgs {
+  int M, N, R;  // output rows, output columns (of each product), reduction
+  const uint8_t *A, *B, *B2;
+  long long lda, ldb, ldb2;  // elements
+  // DX over two weights: reduction rows [0, b_rows) come from B and
+  // [r_split, r_split + b_rows) from B2; r_split is a multiple of 64, and A
+  // holds zeros between.  Without: r_split = b_rows = R.
+  int r_split, b_rows;
+  // epilogue
+  int act;
+  const float *bias, *bias2;
+  const uint8_t* res;  // R, of Y's type
+  long long ldr;
+  uint8_t* Y;
+  long long ldy;
+  int y_f32;
+  uint8_t *Z, *U;  // kept sums, of the operands' type
+  long long ldz, ldu;
+  // DW of two weights: output rows [0, m_rows) go to Y and
+  // [m_split, m_split + m_rows) to Y2.  Without: m_split = m_rows = M.
+  uint8_t* Y2;
+  long long ldy2;
+  int m_split, m_rows;
+  // work split
+  int tiles_m, tiles_n, regroup;
+  int splits;  // workgroups that share a tile's reduction
+  float* part;  // their partial tiles
+  int* cnt;     // one arrival counter per tile, zero between launches
+};
+
+template <bool BF>
+__device__ __forceinline__ void mfma16(f32x4& c, const uint4& a, const uint4& b) {
+  if constexpr (BF)
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// An operand's K tile in LDS: W rows (or columns) x 64 reduction elements.
+//  ROW: W rows of 128 bytes, chunk c of row r in slot c ^ ((r >> 1) & 7).
+//  COL: 64 reduction rows of W elements.  Fragments are read with the
+//  transposing LDS load: 16 lanes take a 4 x 16 block (4 reduction rows of
+//  32 bytes) and each lane gets one column.  A half wave reads reduction rows
+//  {0..3, 8..11} of one 32-byte granule: the granule index is XOR-ed with
+//  those row bits, so the 8 pieces cover all 64 banks.
+template <int W, bool COL>
+struct LdsTile {
+  static constexpr int BYTES = W * 128;
+  static constexpr int ROWB = W * 2;  // COL: bytes per reduction row
+  __device__ static __forceinline__ int gran(int kr) {  // COL: the granule XOR of reduction row kr
+    if constexpr (W >= 128) return (kr & 3) | (((kr >> 3) & 1) << 2);
+    return ((kr >> 1) & 1) | (((kr >> 3) & 1) << 1);
+  }
+  // byte offset of 16-byte chunk c of (ROW) row r / (COL) reduction row r
+  __device__ static __forceinline__ int chunk_off(int r, int c) {
+    if constexpr (!COL) return swz(r, c);
+    return r * ROWB + (((c >> 1) ^ gran(r)) << 5) + (c & 1) * 16;
+  }
+  // fragment of rows (columns) blk0 .. blk0+15, k-step ks: lane l holds row
+  // l % 16, reduction elements 32 ks + 8 (l / 16) .. +7
+  __device__ static __forceinline__ uint4 frag(const uint8_t* st, int blk0, int ks) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (!COL) {
+      return lds_read16(st, swz(blk0 + (lane & 15), ks * 4 + (lane >> 4)));
+    } else {
+      const int i = lane & 15, g = lane >> 4;
+      const int kr = 8 * g + (i >> 2);  // (bit 2 and the bits from 5 up do not enter gran())
+      const int off = kr * ROWB + (((blk0 >> 4) ^ gran(kr)) << 5) + (i & 3) * 8;
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const uint8_t* const p = st + off + ks * 32 * ROWB;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWB));
+      const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
+      return make_uint4(l2.x, l2.y, h2.x, h2.y);
+    }
+  }
+};
+
+// Loading an operand's K tiles through registers, from rows of any
+// alignment, stride and length.
+template <int W, bool COL, bool TWO>
+struct RegOperand {
+  typedef LdsTile<W, COL> Tile;
+  static constexpr int NC = W * 8 / 256;  // 16-byte chunks per thread
+  const uint8_t *p, *p2;
+  long long ld, ld2;  // bytes
+  int o0, extent, R, r_split, r_rows;
+  __device__ __forceinline__ void init(const uint8_t* ptr, long long l, const uint8_t* ptr2, long long l2, int o, int ext,
+                                       int red, int split, int rows) {
+    p = ptr;
+    p2 = ptr2;
+    ld = l * 2;
+    ld2 = l2 * 2;
+    o0 = o;
+    extent = ext;
+    R = red;
+    r_split = split;
+    r_rows = rows;
+  }
+  __device__ __forceinline__ void load(int kt, uint4 (&v)[NC]) const {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int idx = threadIdx.x + 256 * j;
+      if constexpr (!COL) {
+        const int c = idx & 7, k = kt * 64 + c * 8;
+        int row = idx >> 3;
+        const bool second = TWO && row >= W / 2;
+        if (second) row -= W / 2;
+        const int o = o0 + row;
+        const uint8_t* const q = (second ? p2 : p) + (long long)o * (second ? ld2 : ld) + (long long)k * 2;
+        v[j] = load8(q, o < extent ? R - k : 0);
+      } else {
+        const int c = idx % (W / 8);
+        int r = kt * 64 + idx / (W / 8);
+        const int o = o0 + c * 8;
+        const bool in = r < R;  // (without a second operand r_split is R: rows past it are no rows of p2)
+        const bool second = TWO && r >= r_split;
+        if (second) r -= r_split;
+        const uint8_t* const q = (second ? p2 : p) + (long long)r * (second ? ld2 : ld) + (long long)o * 2;
+        v[j] = load8(q, in && r < r_rows ? extent - o : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* st, const uint4 (&v)[NC]) const {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int idx = threadIdx.x + 256 * j;
+      lds_write16(st, COL ? Tile::chunk_off(idx / (W / 8), idx % (W / 8)) : Tile::chunk_off(idx >> 3, idx & 7), v[j]);
+    }
+  }
+};
+
+// Logical tile of workgroup b.  The dispatcher hands workgroups to the 8 XCDs
+// round-robin; with more than one round of compute units each XCD gets a
+// contiguous run of logical tiles, laid out in groups of 8 tile rows, so the
+// workgroups that share an L2 share operand panels.
+__device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& tn) {
+  int t = b;
+  if (p.regroup) {
+    const int n = p.tiles_m * p.tiles_n, x = b & 7;
+    t = x * (n >> 3) + min(x, n & 7) + (b >> 3);
+  }
+  const int per = 8 * p.tiles_n, group = t / per, first = group * 8;
+  const int in = t - group * per, rows = min(8, p.tiles_m - first);
+  tn = in / rows;
+  tm = first + in - tn * rows;
+}
+
+// One wave's 16 x TNW block row leaves for the outputs: `f` holds 8
+// consecutive sums of one row (and `u` those of the second product).
+template <bool BF, int MODE>
+struct Epilogue {
+  const GemmArgs& p;
+  int col;       // this lane's first column
+  int left;      // columns from there to the end
+  float b1[8], b2[8];
+  bool has_bias;
+  __device__ __forceinline__ Epilogue(const GemmArgs& args, int c) : p(args), col(c), left(args.N - c) {
+    has_bias = (MODE == M_FWD && p.bias) || (MODE == M_GLU && (p.bias || p.bias2));
+    if constexpr (MODE == M_FWD || MODE == M_GLU) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        b1[e] = p.bias && e < left ? p.bias[col + e] : 0.0f;
+        b2[e] = MODE == M_GLU && p.bias2 && e < left ? p.bias2[col + e] : 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void put16(uint8_t* base, long long ld, int row, const float (&f)[8]) const {
+    store8(base + ((long long)row * ld + col) * 2, pack8<BF>(f), left);
+  }
+  __device__ __forceinline__ void operator()(int row, float (&f)[8], float (&u)[8]) const {
+    if (row >= p.M || left <= 0) return;
+    if constexpr (MODE == M_DX) {
+      put16(p.Y, p.ldy, row, f);
+    } else if constexpr (MODE == M_DW) {
+      const bool second = row >= p.m_split;
+      const int r = second ? row - p.m_split : row;
+      uint8_t* const y = second ? p.Y2 : p.Y;  // (either may be left out)
+      if (y && r < p.m_rows) put16(y, second ? p.ldy2 : p.ldy, r, f);
+    } else {
+      float y[8], unused[8];
+      if (has_bias) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += b1[e];
+        if constexpr (MODE == M_GLU) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] += b2[e];
+        }
+      }
+      if (p.Z) put16(p.Z, p.ldz, row, f);
+      act_n<false>(p.act, f, y, unused);
+      if constexpr (MODE == M_GLU) {
+        if (p.U) put16(p.U, p.ldu, row, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= u[e];
+        put16(p.Y, p.ldy, row, y);
+      } else if (!p.y_f32) {
+        if (p.res) {
+          float r[8];
+          unpack8<BF>(load8(p.res + ((long long)row * p.ldr + col) * 2, left), r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] += r[e];
+        }
+        put16(p.Y, p.ldy, row, y);
+      } else {
+        if (p.res) {
+          const float* const q = reinterpret_cast<const float*>(p.res) + (long long)row * p.ldr + col;
+          if (left >= 8) {
+            float r[8];
+            __builtin_memcpy(r, q, 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += r[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < left) y[e] += q[e];
+          }
+        }
+        float* const q = reinterpret_cast<float*>(p.Y) + (long long)row * p.ldy + col;
+        if (left >= 8) {
+          __builtin_memcpy(q, y, 32);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < left) q[e] = y[e];
+        }
+      }
+    }
+  }
+};
+
+// Joining the workgroups that share a tile's reduction.  Each writes its
+// accumulators in lane order; the one that arrives last adds all of them in
+// split order (its own included: the sum does not depend on who is last) and
+// carries on to the epilogue.  Returns whether this workgroup does.
+// The stores have reached this XCD's L2 before the barrier (vmcnt 0); the
+// arrival is a device-scope release (writes the L2 back) and acquire
+// (invalidates the caches before the partials are read).
+template <int NQ>
+__device__ __forceinline__ bool join_splits(const GemmArgs& p, int tile, int split, f32x4* acc, uint8_t* lds) {
+  f32x4* const slot = reinterpret_cast<f32x4*>(p.part) + (long long)tile * p.splits * NQ * 256 + threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) slot[((long long)split * NQ + q) * 256] = acc[q];
+  wait_vmcnt_lgkm0<0>();
+  __syncthreads();
+  volatile int* const flag = reinterpret_cast<volatile int*>(lds);
+  if (threadIdx.x == 0) {
+    const int n = __hip_atomic_fetch_add(p.cnt + tile, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = n == p.splits - 1;
+    // every other split has counted itself in: the counter is free again
+    if (last) __hip_atomic_store(p.cnt + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = last;
+  }
+  __syncthreads();
+  const bool last = *flag != 0;
+  __syncthreads();
+  if (!last) return false;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) acc[q] = slot[(long long)q * 256];
+  for (int s = 1; s < p.splits; ++s) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) acc[q] += slot[((long long)s * NQ + q) * 256];
+  }
+  return true;
+}
+
+// The accumulators of a wave (FM x FN blocks, each transposed by the matrix
+// instruction: lane l holds row l % 16, columns 4 (l / 16) .. +3) leave
+// through the wave's own piece of LDS, one block row at a time, so that every
+// lane gets 8 consecutive columns of a row and a store instruction covers
+// whole 128-byte lines.  No barrier: a wave's LDS accesses are in order.
+template <bool BF, int MODE, int FM, int FN>
+__device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[FM][FN], uint8_t* lds, int row0, int col0) {
+  constexpr bool GLU = MODE == M_GLU;
+  constexpr int TN = FN * 16, OUT = GLU ? TN / 2 : TN;  // staged columns, output columns
+  constexpr int LPR = OUT / 8, RPP = 64 / LPR;          // lanes per row, rows per pass
+  static_assert(RPP <= 16, "a pass covers at most one block row");
+  constexpr int XM = TN / 4 < 16 ? TN / 4 - 1 : 15;
+  const int lane = threadIdx.x & 63;
+  const int wr = lane & 15, rr = lane / LPR, rc = lane % LPR;
+  const Epilogue<BF, MODE> out(p, col0 + rc * 8);
+  auto quad = [&](int r, int q) { return r * (TN * 4) + ((q ^ (r & XM)) << 4); };  // 4 columns of a staged row
+  auto read8 = [&](int r, int c, float (&f)[8]) {
+    const uint4 a = lds_read16(lds, quad(r, c >> 2)), b = lds_read16(lds, quad(r, (c >> 2) + 1));
+    __builtin_memcpy(f, &a, 16);
+    __builtin_memcpy(f + 4, &b, 16);
+  };
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < FN; ++j) lds_write16(lds, quad(wr, j * 4 + (lane >> 4)), __builtin_bit_cast(uint4, acc[i][j]));
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < 16; r += RPP) {
+      float f[8], u[8];
+      read8(r + rr, rc * 8, f);
+      if constexpr (GLU) read8(r + rr, OUT + rc * 8, u);
+      out(row0 + i * 16 + r + rr, f, u);
+    }
+  }
+}
+
+// The simple product: K tiles go through registers into two LDS stages.
+// Takes every alignment and stride.
+template <bool BF, int MODE, int BM, int BN>
+__global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
+  constexpr bool GLU = MODE == M_GLU, ACOL = MODE == M_DW, BCOL = MODE == M_DX || MODE == M_DW;
+  constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
+  typedef LdsTile<BM, ACOL> TA;
+  typedef LdsTile<BN, BCOL> TB;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * (TA::BYTES + TB::BYTES)];
+  const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
+  const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+  int tm, tn;
+  tile_of(p, tile, tm, tn);
+  constexpr int ON = GLU ? BN / 2 : BN;  // output columns of a tile
+  const int m0 = tm * BM, n0 = tn * ON;
+  const int nk = max(1, (p.R + 63) / 64);
+  const int k0 = (int)((long long)nk * split / p.splits), k1 = (int)((long long)nk * (split + 1) / p.splits);
+  RegOperand<BM, ACOL, false> la;
+  RegOperand<BN, BCOL, GLU || MODE == M_DX> lb;
+  la.init(p.A, p.lda, nullptr, 0, m0, p.M, p.R, p.R, p.R);
+  lb.init(p.B, p.ldb, p.B2, p.ldb2, n0, p.N, p.R, p.r_split, p.b_rows);
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto blk_b = [&](int j) {
+    if constexpr (GLU) return j < FN / 2 ? wn * (TN / 2) + j * 16 : BN / 2 + wn * (TN / 2) + (j - FN / 2) * 16;
+    return wn * TN + j * 16;
+  };
+  uint4 va[RegOperand<BM, ACOL, false>::NC], vb[RegOperand<BN, BCOL, true>::NC];
+  la.load(k0, va);
+  lb.load(k0, vb);
+  uint8_t* const sa = smem;
+  uint8_t* const sb = smem + 2 * TA::BYTES;
+  la.store(sa, va);
+  lb.store(sb, vb);
+  __syncthreads();
+  for (int kt = k0; kt < k1; ++kt) {
+    const int cur = (kt - k0) & 1;
+    if (kt + 1 < k1) {
+      la.load(kt + 1, va);
+      lb.load(kt + 1, vb);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      uint4 fa[FM], fb[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[i] = TA::frag(sa + cur * TA::BYTES, wm * TM + i * 16, ks);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j] = TB::frag(sb + cur * TB::BYTES, blk_b(j), ks);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) mfma16<BF>(acc[i][j], fb[j], fa[i]);
+    }
+    if (kt + 1 < k1) {
+      la.store(sa + (cur ^ 1) * TA::BYTES, va);
+      lb.store(sb + (cur ^ 1) * TB::BYTES, vb);
+    }
+    __syncthreads();
+  }
+  if (p.splits > 1 && !join_splits<FM * FN>(p, tile, split, &acc[0][0], smem)) return;
+  write_out<BF, MODE, FM, FN>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+}
+
+// ---------------------------------------------------------------------------
+// The element-wise part of the backward passes.
+// ---------------------------------------------------------------------------
+struct ActBackArgs {
+  int M, N;
+  const uint8_t *dY, *Z, *U;
+  long long lddy, ldz, ldu;  // elements
+  int act;
+  uint8_t* D;      // out (NULL: only the column sums): D, or dG and dU side by side, each `width` columns
+  long long ldd;   // elements
+  int width;       // N rounded up to a multiple of 64; columns past N are written as zeros
+  float* sums;     // out (NULL: none): column sums of each row block, [row blocks][1 or 2][width]
+  int rows;        // rows per block
+};
+// A workgroup covers 512 columns (8 per lane) x `rows` rows, its four waves
+// taking rows in turn.  Streams its inputs once: bound by memory.
+template <bool BF, bool GLU>
+__global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p) {
+  __shared__ float part[GLU ? 2 : 1][4][512];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int c = blockIdx.x * 512 + lane * 8;
+  const int left = p.N - c;
+  const int r0 = blockIdx.y * p.rows, r1 = min(p.M, r0 + p.rows);
+  float s1[8], s2[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s1[e] = s2[e] = 0.0f;
+  if (c < p.width) {
+    for (int r = r0 + wave; r < r1; r += 4) {
+      float dy[8], z[8], f[8], d[8];
+      unpack8<BF>(load8(p.dY + ((long long)r * p.lddy + c) * 2, left), dy);
+      if (p.Z) unpack8<BF>(load8(p.Z + ((long long)r * p.ldz + c) * 2, left), z);
+      if constexpr (GLU) {
+        float u[8], du[8];
+        unpack8<BF>(load8(p.U + ((long long)r * p.ldu + c) * 2, left), u);
+        act_n<true>(p.act, z, f, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          du[e] = dy[e] * f[e];
+          d[e] = dy[e] * u[e] * d[e];
+          if (e >= left) du[e] = d[e] = 0.0f;
+          s1[e] += d[e];
+          s2[e] += du[e];
+        }
+        if (p.D) {
+          store8(p.D + ((long long)r * p.ldd + c) * 2, pack8<BF>(d), 8);
+          store8(p.D + ((long long)r * p.ldd + p.width + c) * 2, pack8<BF>(du), 8);
+        }
+      } else {
+        if (p.Z) {
+          act_n<true>(p.act, z, f, d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dy[e] *= d[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (e >= left) dy[e] = 0.0f;
+          s1[e] += dy[e];
+        }
+        if (p.D) store8(p.D + ((long long)r * p.ldd + c) * 2, pack8<BF>(dy), 8);
+      }
+    }
+  }
+  if (!p.sums) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    part[0][wave][lane * 8 + e] = s1[e];
+    if constexpr (GLU) part[1][wave][lane * 8 + e] = s2[e];
+  }
+  __syncthreads();
+  constexpr int NP = GLU ? 2 : 1;
+  for (int i = threadIdx.x; i < NP * 512; i += 256) {
+    const int which = i / 512, cc = i % 512, col = blockIdx.x * 512 + cc;
+    if (col < p.width)
+      p.sums[((long long)blockIdx.y * NP + which) * p.width + col] =
+          (part[which][0][cc] + part[which][1][cc]) + (part[which][2][cc] + part[which][3][cc]);
+  }
+}
+
+// out[n] = sum over row blocks of sums[block][which][n], in block order.
+struct ColsumArgs {
+  const float* sums;
+  int blocks, which_n, width, N;
+  float *out0, *out1;
+};
+template <int NONE = 0>
+__global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs p) {
+  const int n = blockIdx.x * 256 + threadIdx.x, which = blockIdx.y;
+  float* const out = which ? p.out1 : p.out0;
+  if (n >= p.N || !out) return;
+  float s = 0.0f;
+  for (int b = 0; b < p.blocks; ++b) s += p.sums[((long long)b * p.which_n + which) * p.width + n];
+  out[n] = s;
+}
+
+}  // namespace igc_ffn

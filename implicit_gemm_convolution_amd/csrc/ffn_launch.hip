@@ -1,0 +1,42 @@
+// ffn_launch.hip -- the kernels of the feed-forward products: launch_product
+// of ffn_host.hpp for the pairs of IGC_FFN_KINDS.  The build compiles this
+// file once per pair with -DIGC_FFN_UNIT=<n>.
+#include "ffn_host.hpp"
+
+namespace igc_ffn_host {
+
+template <bool BF, int MODE>
+int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t stream) {
+  const long long grid = (long long)pl.tiles_m * pl.tiles_n * pl.splits;
+  if (grid == 0) return IGC_OK;
+  if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many tiles (%lld)", grid);
+  constexpr int BN64 = MODE == igc_ffn::M_GLU ? 128 : 64;
+  if (pl.variant == P_ANY_128)
+    hipLaunchKernelGGL((igc_ffn::gemm_any_kernel<BF, MODE, 128, 128>), dim3((unsigned)grid), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((igc_ffn::gemm_any_kernel<BF, MODE, 64, BN64>), dim3((unsigned)grid), dim3(256), 0, stream, a);
+  return launch_status();
+}
+
+#define IGC_FFN_DEFINE(BF, MODE) template int launch_product<BF, MODE>(const igc_ffn::GemmArgs&, const Plan&, hipStream_t);
+#if IGC_FFN_UNIT == 0
+IGC_FFN_DEFINE(false, igc_ffn::M_FWD)
+#elif IGC_FFN_UNIT == 1
+IGC_FFN_DEFINE(true, igc_ffn::M_FWD)
+#elif IGC_FFN_UNIT == 2
+IGC_FFN_DEFINE(false, igc_ffn::M_GLU)
+#elif IGC_FFN_UNIT == 3
+IGC_FFN_DEFINE(true, igc_ffn::M_GLU)
+#elif IGC_FFN_UNIT == 4
+IGC_FFN_DEFINE(false, igc_ffn::M_DX)
+#elif IGC_FFN_UNIT == 5
+IGC_FFN_DEFINE(true, igc_ffn::M_DX)
+#elif IGC_FFN_UNIT == 6
+IGC_FFN_DEFINE(false, igc_ffn::M_DW)
+#elif IGC_FFN_UNIT == 7
+IGC_FFN_DEFINE(true, igc_ffn::M_DW)
+#else
+#error "IGC_FFN_UNIT: 0 .. 7"
+#endif
+
+}  // namespace igc_ffn_host

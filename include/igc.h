@@ -315,6 +315,223 @@ int conv2d_u8i8_zp_workspace_size(int Nb, int H, int W, int C, int Kout, int R, 
                                   int stride_h, int stride_w, int pad_h, int pad_w,
                                   size_t* bytes);
 
+/* ------------------------------------------------------------------------
+ * The feed-forward operators: 16-bit matrix products with bias, activation
+ * and residual in their epilogue, the gated block, both backward passes, and
+ * the clipping of gradients by their global norm.
+ *
+ * Conventions beside those above
+ *  - Every call takes a descriptor (a host pointer, read during the call) and
+ *    a stream.  A descriptor that is zeroed and then filled leaves every
+ *    optional part out.
+ *  - `type` is the type of the operands, of D and of every output that names
+ *    no other: IGC_F16 or IGC_BF16.  Products accumulate in fp32; bias,
+ *    activation and residual are applied to the fp32 sums, rounded once.
+ *    The backward products take D (below) rounded to `type`.
+ *  - Matrices are row-major with any leading dimension >= their row length
+ *    and any alignment their element type allows.  16-byte aligned operands
+ *    with leading dimensions and row lengths that are multiples of 8 take
+ *    the fast path.
+ *  - Workspace.  <entry>_workspace_size() returns the bytes that the call
+ *    described needs on the current device (`workspace` and `ws_bytes` are
+ *    not read).  Forward calls may go without one (NULL: the reduction is
+ *    then never split); backward calls and grad_clip need theirs when it
+ *    is not 0.  It is 256-byte aligned, and its first IGC_WS_HEADER bytes are
+ *    zero before its first use; every call leaves them zero.  Feed-forward
+ *    calls of any kind and size may take turns with one workspace on one
+ *    stream; the GEMM and convolution entry points above need their own.
+ *    Results do not depend on the order in which workgroups finish.
+ *  - Outputs must not overlap inputs or one another (grad_clip may write in
+ *    place).
+ *  - Activations, with f' as its derivative:
+ *      IGC_ACT_NONE       z
+ *      IGC_ACT_RELU       max(z, 0); derivative 0 at 0
+ *      IGC_ACT_GELU       z (1 + erf(z / sqrt 2)) / 2
+ *      IGC_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
+ *      IGC_ACT_SILU       z / (1 + exp(-z))
+ *      IGC_ACT_SIGMOID    1 / (1 + exp(-z))
+ * ---------------------------------------------------------------------- */
+#define IGC_F16 0
+#define IGC_BF16 1
+#define IGC_F32 2
+
+#define IGC_ACT_NONE 0
+#define IGC_ACT_RELU 1
+#define IGC_ACT_GELU 2
+#define IGC_ACT_GELU_TANH 3
+#define IGC_ACT_SILU 4
+#define IGC_ACT_SIGMOID 5
+
+#define IGC_WS_HEADER 8192
+
+/*
+ * linear_forward -- Z = X W^T + b;  Y = act(Z) + R.
+ *
+ *   X     M x K, W  N x K (one row per output column), of `type`
+ *   bias  fp32 vector of length N, or NULL
+ *   R     M x N residual of y_type, or NULL
+ *   Y     M x N of y_type: `type` or IGC_F32
+ *   Z     M x N of `type`: the sums before the activation, kept for the
+ *         backward pass, or NULL
+ * Errors: IGC_EINVAL (NULL descriptor or operand, negative size, leading
+ * dimension below the row length, unknown type or activation, misaligned
+ * pointer, workspace too small), IGC_ENODEV, IGC_EHIP.
+ */
+typedef struct igc_linear_forward {
+  int M, N, K;
+  int type, act, y_type;
+  const void* X;
+  int ldx;
+  const void* W;
+  int ldw;
+  const float* bias;
+  const void* R;
+  int ldr;
+  void* Y;
+  int ldy;
+  void* Z;
+  int ldz;
+  void* workspace;
+  size_t ws_bytes;
+} igc_linear_forward;
+int linear_forward(const igc_linear_forward* d, void* stream);
+int linear_forward_workspace_size(const igc_linear_forward* d, size_t* bytes);
+
+/*
+ * linear_backward -- the gradients of Y = act(X W^T + b) (+ R, whose gradient
+ * is dY itself), with D = dY act'(Z):
+ *   dX = D W (M x K);  dW = D^T X (N x K);  dbias = sum over rows of D (fp32)
+ *
+ *   dY, Z  M x N of `type`; Z may be NULL when act is IGC_ACT_NONE
+ *   X      needed for dW;  W  needed for dX
+ * Any non-empty subset of dX, dW and dbias may be requested (NULL: not
+ * requested).  M == 0 sets dW and dbias to zero.
+ * Errors: as linear_forward, plus IGC_EINVAL when nothing is requested or the
+ * workspace is missing.
+ */
+typedef struct igc_linear_backward {
+  int M, N, K;
+  int type, act;
+  const void* dY;
+  int lddy;
+  const void* Z;
+  int ldz;
+  const void* X;
+  int ldx;
+  const void* W;
+  int ldw;
+  void* dX;
+  int lddx;
+  void* dW;
+  int lddw;
+  float* dbias;
+  void* workspace;
+  size_t ws_bytes;
+} igc_linear_backward;
+int linear_backward(const igc_linear_backward* d, void* stream);
+int linear_backward_workspace_size(const igc_linear_backward* d, size_t* bytes);
+
+/*
+ * glu_forward -- the gated block G = X Wg^T + bias_g;  U = X Wu^T + bias_u;
+ * H = act(G) U, both products in one kernel.
+ *
+ *   X  M x K, Wg and Wu  N x K, of `type`; the biases fp32 or NULL
+ *   H  M x N;  G, U  M x N, kept for the backward pass, or NULL
+ * Errors: as linear_forward.
+ */
+typedef struct igc_glu_forward {
+  int M, N, K;
+  int type, act;
+  const void* X;
+  int ldx;
+  const void* Wg;
+  int ldwg;
+  const void* Wu;
+  int ldwu;
+  const float* bias_g;
+  const float* bias_u;
+  void* H;
+  int ldh;
+  void* G;
+  int ldg;
+  void* U;
+  int ldu;
+  void* workspace;
+  size_t ws_bytes;
+} igc_glu_forward;
+int glu_forward(const igc_glu_forward* d, void* stream);
+int glu_forward_workspace_size(const igc_glu_forward* d, size_t* bytes);
+
+/*
+ * glu_backward -- the gradients of the gated block, with dU = dH act(G) and
+ * dG = dH U act'(G):
+ *   dX = dG Wg + dU Wu;  dWg = dG^T X;  dWu = dU^T X;  dbias_* = row sums
+ *
+ *   dH, G, U  M x N of `type`;  X needed for dWg or dWu;  Wg and Wu for dX
+ * Any non-empty subset of the outputs may be requested.
+ * Errors: as linear_backward.
+ */
+typedef struct igc_glu_backward {
+  int M, N, K;
+  int type, act;
+  const void* dH;
+  int lddh;
+  const void* G;
+  int ldg;
+  const void* U;
+  int ldu;
+  const void* X;
+  int ldx;
+  const void* Wg;
+  int ldwg;
+  const void* Wu;
+  int ldwu;
+  void* dX;
+  int lddx;
+  void* dWg;
+  int lddwg;
+  void* dWu;
+  int lddwu;
+  float* dbias_g;
+  float* dbias_u;
+  void* workspace;
+  size_t ws_bytes;
+} igc_glu_backward;
+int glu_backward(const igc_glu_backward* d, void* stream);
+int glu_backward_workspace_size(const igc_glu_backward* d, size_t* bytes);
+
+/*
+ * grad_clip -- the global norm over `count` tensors, and clipping:
+ *   norm = sqrt(sum over every element of every tensor of g^2)
+ *   out  = g min(1, max_norm / (norm + 1e-6))
+ *
+ *   grads, outs  host arrays of `count` device pointers; outs NULL or
+ *                outs[i] == grads[i]: in place.  Tensors are contiguous;
+ *                they must not overlap but for that.
+ *   sizes, types host arrays: element counts (0 allowed) and IGC_F16,
+ *                IGC_BF16 or IGC_F32; outs[i] has the type of grads[i]
+ *   norm         one fp32 value, written
+ * The squares are summed in 64 bits in a fixed order.  A norm that is not
+ * finite carries into the outputs as the formula has it (NaN, or 0 for an
+ * infinite norm with finite elements).
+ * Errors: IGC_EINVAL (NULL where something is needed, negative count, size or
+ * max_norm, unknown type, misaligned pointer, workspace missing or too
+ * small), IGC_ENODEV, IGC_EHIP.
+ */
+typedef struct igc_grad_clip {
+  int count;
+  const void* const* grads;
+  void* const* outs;
+  const long long* sizes;
+  const int* types;
+  float max_norm;
+  float* norm;
+  void* workspace;
+  size_t ws_bytes;
+} igc_grad_clip;
+int grad_clip(const igc_grad_clip* d, void* stream);
+int grad_clip_workspace_size(const igc_grad_clip* d, size_t* bytes);
+
 /* Diagnostics. */
 const char* igc_status_string(int status); /* static string for a status code              */
 const char* igc_last_error(void);          /* detail of this thread's last failure, or ""  */

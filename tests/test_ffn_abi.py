@@ -1,0 +1,124 @@
+"""The feed-forward entry points without a GPU: bad arguments are rejected with
+the documented status codes before any HIP call, and the binding checks its
+tensors."""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def igc():
+    import implicit_gemm_convolution_amd as m
+
+    if not os.path.exists(m.LIB_PATH):
+        from implicit_gemm_convolution_amd import build
+
+        build.build()
+    m.load()
+    return m
+
+
+def _rejects(igc, f, good, bad):
+    """Each change of `bad` turns the call `good` into one that is refused."""
+    for change in bad:
+        st = f(**{**good, **change}, check=False)
+        assert st == igc.IGC_EINVAL, change
+        assert igc.last_error()
+
+
+P = 4096  # an address that is never read: every call here is refused or empty
+
+
+def test_linear_forward_refuses(igc):
+    good = dict(M=4, N=6, K=8, X=P, ldx=8, W=P, ldw=8, Y=P, ldy=6, type=igc.IGC_F16, act=igc.IGC_ACT_GELU)
+    _rejects(igc, igc.linear_forward, good, [
+        dict(M=-1), dict(N=-1), dict(K=-1), dict(type=igc.IGC_F32), dict(type=7), dict(act=-1), dict(act=6),
+        dict(y_type=igc.IGC_BF16), dict(X=None), dict(W=None), dict(Y=None), dict(ldx=7), dict(ldw=7), dict(ldy=5),
+        dict(X=P + 1), dict(W=P + 1), dict(Y=P + 1), dict(y_type=igc.IGC_F32, Y=P + 2), dict(R=P, ldr=5), dict(R=P + 1, ldr=6),
+        dict(Z=P, ldz=5), dict(Z=P + 1, ldz=6), dict(bias=P + 2)])
+    assert igc.linear_forward(**{**good, "M": 0, "X": None, "Y": None}, check=False) == igc.IGC_OK
+    assert igc.linear_forward(**{**good, "N": 0, "W": None, "Y": None}, check=False) == igc.IGC_OK
+    with pytest.raises(igc.IGCError, match="ldx|leading dimension 7 of X"):
+        igc.linear_forward(**{**good, "ldx": 7})
+
+
+def test_linear_backward_refuses(igc):
+    good = dict(M=4, N=6, K=8, dY=P, lddy=6, Z=P, ldz=6, X=P, ldx=8, W=P, ldw=8, dX=P, lddx=8, dW=P, lddw=8, dbias=P,
+                type=igc.IGC_BF16, act=igc.IGC_ACT_SILU)
+    _rejects(igc, igc.linear_backward, good, [
+        dict(M=-1), dict(type=igc.IGC_F32), dict(act=9), dict(dX=None, dW=None, dbias=None), dict(dY=None), dict(Z=None),
+        dict(X=None), dict(W=None), dict(lddy=5), dict(ldz=5), dict(ldx=7), dict(ldw=7), dict(lddx=7), dict(lddw=7),
+        dict(dY=P + 1), dict(Z=P + 1), dict(dX=P + 1), dict(dW=P + 1), dict(dbias=P + 2)])
+
+
+def test_glu_forward_refuses(igc):
+    good = dict(M=4, N=6, K=8, X=P, ldx=8, Wg=P, ldwg=8, Wu=P, ldwu=8, H=P, ldh=6, type=igc.IGC_BF16)
+    _rejects(igc, igc.glu_forward, good, [
+        dict(K=-2), dict(type=igc.IGC_F32), dict(act=6), dict(X=None), dict(Wg=None), dict(Wu=None), dict(H=None),
+        dict(ldx=7), dict(ldwg=7), dict(ldwu=7), dict(ldh=5), dict(G=P, ldg=5), dict(U=P, ldu=5), dict(Wu=P + 1),
+        dict(bias_g=P + 1), dict(bias_u=P + 2)])
+    assert igc.glu_forward(**{**good, "M": 0, "X": None, "H": None}, check=False) == igc.IGC_OK
+
+
+def test_glu_backward_refuses(igc):
+    good = dict(M=4, N=6, K=8, dH=P, lddh=6, G=P, ldg=6, U=P, ldu=6, X=P, ldx=8, Wg=P, ldwg=8, Wu=P, ldwu=8, dX=P, lddx=8,
+                dWg=P, lddwg=8, dWu=P, lddwu=8, dbias_g=P, dbias_u=P, type=igc.IGC_F16)
+    _rejects(igc, igc.glu_backward, good, [
+        dict(N=-1), dict(type=igc.IGC_F32), dict(act=-1), dict(dX=None, dWg=None, dWu=None, dbias_g=None, dbias_u=None),
+        dict(dH=None), dict(G=None), dict(U=None), dict(X=None), dict(Wg=None), dict(Wu=None), dict(lddh=5), dict(ldg=5),
+        dict(ldu=5), dict(ldx=7), dict(ldwg=7), dict(ldwu=7), dict(lddx=7), dict(lddwg=7), dict(lddwu=7), dict(dbias_u=P + 1)])
+
+
+def test_descriptor_and_query_pointers(igc):
+    L = igc.load()
+    size = ctypes.c_size_t(0)
+    for name in ("linear_forward", "linear_backward", "glu_forward", "glu_backward", "grad_clip"):
+        assert getattr(L, name)(None, None) == igc.IGC_EINVAL
+        assert getattr(L, name + "_workspace_size")(None, ctypes.byref(size)) == igc.IGC_EINVAL
+    d = igc.binding.LinearForward()
+    assert L.linear_forward_workspace_size(ctypes.byref(d), None) == igc.IGC_EINVAL
+    assert L.linear_forward_workspace_size(ctypes.byref(d), ctypes.byref(size)) == igc.IGC_OK and size.value == 0
+
+
+def _clip(igc, sizes=(4, 4), types=None, ptrs=(P, P), outs=None, count=None, max_norm=1.0, norm=P, arrays=True, ws=P, ws_bytes=1 << 20):
+    n = len(sizes)
+    types = (igc.IGC_F32,) * n if types is None else types
+    a = ctypes.addressof
+    g = (ctypes.c_void_p * n)(*ptrs)
+    o = None if outs is None else (ctypes.c_void_p * n)(*outs)
+    s, t = (ctypes.c_longlong * n)(*sizes), (ctypes.c_int * n)(*types)
+    d = igc.binding.GradClip(n if count is None else count, a(g) if arrays else None, a(o) if o else None, a(s), a(t), max_norm,
+                             norm, ws, ws_bytes)
+    return igc.load().grad_clip(ctypes.byref(d), None)
+
+
+def test_grad_clip_refuses(igc):
+    E = igc.IGC_EINVAL
+    assert _clip(igc, count=-1) == E
+    assert _clip(igc, max_norm=-1.0) == E
+    assert _clip(igc, norm=None) == E
+    assert _clip(igc, norm=P + 2) == E
+    assert _clip(igc, arrays=False) == E
+    assert _clip(igc, sizes=(4, -1)) == E
+    assert _clip(igc, types=(igc.IGC_F32, 3)) == E
+    assert _clip(igc, ptrs=(P, None)) == E
+    assert _clip(igc, ptrs=(P, P + 2)) == E              # an fp32 tensor at a 2-byte address
+    assert _clip(igc, outs=(P, P + 1), types=(igc.IGC_F16,) * 2) == E
+
+
+def test_grad_clip_binding_checks_its_tensors(igc):
+    import torch
+
+    norm = torch.zeros(1)
+    a, b = torch.zeros(4, 6), torch.zeros(3, dtype=torch.float16)
+    with pytest.raises(ValueError, match="contiguous"):
+        igc.grad_clip([a.t()], 1.0, norm)
+    with pytest.raises(ValueError, match="outputs"):
+        igc.grad_clip([a, b], 1.0, norm, out=[a])
+    with pytest.raises(ValueError, match="type or size"):
+        igc.grad_clip([a, b], 1.0, norm, out=[a, torch.zeros(3)])
+    with pytest.raises(TypeError, match="float64"):
+        igc.grad_clip([a.double()], 1.0, norm)
