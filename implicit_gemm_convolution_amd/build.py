@@ -84,31 +84,38 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     return LIB_PATH
 
 
-def assembly(out_dir: str, extra_flags=()) -> str:
-    """Write the gfx950 assembly of every kernel to out_dir (one file); returns its path."""
+def _assembly(out_dir, name, source, define, units, extra_flags):
     os.makedirs(out_dir, exist_ok=True)
-    flags = [f for f in HIP_FLAGS]
 
     def one(n):
         d = os.path.join(out_dir, f"unit{n}")
         os.makedirs(d, exist_ok=True)
-        cmd = [HIPCC, *flags, *extra_flags, f"-DIGC_LAUNCH_UNIT={n}", "-c", "--save-temps",
-               LAUNCH_SOURCE, "-o", os.path.join(d, "u.o")]
+        cmd = [HIPCC, *HIP_FLAGS, *extra_flags, f"-D{define}={n}", "-c", "--save-temps", source, "-o", os.path.join(d, "u.o")]
         subprocess.check_call(cmd, cwd=d, stderr=subprocess.DEVNULL)
-        for name in os.listdir(d):
-            if name.endswith("gfx950.s"):
-                return os.path.join(d, name)
+        for f in os.listdir(d):
+            if f.endswith("gfx950.s"):
+                return os.path.join(d, f)
         raise FileNotFoundError("no gfx950 assembly produced")
 
     with ThreadPoolExecutor(_jobs()) as ex:
-        parts = list(ex.map(one, range(LAUNCH_UNITS)))
-    out = os.path.join(out_dir, "igc-kernels-gfx950.s")
+        parts = list(ex.map(one, range(units)))
+    out = os.path.join(out_dir, name)
     with open(out, "w") as f:
         for part in parts:
             with open(part) as g:
                 f.write(g.read())
             f.write("\n")
     return out
+
+
+def assembly(out_dir: str, extra_flags=()) -> str:
+    """Write the gfx950 assembly of every GEMM and convolution kernel to out_dir (one file); returns its path."""
+    return _assembly(out_dir, "igc-kernels-gfx950.s", LAUNCH_SOURCE, "IGC_LAUNCH_UNIT", LAUNCH_UNITS, extra_flags)
+
+
+def ffn_assembly(out_dir: str, extra_flags=()) -> str:
+    """The same for the kernels of the feed-forward products."""
+    return _assembly(out_dir, "ffn-kernels-gfx950.s", FFN_LAUNCH_SOURCE, "IGC_FFN_UNIT", FFN_LAUNCH_UNITS, extra_flags)
 
 
 if __name__ == "__main__":

@@ -96,7 +96,9 @@ int forward(GemmArgs& a, int type, void* ws, size_t ws_bytes, size_t* query, hip
   int dev;
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
-  const Plan pl = make_plan(MODE, a.M, a.N, a.R, cus, query || ws);
+  const bool aligned = dma_operand(a.A, a.lda, a.R) && dma_operand(a.B, a.ldb, a.R) &&
+                       (MODE != igc_ffn::M_GLU || dma_operand(a.B2, a.ldb2, a.R));
+  const Plan pl = make_plan(MODE, a.M, a.N, a.R, aligned, cus, query || ws);
   const size_t need = pl.part_bytes ? IGC_WS_HEADER + pl.part_bytes : 0;
   if (query) {
     *query = need;
@@ -211,8 +213,12 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   const size_t s_bytes = sums ? round256((size_t)blocks * np * width * 4) : 0;
   // D made here is padded with zeros to `width` columns
   const int red = make_d ? np * width : b.N;
-  const Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red, cus, true);
-  const Plan pw = make_plan(igc_ffn::M_DW, red, b.K, b.M, cus, true);
+  // (the two weights of the gated block take turns under one set of lane
+  // offsets, so the direct loads need one leading dimension for both)
+  const bool d_ok = make_d ? (long long)np * width <= (1 << 21) - 8 : dma_operand(b.dY, b.lddy, b.N);
+  const bool x_ok = d_ok && dma_operand(b.W, b.ldw, b.K) && (!b.glu || (dma_operand(b.W2, b.ldw2, b.K) && b.ldw == b.ldw2));
+  const Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red, x_ok, cus, true);
+  const Plan pw = make_plan(igc_ffn::M_DW, red, b.K, b.M, d_ok && dma_operand(b.X, b.ldx, b.K), cus, true);
   const size_t part = std::max(b.dX ? px.part_bytes : 0, b.dW || b.dW2 ? pw.part_bytes : 0);
   const size_t body = d_bytes + s_bytes + part;
   const size_t need = body ? IGC_WS_HEADER + body : 0;

@@ -30,7 +30,9 @@ inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // The kernels of a product, by output tile (the gated block's tiles hold two
 // products: half as many output columns).
-enum Variant { P_ANY_128, P_ANY_64 };
+// P_TILE_*: aligned operands, straight into LDS; P_ANY_*: any operand,
+// through registers.
+enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_ANY_128, P_ANY_64 };
 
 struct Plan {
   int variant = P_ANY_64;
@@ -41,18 +43,34 @@ struct Plan {
 
 inline void plan_tile(int mode, int variant, int& bm, int& bn) {
   switch (variant) {
+    case P_TILE_256: bm = 256; bn = mode == igc_ffn::M_GLU ? 128 : 256; return;
+    case P_TILE_128:
     case P_ANY_128: bm = 128; bn = mode == igc_ffn::M_GLU ? 64 : 128; return;
     default: bm = 64; bn = 64; return;
   }
 }
 
+// Operands of the direct-to-LDS loaders: 16-byte aligned rows, lengths in
+// whole 16-byte chunks (at least one), and a tile's worth of rows within a descriptor (256
+// rows below 2^30 bytes).
+inline bool dma_operand(const void* p, long long ld, long long length) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0 && length > 0 && length % 8 == 0 && ld <= (1 << 21) - 8;
+}
+
 // A pure function of the problem and the device, so that the size queries and
 // the calls agree.  may_split: the call has (or the query assumes) a
 // workspace.
-inline Plan make_plan(int mode, long long M, long long N, long long R, int cus, bool may_split) {
+inline Plan make_plan(int mode, long long M, long long N, long long R, bool aligned, int cus, bool may_split) {
   Plan pl;
-  pl.variant = ceil_div(M, 128) * ceil_div(N, 128) >= cus ? P_ANY_128 : P_ANY_64;
   int bm, bn;
+  plan_tile(mode, P_TILE_256, bm, bn);
+  if (aligned && ceil_div(M, bm) * ceil_div(N, bn) >= cus * 3 / 4) {
+    pl.variant = P_TILE_256;
+  } else {
+    plan_tile(mode, P_TILE_128, bm, bn);
+    const bool large = ceil_div(M, bm) * ceil_div(N, bn) >= cus;
+    pl.variant = aligned ? (large ? P_TILE_128 : P_TILE_64) : (large ? P_ANY_128 : P_ANY_64);
+  }
   plan_tile(mode, pl.variant, bm, bn);
   pl.tiles_m = (int)ceil_div(M, bm);
   pl.tiles_n = (int)ceil_div(N, bn);

@@ -332,6 +332,98 @@ struct RegOperand {
   }
 };
 
+// Loading an operand's K tiles straight into LDS (no registers): 16-byte
+// aligned rows whose length is a multiple of 8.  A wave instruction fills
+// 1 KB of the tile; instruction i of wave w fills the KB 4 i + w.  Each lane
+// fetches the chunk that belongs in its slot, so the swizzle costs nothing.
+// Out of range reads as zeros: rows (columns) past the operand and reduction
+// elements past R.
+//  ROW: each load is one of the lane's fixed offsets plus a scalar offset
+//  along the row; the lanes past R are moved out of range when the last K
+//  tile comes up.
+//  COL: the descriptor moves down the rows, with the rows that are left as
+//  its size.
+template <int W, bool COL, bool TWO>
+struct DmaOperand {
+  typedef LdsTile<W, COL> Tile;
+  static constexpr int NQ = Tile::BYTES / 4096;  // instructions per wave and tile
+  static constexpr uint32_t OUT = 0x80000000u;   // past every descriptor (they end below 2^30)
+  uint32_t voff[NQ];
+  Rsrc rs, rs2;
+  uint32_t wofs;
+  uint32_t soff;  // ROW: this tile's scalar offset
+  int R, kend, nk;
+  // COL
+  const uint8_t *p, *p2;
+  long long ldb;  // bytes
+  int o0, extent, r_split, r_rows;
+
+  __device__ __forceinline__ void init(const uint8_t* ptr, long long l, const uint8_t* ptr2, long long l2, int o, int ext,
+                                       int red, int split, int rows, int k_end) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    wofs = (uint32_t)wave_id() * 1024u;
+    R = red;
+    kend = k_end;
+    nk = max(1, (R + 63) / 64);
+    if constexpr (!COL) {
+      // (the two products of the gated block: half of the rows from each)
+      constexpr int WR = TWO ? W / 2 : W;
+      const int nrows = min(ext - o, WR);
+      rs = make_rsrc(ptr + (long long)o * l * 2, (uint32_t)((long long)(nrows - 1) * l * 2 + R * 2));
+      if constexpr (TWO) rs2 = make_rsrc(ptr2 + (long long)o * l2 * 2, (uint32_t)((long long)(nrows - 1) * l2 * 2 + R * 2));
+      const uint32_t chunk = (uint32_t)((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7));
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const bool second = TWO && i >= NQ / 2;
+        const int row = (i * 4 + wave) * 8 + (lane >> 3) - (second ? WR : 0);
+        voff[i] = (uint32_t)(row * (int)(second ? l2 : l) * 2) + chunk * 16;
+      }
+    } else {
+      p = ptr;
+      p2 = ptr2;
+      ldb = l * 2;
+      o0 = o;
+      extent = ext;
+      r_split = split;
+      r_rows = rows;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int kr = (i * 4 + wave) * (512 / W) + lane / (W / 8), s = lane % (W / 8);
+        const int c = (((s >> 1) ^ Tile::gran(kr)) << 1) | (s & 1);
+        voff[i] = o + c * 8 < ext ? (uint32_t)(kr * (int)ldb) + (uint32_t)c * 16 : OUT;
+      }
+    }
+  }
+  // before the loads of tile kt
+  __device__ __forceinline__ void prepare(int kt) {
+    if constexpr (!COL) {
+      soff = kt < kend ? (uint32_t)kt * 128u : 0x40000000u;
+      if (kt == nk - 1 && (R & 63)) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
+        const bool in = kt * 64 + chunk * 8 < R;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) voff[i] = in ? voff[i] : OUT;
+      }
+    } else {
+      int r = kt * 64;
+      const bool second = TWO && r >= r_split;
+      if (second) r -= r_split;
+      const int rows = kt < kend ? min(max(r_rows - r, 0), 64) : 0;
+      const uint8_t* const q = (second ? p2 : p) + (long long)r * ldb + (long long)o0 * 2;
+      rs = make_rsrc(q, rows > 0 ? (uint32_t)((rows - 1) * (int)ldb + min(W, extent - o0) * 2) : 0u);
+    }
+  }
+  template <int NOPS = igc::NOPS_LOOP>
+  __device__ __forceinline__ void part(uint8_t* st, int i) const {
+    uint8_t* const dst = st + i * 4096 + wofs;
+    if constexpr (COL)
+      igc::dma16<NOPS>(rs, dst, voff[i]);
+    else
+      igc::dma16s<NOPS>(TWO && i >= NQ / 2 ? rs2 : rs, dst, voff[i], soff);
+  }
+};
+
 // Logical tile of workgroup b.  The dispatcher hands workgroups to the 8 XCDs
 // round-robin; with more than one round of compute units each XCD gets a
 // contiguous run of logical tiles, laid out in groups of 8 tile rows, so the
@@ -447,7 +539,10 @@ __device__ __forceinline__ bool join_splits(const GemmArgs& p, int tile, int spl
   __syncthreads();
   volatile int* const flag = reinterpret_cast<volatile int*>(lds);
   if (threadIdx.x == 0) {
-    const int n = __hip_atomic_fetch_add(p.cnt + tile, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    wait_vmcnt_lgkm0<0>();  // (the compiler lets the count pass the write-back without it)
+    const int n = __hip_atomic_fetch_add(p.cnt + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     const bool last = n == p.splits - 1;
     // every other split has counted itself in: the counter is free again
     if (last) __hip_atomic_store(p.cnt + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -469,15 +564,19 @@ __device__ __forceinline__ bool join_splits(const GemmArgs& p, int tile, int spl
 
 // The accumulators of a wave (FM x FN blocks, each transposed by the matrix
 // instruction: lane l holds row l % 16, columns 4 (l / 16) .. +3) leave
-// through the wave's own piece of LDS, one block row at a time, so that every
-// lane gets 8 consecutive columns of a row and a store instruction covers
-// whole 128-byte lines.  No barrier: a wave's LDS accesses are in order.
-template <bool BF, int MODE, int FM, int FN>
+// through the wave's own REGION bytes of LDS, as many block rows at a time as
+// fit, so that every lane gets 8 consecutive columns of a row and a store
+// instruction covers whole 128-byte lines.  No barrier: a wave's LDS accesses
+// are in order.  The arithmetic sits in a real loop over the staged rows
+// (unrolled over the accumulators, its six activations overflow the
+// instruction cache).
+template <bool BF, int MODE, int FM, int FN, int REGION>
 __device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[FM][FN], uint8_t* lds, int row0, int col0) {
   constexpr bool GLU = MODE == M_GLU;
   constexpr int TN = FN * 16, OUT = GLU ? TN / 2 : TN;  // staged columns, output columns
   constexpr int LPR = OUT / 8, RPP = 64 / LPR;          // lanes per row, rows per pass
-  static_assert(RPP <= 16, "a pass covers at most one block row");
+  constexpr int FIT = REGION / (16 * TN * 4), GR = FIT >= FM ? FM : FM / 2;  // block rows staged at a time
+  static_assert(RPP <= 16 && FIT >= GR && FM % GR == 0, "staging");
   constexpr int XM = TN / 4 < 16 ? TN / 4 - 1 : 15;
   const int lane = threadIdx.x & 63;
   const int wr = lane & 15, rr = lane / LPR, rc = lane % LPR;
@@ -488,20 +587,23 @@ __device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[
     __builtin_memcpy(f, &a, 16);
     __builtin_memcpy(f + 4, &b, 16);
   };
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  static_for<FM / GR>([&](auto g) {
+    constexpr int G0 = decltype(g)::value * GR;
     asm volatile("" ::: "memory");
+    static_for<GR>([&](auto i) {
+      constexpr int I = decltype(i)::value;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) lds_write16(lds, quad(wr, j * 4 + (lane >> 4)), __builtin_bit_cast(uint4, acc[i][j]));
+      for (int j = 0; j < FN; ++j)
+        lds_write16(lds, quad(I * 16 + wr, j * 4 + (lane >> 4)), __builtin_bit_cast(uint4, acc[G0 + I][j]));
+    });
     asm volatile("" ::: "memory");
-#pragma unroll
-    for (int r = 0; r < 16; r += RPP) {
+    for (int r = 0; r < GR * 16; r += RPP) {
       float f[8], u[8];
       read8(r + rr, rc * 8, f);
       if constexpr (GLU) read8(r + rr, OUT + rc * 8, u);
-      out(row0 + i * 16 + r + rr, f, u);
+      out(row0 + G0 * 16 + r + rr, f, u);
     }
-  }
+  });
 }
 
 // The simple product: K tiles go through registers into two LDS stages.
@@ -567,7 +669,149 @@ __global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
     __syncthreads();
   }
   if (p.splits > 1 && !join_splits<FM * FN>(p, tile, split, &acc[0][0], smem)) return;
-  write_out<BF, MODE, FM, FN>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+  write_out<BF, MODE, FM, FN, sizeof(smem) / 4>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+}
+
+// The product on aligned operands: both go from memory straight into LDS, A
+// in three stages and B in two, and the K loop is software-pipelined over
+// them.  A K tile of 64 is two k-steps of FM chunks; a chunk is the FN matrix
+// instructions of one block row, with at most one load and its share of the
+// next k-step's fragment reads between them, fenced so that program order is
+// issue order.  During the first k-step of tile kt the loads of A tile kt+2
+// go out; then the wave waits until tile kt+1 has landed (only those A loads
+// may still fly) and a barrier frees tile kt's stages; during the second
+// k-step the loads of B tile kt+2 go into tile kt's stage and tile kt+1's
+// first fragments are read.
+// Four waves, 2 x 2.  256 x 256: a wave holds 128 x 128 sums (all 256
+// accumulation registers), the least LDS traffic per matrix instruction.
+template <bool BF, int MODE, int BM, int BN>
+__global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) gemm_tile_kernel(const GemmArgs p) {
+  constexpr bool GLU = MODE == M_GLU, ACOL = MODE == M_DW, BCOL = MODE == M_DX || MODE == M_DW;
+  constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
+  typedef LdsTile<BM, ACOL> TA;
+  typedef LdsTile<BN, BCOL> TB;
+  typedef DmaOperand<BM, ACOL, false> LoadA;
+  typedef DmaOperand<BN, BCOL, GLU || MODE == M_DX> LoadB;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[3 * TA::BYTES + 2 * TB::BYTES];
+  auto stA = [&](auto u) -> uint8_t* { return smem + (decltype(u)::value % 3) * TA::BYTES; };
+  auto stB = [&](auto u) -> uint8_t* { return smem + 3 * TA::BYTES + (decltype(u)::value % 2) * TB::BYTES; };
+  const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
+  int tile = blockIdx.x, split = 0;
+  if (p.splits > 1) {
+    tile = blockIdx.x / p.splits;
+    split = blockIdx.x - tile * p.splits;
+  }
+  int tm, tn;
+  tile_of(p, tile, tm, tn);
+  constexpr int ON = GLU ? BN / 2 : BN;
+  const int m0 = tm * BM, n0 = tn * ON;
+  const int nk = max(1, (p.R + 63) / 64);
+  int k0 = 0, k1 = nk;
+  if (p.splits > 1) {
+    k0 = (int)((long long)nk * split / p.splits);
+    k1 = (int)((long long)nk * (split + 1) / p.splits);
+  }
+  LoadA la;
+  LoadB lb;
+  la.init(p.A, p.lda, nullptr, 0, m0, p.M, p.R, p.R, p.R, k1);
+  lb.init(p.B, p.ldb, p.B2, p.ldb2, n0, p.N, p.R, p.r_split, p.b_rows, k1);
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto blk_b = [&](int j) {
+    if constexpr (GLU) return j < FN / 2 ? wn * (TN / 2) + j * 16 : BN / 2 + wn * (TN / 2) + (j - FN / 2) * 16;
+    return wn * TN + j * 16;
+  };
+  uint4 fa[2][FM], fb[2][FN];
+
+  // one block row c of a k-step
+  auto chunk = [&](int c, const uint4(&a)[FM], const uint4(&b)[FN], const uint8_t* An, const uint8_t* Bn, int ksn,
+                   uint4(&an)[FM], uint4(&bn)[FN], auto issue) {
+    __builtin_amdgcn_sched_barrier(0);
+    mfma16<BF>(acc[c][0], b[0], a[c]);
+    __builtin_amdgcn_sched_barrier(0);
+    issue();
+    __builtin_amdgcn_sched_barrier(0);
+    // the next k-step's fragments: B first (its first chunk needs all of them)
+    int nrd = 0;
+#pragma unroll
+    for (int r = 0; r < FN + FM; ++r)
+      if (r * FM / (FN + FM) == c) {
+        if (r < FN) {
+          bn[r] = TB::frag(Bn, blk_b(r), ksn);
+          nrd += BCOL ? 2 : 1;
+        } else {
+          an[r - FN] = TA::frag(An, wm * TM + (r - FN) * 16, ksn);
+          nrd += ACOL ? 2 : 1;
+        }
+      }
+#pragma unroll
+    for (int j = 1; j < FN; ++j) mfma16<BF>(acc[c][j], b[j], a[c]);
+#pragma unroll
+    for (int q = 1; q < FN; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+      if (q <= nrd) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+    }
+  };
+
+  static_for<2>([&](auto d) {
+    constexpr int D = decltype(d)::value;
+    la.prepare(k0 + D);
+    lb.prepare(k0 + D);
+#pragma unroll
+    for (int i = 0; i < LoadA::NQ; ++i) la.template part<igc::NOPS_SAFE>(stA(d), i);
+#pragma unroll
+    for (int i = 0; i < LoadB::NQ; ++i) lb.template part<igc::NOPS_SAFE>(stB(d), i);
+  });
+  wait_vmcnt_lgkm0<LoadA::NQ + LoadB::NQ>();
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < FM; ++i) fa[0][i] = TA::frag(smem, wm * TM + i * 16, 0);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) fb[0][j] = TB::frag(smem + 3 * TA::BYTES, blk_b(j), 0);
+
+  auto ktile = [&](int kt, auto U) {
+    constexpr int u = decltype(U)::value;
+    const uint8_t *As = stA(U), *Bs = stB(U);
+    uint8_t* const An = stA(std::integral_constant<int, u + 2>());
+    uint8_t* const Bn = stB(std::integral_constant<int, u + 2>());
+    const uint8_t* const A1 = stA(std::integral_constant<int, u + 1>());
+    const uint8_t* const B1 = stB(std::integral_constant<int, u + 1>());
+    la.prepare(kt + 2);
+    lb.prepare(kt + 2);
+#pragma unroll
+    for (int c = 0; c < FM; ++c)
+      chunk(c, fa[0], fb[0], As, Bs, 1, fa[1], fb[1], [&]() {
+#pragma unroll
+        for (int i = 0; i < LoadA::NQ; ++i)
+          if (i * FM / LoadA::NQ == c) la.part(An, i);
+      });
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt_lgkm0<LoadA::NQ>();
+    lds_barrier();
+#pragma unroll
+    for (int c = 0; c < FM; ++c)
+      chunk(c, fa[1], fb[1], A1, B1, 0, fa[0], fb[0], [&]() {
+#pragma unroll
+        for (int i = 0; i < LoadB::NQ; ++i)
+          if (i * FM / LoadB::NQ == c) lb.part(Bn, i);
+      });
+  };
+  for (int kt = k0; kt < k1; kt += 6) {
+    ktile(kt, std::integral_constant<int, 0>());
+    static_for<5>([&](auto J) {
+      constexpr int j = decltype(J)::value + 1;
+      if (kt + j < k1) ktile(kt + j, std::integral_constant<int, j>());
+    });
+  }
+  // loads past the last tile may still be writing LDS
+  wait_vmcnt_lgkm0<0>();
+  lds_barrier();
+  if (p.splits > 1 && !join_splits<FM * FN>(p, tile, split, &acc[0][0], smem)) return;
+  write_out<BF, MODE, FM, FN, sizeof(smem) / 4>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
 }
 
 // ---------------------------------------------------------------------------

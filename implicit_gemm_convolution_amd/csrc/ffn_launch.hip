@@ -11,7 +11,13 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
   if (grid == 0) return IGC_OK;
   if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many tiles (%lld)", grid);
   constexpr int BN64 = MODE == igc_ffn::M_GLU ? 128 : 64;
-  if (pl.variant == P_ANY_128)
+  if (pl.variant == P_TILE_256)
+    hipLaunchKernelGGL((igc_ffn::gemm_tile_kernel<BF, MODE, 256, 256>), dim3((unsigned)grid), dim3(256), 0, stream, a);
+  else if (pl.variant == P_TILE_128)
+    hipLaunchKernelGGL((igc_ffn::gemm_tile_kernel<BF, MODE, 128, 128>), dim3((unsigned)grid), dim3(256), 0, stream, a);
+  else if (pl.variant == P_TILE_64)
+    hipLaunchKernelGGL((igc_ffn::gemm_tile_kernel<BF, MODE, 64, BN64>), dim3((unsigned)grid), dim3(256), 0, stream, a);
+  else if (pl.variant == P_ANY_128)
     hipLaunchKernelGGL((igc_ffn::gemm_any_kernel<BF, MODE, 128, 128>), dim3((unsigned)grid), dim3(256), 0, stream, a);
   else
     hipLaunchKernelGGL((igc_ffn::gemm_any_kernel<BF, MODE, 64, BN64>), dim3((unsigned)grid), dim3(256), 0, stream, a);

@@ -117,12 +117,13 @@ def _store(kind, value):
 
 # (M, N, K, extra row length, shift of the start in elements)
 SIZES = [
-    (1, 1, 1, 0, 0), (1, 16, 8, 0, 0), (3, 5, 7, 2, 1), (1, 300, 520, 0, 0), (2, 1001, 333, 0, 1), (5, 64, 0, 3, 0),
+    (1, 1, 1, 0, 0), (1, 16, 8, 0, 0), (3, 5, 7, 2, 1), (1, 300, 520, 0, 0), (2, 1001, 333, 0, 1), (5, 64, 0, 3, 0), (70, 64, 0, 8, 0),
     (16, 96, 2048, 0, 0), (17, 33, 65, 0, 0), (24, 520, 1000, 8, 8), (33, 130, 264, 0, 0), (63, 200, 72, 8, 0), (64, 64, 64, 0, 0),
     (65, 257, 129, 1, 3), (128, 256, 512, 0, 0), (131, 1000, 520, 0, 0), (200, 264, 328, 8, 16), (256, 512, 256, 0, 0), (300, 777, 1001, 0, 0),
     (513, 640, 192, 0, 0),
 ]
-LARGE = [(2100, 2056, 264, 0, 0), (1025, 4104, 200, 8, 0), (4100, 1030, 136, 0, 2)]
+LARGE = [(2100, 2056, 264, 0, 0), (1025, 4104, 200, 8, 0), (4100, 1030, 136, 0, 2), (3400, 4104, 136, 0, 0), (3400, 136, 4104, 8, 8),
+         (136, 3400, 4104, 0, 0), (520, 4104, 4096, 0, 0)]
 
 
 def _linear_forward(torch, igc, ws, size, kind, act, bias, residual, save, y, seed=0, use_ws=True, stream=None):
