@@ -13,7 +13,9 @@ fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 import sys
 
@@ -178,11 +180,31 @@ def _addr(x) -> int | None:
     raise TypeError(f"expected a device address or a tensor, got {type(x)}")
 
 
+_raw_stream = None  # torch's current stream as a raw hipStream_t, found at the first call
+
+
+def _current_stream() -> int:
+    """torch's current stream.  Looked up by every call, so through the raw
+    getter where torch has it (0.2 us; a Stream object costs 3)."""
+    global _raw_stream
+    torch = sys.modules["torch"]
+    if _raw_stream is None:
+        get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if get is not None and device is not None:
+            torch.cuda.init()
+            _raw_stream = lambda: get(device())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return int(_raw_stream())
+
+
 def _stream(s) -> int | None:
     if s is None:
+        if _raw_stream is not None:
+            return _current_stream()
         torch = sys.modules.get("torch")
         if torch is not None and torch.cuda.is_available():
-            return int(torch.cuda.current_stream().cuda_stream)
+            return _current_stream()
         return None
     if isinstance(s, int):
         return s
@@ -401,36 +423,40 @@ def glu_backward_workspace_size(M, N, K, dH, lddh, G, ldg, U, ldu, *, X=None, ld
                                    lddwu, dbias_g, dbias_u, type, act, None, 0))
 
 
-_DTYPES = {"torch.float16": IGC_F16, "torch.bfloat16": IGC_BF16, "torch.float32": IGC_F32}
+_DTYPES = {}  # torch's dtypes, filled at the first call
 
 
-def _tensor_type(t) -> int:
+def _tensor_types(dtypes):
+    if not _DTYPES:
+        import torch
+
+        _DTYPES.update({torch.float16: IGC_F16, torch.bfloat16: IGC_BF16, torch.float32: IGC_F32})
     try:
-        return _DTYPES[str(t.dtype)]
-    except KeyError:
-        raise TypeError(f"grad_clip takes float16, bfloat16 and float32 tensors, not {t.dtype}") from None
+        return array.array("i", [_DTYPES[t] for t in dtypes])
+    except KeyError as e:
+        raise TypeError(f"grad_clip takes float16, bfloat16 and float32 tensors, not {e.args[0]}") from None
+
+
+_dtype = operator.attrgetter("dtype")
 
 
 def _grad_clip(grads, max_norm, norm, out, workspace, ws_bytes):
+    # (a model has hundreds of gradients: one C-level pass per property)
+    from torch import Tensor
+
+    _contiguous, _numel, _data_ptr = Tensor.is_contiguous, Tensor.numel, Tensor.data_ptr
     n = len(grads)
     if out is not None and len(out) != n:
         raise ValueError(f"{n} gradients but {len(out)} outputs")
-    for pair in (grads, out or ()):
-        for t in pair:
-            if not t.is_contiguous():
-                raise ValueError("grad_clip takes contiguous tensors")
-    types = [_tensor_type(t) for t in grads]
-    sizes = [t.numel() for t in grads]
-    if out is not None:
-        for g, o in zip(grads, out):
-            if o.dtype != g.dtype or o.numel() != g.numel():
-                raise ValueError("an output differs from its gradient in type or size")
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
-    outs = None if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
-    sizes, types = (ctypes.c_longlong * n)(*sizes), (ctypes.c_int * n)(*types)
-    a = ctypes.addressof
-    d = GradClip(n, a(ptrs), None if outs is None else a(outs), a(sizes), a(types), float(max_norm), _addr(norm),
-                 _addr(workspace), _ws_bytes(workspace, ws_bytes))
+    if not all(map(_contiguous, grads)) or (out is not None and not all(map(_contiguous, out))):
+        raise ValueError("grad_clip takes contiguous tensors")
+    dtypes, sizes = list(map(_dtype, grads)), array.array("q", map(_numel, grads))
+    if out is not None and (dtypes != list(map(_dtype, out)) or sizes != array.array("q", map(_numel, out))):
+        raise ValueError("an output differs from its gradient in type or size")
+    types, ptrs = _tensor_types(dtypes), array.array("Q", map(_data_ptr, grads))
+    outs = None if out is None else array.array("Q", map(_data_ptr, out))
+    d = GradClip(n, ptrs.buffer_info()[0], outs and outs.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0],
+                 float(max_norm), _addr(norm), _addr(workspace), _ws_bytes(workspace, ws_bytes))
     return d, (ptrs, outs, sizes, types)  # (the arrays live until the call returns)
 
 

@@ -31,8 +31,10 @@ inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // The kernels of a product, by output tile (the gated block's tiles hold two
 // products: half as many output columns).
 // P_TILE_*: aligned operands, straight into LDS; P_ANY_*: any operand,
-// through registers.
-enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_ANY_128, P_ANY_64 };
+// through registers; P_SKINNY_*: few rows, any operand, 16 or 32 weight rows
+// per workgroup.
+enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_ANY_128, P_ANY_64, P_SKINNY_16, P_SKINNY_32 };
+constexpr int kSkinnyRows = 64;
 
 struct Plan {
   int variant = P_ANY_64;
@@ -62,6 +64,13 @@ inline bool dma_operand(const void* p, long long ld, long long length) {
 // workspace.
 inline Plan make_plan(int mode, long long M, long long N, long long R, bool aligned, int cus, bool may_split) {
   Plan pl;
+  if ((mode == igc_ffn::M_FWD || mode == igc_ffn::M_GLU) && M <= kSkinnyRows) {
+    // 32 weight rows share the loads of X; 16 where there would be too few workgroups
+    pl.variant = mode == igc_ffn::M_GLU || N >= 32LL * cus ? P_SKINNY_32 : P_SKINNY_16;
+    pl.tiles_m = 1;
+    pl.tiles_n = (int)ceil_div(N, pl.variant == P_SKINNY_32 && mode == igc_ffn::M_FWD ? 32 : 16);
+    return pl;
+  }
   int bm, bn;
   plan_tile(mode, P_TILE_256, bm, bn);
   if (aligned && ceil_div(M, bm) * ceil_div(N, bn) >= cus * 3 / 4) {

@@ -111,6 +111,60 @@ __device__ __forceinline__ void store8(uint8_t* p, const uint4& v, int valid) {
   }
 }
 
+// V (4 or 8) 16-bit or fp32 elements as fp32 values, from and to any address;
+// those past `valid` are left alone.
+template <bool BF, int V>
+__device__ __forceinline__ void load_n(const uint8_t* p, int valid, float (&f)[V]) {
+  if constexpr (V == 8) {
+    unpack8<BF>(load8(p, valid), f);
+  } else {
+    uint32_t w[2] = {0, 0};
+    if (valid >= 4) {
+      __builtin_memcpy(w, p, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < valid) w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+    }
+    unpack2<BF>(w[0], f[0], f[1]);
+    unpack2<BF>(w[1], f[2], f[3]);
+  }
+}
+template <bool BF, int V>
+__device__ __forceinline__ void store_n(uint8_t* p, int valid, const float (&f)[V]) {
+  if constexpr (V == 8) {
+    store8(p, pack8<BF>(f), valid);
+  } else {
+    const uint32_t w[2] = {pack2<BF>(f[0], f[1]), pack2<BF>(f[2], f[3])};
+    if (valid >= 4) {
+      __builtin_memcpy(p, w, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < valid) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_f32(const float* p, int valid, float (&f)[V]) {
+  if (valid >= V) {
+    __builtin_memcpy(f, p, 4 * V);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = e < valid ? p[e] : 0.0f;
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_f32(float* p, int valid, const float (&f)[V]) {
+  if (valid >= V) {
+    __builtin_memcpy(p, f, 4 * V);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < valid) p[e] = f[e];
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Activations, in fp32.
 // ---------------------------------------------------------------------------
@@ -440,84 +494,68 @@ __device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& 
   tm = first + in - tn * rows;
 }
 
-// One wave's 16 x TNW block row leaves for the outputs: `f` holds 8
-// consecutive sums of one row (and `u` those of the second product).
-template <bool BF, int MODE>
+// V consecutive sums of one row (`f`, and `u` of the second product) leave for
+// the outputs.
+template <bool BF, int MODE, int V>
 struct Epilogue {
   const GemmArgs& p;
   int col;       // this lane's first column
   int left;      // columns from there to the end
-  float b1[8], b2[8];
+  float b1[V], b2[V];
   bool has_bias;
   __device__ __forceinline__ Epilogue(const GemmArgs& args, int c) : p(args), col(c), left(args.N - c) {
     has_bias = (MODE == M_FWD && p.bias) || (MODE == M_GLU && (p.bias || p.bias2));
     if constexpr (MODE == M_FWD || MODE == M_GLU) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < V; ++e) {
         b1[e] = p.bias && e < left ? p.bias[col + e] : 0.0f;
         b2[e] = MODE == M_GLU && p.bias2 && e < left ? p.bias2[col + e] : 0.0f;
       }
     }
   }
-  __device__ __forceinline__ void put16(uint8_t* base, long long ld, int row, const float (&f)[8]) const {
-    store8(base + ((long long)row * ld + col) * 2, pack8<BF>(f), left);
+  __device__ __forceinline__ void put(uint8_t* base, long long ld, int row, const float (&f)[V]) const {
+    store_n<BF, V>(base + ((long long)row * ld + col) * 2, left, f);
   }
-  __device__ __forceinline__ void operator()(int row, float (&f)[8], float (&u)[8]) const {
+  __device__ __forceinline__ void operator()(int row, float (&f)[V], float (&u)[V]) const {
     if (row >= p.M || left <= 0) return;
     if constexpr (MODE == M_DX) {
-      put16(p.Y, p.ldy, row, f);
+      put(p.Y, p.ldy, row, f);
     } else if constexpr (MODE == M_DW) {
       const bool second = row >= p.m_split;
       const int r = second ? row - p.m_split : row;
       uint8_t* const y = second ? p.Y2 : p.Y;  // (either may be left out)
-      if (y && r < p.m_rows) put16(y, second ? p.ldy2 : p.ldy, r, f);
+      if (y && r < p.m_rows) put(y, second ? p.ldy2 : p.ldy, r, f);
     } else {
-      float y[8], unused[8];
+      float y[V], unused[V];
       if (has_bias) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] += b1[e];
+        for (int e = 0; e < V; ++e) f[e] += b1[e];
         if constexpr (MODE == M_GLU) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] += b2[e];
+          for (int e = 0; e < V; ++e) u[e] += b2[e];
         }
       }
-      if (p.Z) put16(p.Z, p.ldz, row, f);
+      if (p.Z) put(p.Z, p.ldz, row, f);
       act_n<false>(p.act, f, y, unused);
       if constexpr (MODE == M_GLU) {
-        if (p.U) put16(p.U, p.ldu, row, u);
+        if (p.U) put(p.U, p.ldu, row, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= u[e];
-        put16(p.Y, p.ldy, row, y);
-      } else if (!p.y_f32) {
-        if (p.res) {
-          float r[8];
-          unpack8<BF>(load8(p.res + ((long long)row * p.ldr + col) * 2, left), r);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] += r[e];
-        }
-        put16(p.Y, p.ldy, row, y);
+        for (int e = 0; e < V; ++e) y[e] *= u[e];
+        put(p.Y, p.ldy, row, y);
       } else {
         if (p.res) {
-          const float* const q = reinterpret_cast<const float*>(p.res) + (long long)row * p.ldr + col;
-          if (left >= 8) {
-            float r[8];
-            __builtin_memcpy(r, q, 32);
+          float r[V];
+          if (p.y_f32)
+            load_f32(reinterpret_cast<const float*>(p.res) + (long long)row * p.ldr + col, left, r);
+          else
+            load_n<BF, V>(p.res + ((long long)row * p.ldr + col) * 2, left, r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] += r[e];
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < left) y[e] += q[e];
-          }
+          for (int e = 0; e < V; ++e) y[e] += r[e];
         }
-        float* const q = reinterpret_cast<float*>(p.Y) + (long long)row * p.ldy + col;
-        if (left >= 8) {
-          __builtin_memcpy(q, y, 32);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < left) q[e] = y[e];
-        }
+        if (p.y_f32)
+          store_f32(reinterpret_cast<float*>(p.Y) + (long long)row * p.ldy + col, left, y);
+        else
+          put(p.Y, p.ldy, row, y);
       }
     }
   }
@@ -580,7 +618,7 @@ __device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[
   constexpr int XM = TN / 4 < 16 ? TN / 4 - 1 : 15;
   const int lane = threadIdx.x & 63;
   const int wr = lane & 15, rr = lane / LPR, rc = lane % LPR;
-  const Epilogue<BF, MODE> out(p, col0 + rc * 8);
+  const Epilogue<BF, MODE, 8> out(p, col0 + rc * 8);
   auto quad = [&](int r, int q) { return r * (TN * 4) + ((q ^ (r & XM)) << 4); };  // 4 columns of a staged row
   auto read8 = [&](int r, int c, float (&f)[8]) {
     const uint4 a = lds_read16(lds, quad(r, c >> 2)), b = lds_read16(lds, quad(r, (c >> 2) + 1));
@@ -670,6 +708,104 @@ __global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
   }
   if (p.splits > 1 && !join_splits<FM * FN>(p, tile, split, &acc[0][0], smem)) return;
   write_out<BF, MODE, FM, FN, sizeof(smem) / 4>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+}
+
+// The forward products of few rows (M <= 16 MB): bound by streaming the
+// weights once.  A workgroup takes NB blocks of 16 weight rows (the gated
+// block: half of them from each weight) and its waves split the reduction;
+// every lane loads its matrix-instruction operands straight into registers,
+// UN steps of 32 elements at once, so that a compute unit keeps over 100 KB
+// of weights in flight, which is what it takes to reach the memory's rate.
+// The waves' sums are added through LDS in wave order.  Any alignment.
+template <bool BF, int MODE, int MB, int NB, int NW>
+__global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) {
+  constexpr bool GLU = MODE == M_GLU;
+  constexpr int PB = GLU ? NB / 2 : NB;  // column blocks
+  constexpr int UN = MB == 1 ? 8 : 4;
+  __shared__ f32x4 red[NW][NB * MB][64];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * (PB * 16);
+  // rows past the end repeat the last one; their sums are not stored
+  const uint8_t *w[NB], *x[MB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const bool second = GLU && j >= PB;
+    const long long n = min(n0 + (second ? j - PB : j) * 16 + r, p.N - 1);
+    w[j] = (second ? p.B2 + n * p.ldb2 * 2 : p.B + n * p.ldb * 2) + g * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i) x[i] = p.A + (long long)min(i * 16 + r, p.M - 1) * p.lda * 2 + g * 16;
+  f32x4 acc[NB][MB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int steps = p.R / 32 + (p.R % 32 >= 8);  // (what is left of a chunk of 8 follows below)
+  const int s1 = (int)((long long)steps * (wave + 1) / NW);
+  int s = (int)((long long)steps * wave / NW);
+  uint4 fw[UN][NB], fx[UN][MB];
+  auto multiply = [&](int u) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int i = 0; i < MB; ++i) mfma16<BF>(acc[j][i], fw[u][j], fx[u][i]);
+  };
+  auto chunk = [](const uint8_t* q) {
+    uint4 v;
+    __builtin_memcpy(&v, q, 16);
+    return v;
+  };
+  for (; s + UN <= s1 && (s + UN) * 32 <= p.R; s += UN) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) fw[u][j] = chunk(w[j] + (long long)(s + u) * 64);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) fx[u][i] = chunk(x[i] + (long long)(s + u) * 64);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) multiply(u);
+  }
+  if (s < s1) {  // the last batch: the steps that are left, the lanes whose chunk is whole
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const bool in = s + u < s1 && (s + u) * 32 + g * 8 + 8 <= p.R;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) fw[u][j] = in ? chunk(w[j] + (long long)(s + u) * 64) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) fx[u][i] = in ? chunk(x[i] + (long long)(s + u) * 64) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) multiply(u);
+  }
+  if ((p.R & 7) && wave == NW - 1) {  // the elements past the last whole chunk
+    const int k = p.R & ~7, left = g == 0 ? p.R & 7 : 0;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) fw[0][j] = load8(w[j] - g * 16 + (long long)k * 2, left);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) fx[0][i] = load8(x[i] - g * 16 + (long long)k * 2, left);
+    multiply(0);
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) red[wave][j * MB + i][lane] = acc[j][i];
+  __syncthreads();
+  // lane l of a block holds row l % 16, columns 4 (l / 16) .. +3
+  for (int t = threadIdx.x; t < PB * MB * 64; t += 64 * NW) {
+    const int b = t >> 6, l = t & 63;
+    f32x4 f4 = red[0][b][l], u4 = GLU ? red[0][PB * MB + b][l] : f4;
+#pragma unroll
+    for (int q = 1; q < NW; ++q) {
+      f4 += red[q][b][l];
+      if constexpr (GLU) u4 += red[q][PB * MB + b][l];
+    }
+    float f[4] = {f4[0], f4[1], f4[2], f4[3]}, u[4] = {u4[0], u4[1], u4[2], u4[3]};
+    const Epilogue<BF, MODE, 4> out(p, n0 + (b / MB) * 16 + 4 * (l >> 4));
+    out((b % MB) * 16 + (l & 15), f, u);
+  }
 }
 
 // The product on aligned operands: both go from memory straight into LDS, A

@@ -5,12 +5,31 @@
 
 namespace igc_ffn_host {
 
+template <bool BF, int MODE, int MB>
+void launch_skinny(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t stream) {
+  if (pl.variant == P_SKINNY_32)
+    hipLaunchKernelGGL((igc_ffn::gemm_skinny_kernel<BF, MODE, MB, 2, 8>), dim3((unsigned)pl.tiles_n), dim3(512), 0, stream, a);
+  else if constexpr (MODE == igc_ffn::M_FWD)
+    hipLaunchKernelGGL((igc_ffn::gemm_skinny_kernel<BF, MODE, MB, 1, 16>), dim3((unsigned)pl.tiles_n), dim3(1024), 0, stream, a);
+}
+
 template <bool BF, int MODE>
 int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t stream) {
   const long long grid = (long long)pl.tiles_m * pl.tiles_n * pl.splits;
   if (grid == 0) return IGC_OK;
   if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many tiles (%lld)", grid);
   constexpr int BN64 = MODE == igc_ffn::M_GLU ? 128 : 64;
+  if constexpr (MODE == igc_ffn::M_FWD || MODE == igc_ffn::M_GLU) {
+    if (pl.variant == P_SKINNY_16 || pl.variant == P_SKINNY_32) {
+      if (a.M <= 16)
+        launch_skinny<BF, MODE, 1>(a, pl, stream);
+      else if (a.M <= 32)
+        launch_skinny<BF, MODE, 2>(a, pl, stream);
+      else
+        launch_skinny<BF, MODE, 4>(a, pl, stream);
+      return launch_status();
+    }
+  }
   if (pl.variant == P_TILE_256)
     hipLaunchKernelGGL((igc_ffn::gemm_tile_kernel<BF, MODE, 256, 256>), dim3((unsigned)grid), dim3(256), 0, stream, a);
   else if (pl.variant == P_TILE_128)
