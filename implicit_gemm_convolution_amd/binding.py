@@ -39,7 +39,6 @@ IGC_ACT_GELU = 2
 IGC_ACT_GELU_TANH = 3
 IGC_ACT_SILU = 4
 IGC_ACT_SIGMOID = 5
-IGC_WS_HEADER = 8192  # workspace bytes that are zero between calls
 
 # Every symbol include/igc.h declares.
 EXPORTED = ("gemm_f16f32", "gemm_u8i8_zp", "conv2d_implicit_gemm", "conv2d_u8i8_zp",

@@ -71,18 +71,13 @@ GemmArgs product(long long M, long long N, long long R, const void* A, long long
   return a;
 }
 
-// `ws`: the whole workspace (its header holds the arrival counters), part_at:
-// where the partial tiles start in it.
+// part: where the partial tiles of a split reduction go.
 template <int MODE>
-int run_product(GemmArgs& a, const Plan& pl, int type, uint8_t* ws, size_t part_at, int cus, hipStream_t stream) {
+int run_product(GemmArgs& a, const Plan& pl, int type, uint8_t* part, hipStream_t stream) {
   a.tiles_m = pl.tiles_m;
   a.tiles_n = pl.tiles_n;
   a.splits = pl.splits;
-  a.regroup = (long long)pl.tiles_m * pl.tiles_n > cus;
-  if (pl.splits > 1) {
-    a.cnt = reinterpret_cast<int*>(ws);
-    a.part = reinterpret_cast<float*>(ws + part_at);
-  }
+  a.part = reinterpret_cast<float*>(part);
   return type == IGC_BF16 ? launch_product<true, MODE>(a, pl, stream) : launch_product<false, MODE>(a, pl, stream);
 }
 
@@ -99,13 +94,13 @@ int forward(GemmArgs& a, int type, void* ws, size_t ws_bytes, size_t* query, hip
   const bool aligned = dma_operand(a.A, a.lda, a.R) && dma_operand(a.B, a.ldb, a.R) &&
                        (MODE != igc_ffn::M_GLU || dma_operand(a.B2, a.ldb2, a.R));
   const Plan pl = make_plan(MODE, a.M, a.N, a.R, aligned, cus, query || ws);
-  const size_t need = pl.part_bytes ? IGC_WS_HEADER + pl.part_bytes : 0;
+  const size_t need = pl.part_bytes;
   if (query) {
     *query = need;
     return IGC_OK;
   }
   if (int s = check_ws(ws, ws_bytes, need, false)) return s;
-  return run_product<MODE>(a, pl, type, static_cast<uint8_t*>(ws), IGC_WS_HEADER, cus, stream);
+  return run_product<MODE>(a, pl, type, static_cast<uint8_t*>(ws), stream);
 }
 
 int linear_forward_impl(const igc_linear_forward* d, size_t* query, hipStream_t stream) {
@@ -205,7 +200,7 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
 
-  // workspace: header, D, column sums, partial tiles (the two products take
+  // workspace: D, column sums, partial tiles (the two products take
   // turns with them)
   const int rows = act_rows(b.M, std::max(width, 1), cus);
   const int blocks = (int)ceil_div(b.M, rows);
@@ -220,17 +215,16 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   const Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red, x_ok, cus, true);
   const Plan pw = make_plan(igc_ffn::M_DW, red, b.K, b.M, d_ok && dma_operand(b.X, b.ldx, b.K), cus, true);
   const size_t part = std::max(b.dX ? px.part_bytes : 0, b.dW || b.dW2 ? pw.part_bytes : 0);
-  const size_t body = d_bytes + s_bytes + part;
-  const size_t need = body ? IGC_WS_HEADER + body : 0;
+  const size_t need = d_bytes + s_bytes + part;
   if (query) {
     *query = need;
     return IGC_OK;
   }
   if (int s = check_ws(b.ws, b.ws_bytes, need, true)) return s;
   uint8_t* const ws = static_cast<uint8_t*>(b.ws);
-  uint8_t* const D = make_d ? ws + IGC_WS_HEADER : nullptr;
-  float* const part_sums = sums ? reinterpret_cast<float*>(ws + IGC_WS_HEADER + d_bytes) : nullptr;
-  const size_t part_at = IGC_WS_HEADER + d_bytes + s_bytes;
+  uint8_t* const D = make_d ? ws : nullptr;
+  float* const part_sums = sums ? reinterpret_cast<float*>(ws + d_bytes) : nullptr;
+  uint8_t* const parts = ws + d_bytes + s_bytes;
 
   if ((make_d || sums) && b.M > 0 && b.N > 0) {
     igc_ffn::ActBackArgs e;
@@ -273,7 +267,7 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
       a.ldb2 = b.ldw2;
       a.r_split = width;
     }
-    if (int s = run_product<igc_ffn::M_DX>(a, px, b.type, ws, part_at, cus, stream)) return s;
+    if (int s = run_product<igc_ffn::M_DX>(a, px, b.type, parts, stream)) return s;
   }
   if ((b.dW || b.dW2) && b.N > 0 && b.K > 0) {
     GemmArgs a = product(red, b.K, b.M, A, lda, b.X, b.ldx, b.dW, b.lddw);
@@ -283,7 +277,7 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
       a.ldy2 = b.lddw2;
       a.m_split = width;
     }
-    if (int s = run_product<igc_ffn::M_DW>(a, pw, b.type, ws, part_at, cus, stream)) return s;
+    if (int s = run_product<igc_ffn::M_DW>(a, pw, b.type, parts, stream)) return s;
   }
   return IGC_OK;
 }
@@ -373,7 +367,7 @@ int grad_clip_impl(const igc_grad_clip* d, size_t* query, hipStream_t stream) {
     t.first[t.count] = (int)chunks;
     return (int)std::min<long long>(chunks, CLIP_GRID);
   };
-  const size_t need = IGC_WS_HEADER + (size_t)launches * CLIP_GRID * sizeof(double);
+  const size_t need = (size_t)launches * CLIP_GRID * sizeof(double);
   if (query) {
     *query = need;
     return IGC_OK;
@@ -383,7 +377,7 @@ int grad_clip_impl(const igc_grad_clip* d, size_t* query, hipStream_t stream) {
   if (int s = check_ws(d->workspace, d->ws_bytes, need, true)) return s;
   ClipTable t;
   std::memset(&t, 0, sizeof(t));
-  t.part = reinterpret_cast<double*>(static_cast<uint8_t*>(d->workspace) + IGC_WS_HEADER);
+  t.part = static_cast<double*>(d->workspace);
   t.max_norm = d->max_norm;
   int slots = 0;
   for (int l = 0; l < launches; ++l)

@@ -34,7 +34,6 @@ inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // through registers; P_SKINNY_*: few rows, any operand, 16 or 32 weight rows
 // per workgroup.
 enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_ANY_128, P_ANY_64, P_SKINNY_16, P_SKINNY_32 };
-constexpr int kSkinnyRows = 64;
 
 struct Plan {
   int variant = P_ANY_64;
@@ -61,33 +60,50 @@ inline bool dma_operand(const void* p, long long ld, long long length) {
 
 // A pure function of the problem and the device, so that the size queries and
 // the calls agree.  may_split: the call has (or the query assumes) a
-// workspace.
+// workspace.  Times below: bf16 on MI355X, N = K = 4096 unless said.
 inline Plan make_plan(int mode, long long M, long long N, long long R, bool aligned, int cus, bool may_split) {
   Plan pl;
-  if ((mode == igc_ffn::M_FWD || mode == igc_ffn::M_GLU) && M <= kSkinnyRows) {
+  int bm, bn;
+  // Few rows: streaming the weights into registers beats 64-row tiles up to
+  // 16 rows (12 rows 10.0 us against 11.9) and, on short reductions, up to 32
+  // (24x2048x1024 5.1 against 6.3; 32 rows 14.0 against 12.3).  Rows of any
+  // alignment have no better kernel up to 64.
+  if ((mode == igc_ffn::M_FWD || mode == igc_ffn::M_GLU) && (M <= 16 || (M <= 32 && R <= 1024) || (M <= 64 && !aligned))) {
     // 32 weight rows share the loads of X; 16 where there would be too few workgroups
     pl.variant = mode == igc_ffn::M_GLU || N >= 32LL * cus ? P_SKINNY_32 : P_SKINNY_16;
     pl.tiles_m = 1;
     pl.tiles_n = (int)ceil_div(N, pl.variant == P_SKINNY_32 && mode == igc_ffn::M_FWD ? 32 : 16);
     return pl;
   }
-  int bm, bn;
-  plan_tile(mode, P_TILE_256, bm, bn);
-  if (aligned && ceil_div(M, bm) * ceil_div(N, bn) >= cus * 3 / 4) {
+  // The largest tile that fills the card: 256 x 256 from three quarters of
+  // the compute units (M = 4096: 102 us against 118 on 128 x 128 tiles; at
+  // half of them, M = 2048, 93 against 66), 128 x 128 likewise (M = 1024
+  // 37 us against 53 on 64 x 64; M = 512 29.4 against 28.4).
+  auto tiles = [&](int variant) {
+    plan_tile(mode, variant, bm, bn);
+    return ceil_div(M, bm) * ceil_div(N, bn);
+  };
+  if (aligned && 4 * tiles(P_TILE_256) >= 3 * cus)
     pl.variant = P_TILE_256;
-  } else {
-    plan_tile(mode, P_TILE_128, bm, bn);
-    const bool large = ceil_div(M, bm) * ceil_div(N, bn) >= cus;
-    pl.variant = aligned ? (large ? P_TILE_128 : P_TILE_64) : (large ? P_ANY_128 : P_ANY_64);
-  }
+  else if (4 * tiles(P_TILE_128) >= 3 * cus)
+    pl.variant = aligned ? P_TILE_128 : P_ANY_128;
+  else
+    pl.variant = aligned ? P_TILE_64 : P_ANY_64;
   plan_tile(mode, pl.variant, bm, bn);
   pl.tiles_m = (int)ceil_div(M, bm);
   pl.tiles_n = (int)ceil_div(N, bn);
-  const long long tiles = (long long)pl.tiles_m * pl.tiles_n;
+  const long long count = (long long)pl.tiles_m * pl.tiles_n;
   const long long nk = std::max(1LL, ceil_div(R, 64));
-  if (may_split && tiles > 0 && tiles < cus) {
-    pl.splits = (int)std::max(1LL, std::min(nk / 4, (long long)cus / tiles));
-    if (pl.splits > 1) pl.part_bytes = (size_t)tiles * pl.splits * bm * bn * (mode == igc_ffn::M_GLU ? 8 : 4);
+  // Splitting the reduction costs a second launch and the partial tiles'
+  // traffic, about 20 K tiles' time: 64 tiles of 64 K tiles (M = 64) in four
+  // splits 12.5 us against 15.4, 128 tiles (M = 128) in two 13.8 against
+  // 16.0, but 64 tiles of 32 K tiles in two 11.8 against 9.7.
+  if (may_split && count > 0) {
+    const long long s = std::min(nk / 8, (long long)cus / count);
+    if (s > 1 && nk - nk / s > 24) {
+      pl.splits = (int)s;
+      pl.part_bytes = (size_t)count * pl.splits * bm * bn * (mode == igc_ffn::M_GLU ? 8 : 4);
+    }
   }
   return pl;
 }

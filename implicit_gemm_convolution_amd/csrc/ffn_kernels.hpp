@@ -278,10 +278,9 @@ struct GemmArgs {
   long long ldy2;
   int m_split, m_rows;
   // work split
-  int tiles_m, tiles_n, regroup;
+  int tiles_m, tiles_n;
   int splits;  // workgroups that share a tile's reduction
   float* part;  // their partial tiles
-  int* cnt;     // one arrival counter per tile, zero between launches
 };
 
 template <bool BF>
@@ -478,16 +477,14 @@ struct DmaOperand {
   }
 };
 
-// Logical tile of workgroup b.  The dispatcher hands workgroups to the 8 XCDs
-// round-robin; with more than one round of compute units each XCD gets a
-// contiguous run of logical tiles, laid out in groups of 8 tile rows, so the
-// workgroups that share an L2 share operand panels.
+// Tile of workgroup t of p.tiles_m x p.tiles_n.  The dispatcher hands
+// workgroups to the 8 XCDs round-robin: each XCD gets a contiguous run of
+// tiles, laid out in groups of 8 tile rows, so the workgroups that share an
+// L2 share operand panels (256 x 4096 x 4096 on 64 x 64 tiles 22.6 -> 16.9 us,
+// 4096^3 on 256 x 256 109 -> 102 us).
 __device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& tn) {
-  int t = b;
-  if (p.regroup) {
-    const int n = p.tiles_m * p.tiles_n, x = b & 7;
-    t = x * (n >> 3) + min(x, n & 7) + (b >> 3);
-  }
+  const int n = p.tiles_m * p.tiles_n, x = b & 7;
+  const int t = x * (n >> 3) + min(x, n & 7) + (b >> 3);
   const int per = 8 * p.tiles_n, group = t / per, first = group * 8;
   const int in = t - group * per, rows = min(8, p.tiles_m - first);
   tn = in / rows;
@@ -561,43 +558,14 @@ struct Epilogue {
   }
 };
 
-// Joining the workgroups that share a tile's reduction.  Each writes its
-// accumulators in lane order; the one that arrives last adds all of them in
-// split order (its own included: the sum does not depend on who is last) and
-// carries on to the epilogue.  Returns whether this workgroup does.
-// The stores have reached this XCD's L2 before the barrier (vmcnt 0); the
-// arrival is a device-scope release (writes the L2 back) and acquire
-// (invalidates the caches before the partials are read).
+// A reduction split between workgroups: each leaves its accumulators in lane
+// order, and a second launch adds them in split order and runs the epilogue.
+// (Joined in the same launch by the last workgroup to arrive, every arrival
+// writes its XCD's L2 back and every join drops it: 256 x 4096 x 4096 on
+// 64 x 64 tiles in two splits took 51 us so, against 23 unsplit.)
 template <int NQ>
-__device__ __forceinline__ bool join_splits(const GemmArgs& p, int tile, int split, f32x4* acc, uint8_t* lds) {
-  f32x4* const slot = reinterpret_cast<f32x4*>(p.part) + (long long)tile * p.splits * NQ * 256 + threadIdx.x;
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) slot[((long long)split * NQ + q) * 256] = acc[q];
-  wait_vmcnt_lgkm0<0>();
-  __syncthreads();
-  volatile int* const flag = reinterpret_cast<volatile int*>(lds);
-  if (threadIdx.x == 0) {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    wait_vmcnt_lgkm0<0>();  // (the compiler lets the count pass the write-back without it)
-    const int n = __hip_atomic_fetch_add(p.cnt + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    const bool last = n == p.splits - 1;
-    // every other split has counted itself in: the counter is free again
-    if (last) __hip_atomic_store(p.cnt + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *flag = last;
-  }
-  __syncthreads();
-  const bool last = *flag != 0;
-  __syncthreads();
-  if (!last) return false;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) acc[q] = slot[(long long)q * 256];
-  for (int s = 1; s < p.splits; ++s) {
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) acc[q] += slot[((long long)s * NQ + q) * 256];
-  }
-  return true;
+__device__ __forceinline__ f32x4* partial(const GemmArgs& p, int tile, int split, int thread) {
+  return reinterpret_cast<f32x4*>(p.part) + ((long long)tile * p.splits + split) * NQ * 256 + thread;
 }
 
 // The accumulators of a wave (FM x FN blocks, each transposed by the matrix
@@ -706,7 +674,14 @@ __global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
     }
     __syncthreads();
   }
-  if (p.splits > 1 && !join_splits<FM * FN>(p, tile, split, &acc[0][0], smem)) return;
+  if (p.splits > 1) {
+    f32x4* const out = partial<FM * FN>(p, tile, split, threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) out[(i * FN + j) * 256] = acc[i][j];
+    return;
+  }
   write_out<BF, MODE, FM, FN, sizeof(smem) / 4>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
 }
 
@@ -808,29 +783,38 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
   }
 }
 
-// The product on aligned operands: both go from memory straight into LDS, A
-// in three stages and B in two, and the K loop is software-pipelined over
-// them.  A K tile of 64 is two k-steps of FM chunks; a chunk is the FN matrix
+// The product on aligned operands: both go from memory straight into LDS,
+// DEPTH K tiles ahead, and the K loop is software-pipelined over the stages.
+// A K tile of 64 is two k-steps of FM chunks; a chunk is the FN matrix
 // instructions of one block row, with at most one load and its share of the
 // next k-step's fragment reads between them, fenced so that program order is
-// issue order.  During the first k-step of tile kt the loads of A tile kt+2
-// go out; then the wave waits until tile kt+1 has landed (only those A loads
-// may still fly) and a barrier frees tile kt's stages; during the second
-// k-step the loads of B tile kt+2 go into tile kt's stage and tile kt+1's
-// first fragments are read.
-// Four waves, 2 x 2.  256 x 256: a wave holds 128 x 128 sums (all 256
-// accumulation registers), the least LDS traffic per matrix instruction.
-template <bool BF, int MODE, int BM, int BN>
-__global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) gemm_tile_kernel(const GemmArgs p) {
+// issue order.  During the first k-step of tile kt the loads of A tile
+// kt + DEPTH go out; then the wave waits until tile kt + 1 has landed (only
+// later tiles' loads may still fly) and a barrier frees tile kt's stages;
+// during the second k-step the loads of B tile kt + DEPTH go out and tile
+// kt + 1's first fragments are read.
+// Four waves, 2 x 2.  256 x 256 at depth 2 (A in three stages, B in two, all
+// 160 KB of LDS): a wave holds 128 x 128 sums (all 256 accumulation
+// registers), the least LDS traffic per matrix instruction; bound by the
+// matrix cores at the clock that the power limit leaves them (2200 cycles per
+// K tile, of which they take 2048).  128 x 128 at depth 2, two workgroups per
+// compute unit.  64 x 64 at depth 4 (80 KB: two workgroups), where a compute
+// unit's loads in flight are the bound: 64 x 4096 x 4096 unsplit 26.7 us at
+// depth 2, 15.4 at 4, 15.5 at 6.
+constexpr int tile_lds(int bm, int bn, int depth) { return 128 * ((depth + 1) * bm + (depth == 2 ? 2 : depth + 1) * bn); }
+constexpr int tile_waves(int bm, int bn, int depth) { return 160 * 1024 / tile_lds(bm, bn, depth) > 1 ? 2 : 1; }  // per SIMD
+template <bool BF, int MODE, int BM, int BN, int DEPTH>
+__global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH)) gemm_tile_kernel(const GemmArgs p) {
   constexpr bool GLU = MODE == M_GLU, ACOL = MODE == M_DW, BCOL = MODE == M_DX || MODE == M_DW;
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   typedef LdsTile<BM, ACOL> TA;
   typedef LdsTile<BN, BCOL> TB;
   typedef DmaOperand<BM, ACOL, false> LoadA;
   typedef DmaOperand<BN, BCOL, GLU || MODE == M_DX> LoadB;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[3 * TA::BYTES + 2 * TB::BYTES];
-  auto stA = [&](auto u) -> uint8_t* { return smem + (decltype(u)::value % 3) * TA::BYTES; };
-  auto stB = [&](auto u) -> uint8_t* { return smem + 3 * TA::BYTES + (decltype(u)::value % 2) * TB::BYTES; };
+  constexpr int RA = DEPTH + 1, RB = DEPTH == 2 ? 2 : DEPTH + 1, UNR = RA == RB ? RA : RA * RB;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[RA * TA::BYTES + RB * TB::BYTES];
+  auto stA = [&](auto u) -> uint8_t* { return smem + (decltype(u)::value % RA) * TA::BYTES; };
+  auto stB = [&](auto u) -> uint8_t* { return smem + RA * TA::BYTES + (decltype(u)::value % RB) * TB::BYTES; };
   const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
   int tile = blockIdx.x, split = 0;
   if (p.splits > 1) {
@@ -893,7 +877,7 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) gemm_tile_ke
     }
   };
 
-  static_for<2>([&](auto d) {
+  static_for<DEPTH>([&](auto d) {
     constexpr int D = decltype(d)::value;
     la.prepare(k0 + D);
     lb.prepare(k0 + D);
@@ -902,22 +886,22 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) gemm_tile_ke
 #pragma unroll
     for (int i = 0; i < LoadB::NQ; ++i) lb.template part<igc::NOPS_SAFE>(stB(d), i);
   });
-  wait_vmcnt_lgkm0<LoadA::NQ + LoadB::NQ>();
+  wait_vmcnt_lgkm0<(DEPTH - 1) * (LoadA::NQ + LoadB::NQ)>();
   lds_barrier();
 #pragma unroll
   for (int i = 0; i < FM; ++i) fa[0][i] = TA::frag(smem, wm * TM + i * 16, 0);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) fb[0][j] = TB::frag(smem + 3 * TA::BYTES, blk_b(j), 0);
+  for (int j = 0; j < FN; ++j) fb[0][j] = TB::frag(smem + RA * TA::BYTES, blk_b(j), 0);
 
   auto ktile = [&](int kt, auto U) {
     constexpr int u = decltype(U)::value;
     const uint8_t *As = stA(U), *Bs = stB(U);
-    uint8_t* const An = stA(std::integral_constant<int, u + 2>());
-    uint8_t* const Bn = stB(std::integral_constant<int, u + 2>());
+    uint8_t* const An = stA(std::integral_constant<int, u + DEPTH>());
+    uint8_t* const Bn = stB(std::integral_constant<int, u + DEPTH>());
     const uint8_t* const A1 = stA(std::integral_constant<int, u + 1>());
     const uint8_t* const B1 = stB(std::integral_constant<int, u + 1>());
-    la.prepare(kt + 2);
-    lb.prepare(kt + 2);
+    la.prepare(kt + DEPTH);
+    lb.prepare(kt + DEPTH);
 #pragma unroll
     for (int c = 0; c < FM; ++c)
       chunk(c, fa[0], fb[0], As, Bs, 1, fa[1], fb[1], [&]() {
@@ -926,7 +910,7 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) gemm_tile_ke
           if (i * FM / LoadA::NQ == c) la.part(An, i);
       });
     __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt_lgkm0<LoadA::NQ>();
+    wait_vmcnt_lgkm0<(DEPTH - 2) * (LoadA::NQ + LoadB::NQ) + LoadA::NQ>();
     lds_barrier();
 #pragma unroll
     for (int c = 0; c < FM; ++c)
@@ -936,9 +920,9 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) gemm_tile_ke
           if (i * FM / LoadB::NQ == c) lb.part(Bn, i);
       });
   };
-  for (int kt = k0; kt < k1; kt += 6) {
+  for (int kt = k0; kt < k1; kt += UNR) {
     ktile(kt, std::integral_constant<int, 0>());
-    static_for<5>([&](auto J) {
+    static_for<UNR - 1>([&](auto J) {
       constexpr int j = decltype(J)::value + 1;
       if (kt + j < k1) ktile(kt + j, std::integral_constant<int, j>());
     });
@@ -946,8 +930,38 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) gemm_tile_ke
   // loads past the last tile may still be writing LDS
   wait_vmcnt_lgkm0<0>();
   lds_barrier();
-  if (p.splits > 1 && !join_splits<FM * FN>(p, tile, split, &acc[0][0], smem)) return;
+  if (p.splits > 1) {
+    f32x4* const out = partial<FM * FN>(p, tile, split, threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) out[(i * FN + j) * 256] = acc[i][j];
+    return;
+  }
   write_out<BF, MODE, FM, FN, sizeof(smem) / 4>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+}
+
+// The second launch of a split reduction: one wave for each wave of a tile.
+template <bool BF, int MODE, int BM, int BN>
+__global__ void __launch_bounds__(64) gemm_join_kernel(const GemmArgs p) {
+  constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
+  constexpr int ON = MODE == M_GLU ? BN / 2 : BN;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[(FM > 4 ? FM / 2 : FM) * 16 * TN * 4];
+  const int tile = blockIdx.x >> 2, wave = blockIdx.x & 3, wm = wave >> 1, wn = wave & 1;
+  int tm, tn;
+  tile_of(p, tile, tm, tn);
+  f32x4 acc[FM][FN];
+  for (int s = 0; s < p.splits; ++s) {
+    const f32x4* const in = partial<FM * FN>(p, tile, s, wave * 64 + threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const f32x4 v = in[(i * FN + j) * 256];
+        acc[i][j] = s == 0 ? v : acc[i][j] + v;
+      }
+  }
+  write_out<BF, MODE, FM, FN, sizeof(smem)>(p, acc, smem, tm * BM + wm * TM, tn * ON + wn * (ON / 2));
 }
 
 // ---------------------------------------------------------------------------

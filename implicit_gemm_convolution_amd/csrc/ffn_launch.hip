@@ -30,16 +30,22 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
       return launch_status();
     }
   }
-  if (pl.variant == P_TILE_256)
-    hipLaunchKernelGGL((igc_ffn::gemm_tile_kernel<BF, MODE, 256, 256>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-  else if (pl.variant == P_TILE_128)
-    hipLaunchKernelGGL((igc_ffn::gemm_tile_kernel<BF, MODE, 128, 128>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-  else if (pl.variant == P_TILE_64)
-    hipLaunchKernelGGL((igc_ffn::gemm_tile_kernel<BF, MODE, 64, BN64>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-  else if (pl.variant == P_ANY_128)
-    hipLaunchKernelGGL((igc_ffn::gemm_any_kernel<BF, MODE, 128, 128>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL((igc_ffn::gemm_any_kernel<BF, MODE, 64, BN64>), dim3((unsigned)grid), dim3(256), 0, stream, a);
+  const dim3 g((unsigned)grid), t(256);
+  const dim3 gj((unsigned)(pl.tiles_m * pl.tiles_n * 4)), tj(64);
+#define IGC_FFN_TILE(kernel, BM, BN, ...)                                                                       \
+  do {                                                                                                          \
+    hipLaunchKernelGGL((igc_ffn::kernel<BF, MODE, BM, BN, ##__VA_ARGS__>), g, t, 0, stream, a);                  \
+    if (pl.splits > 1) hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, MODE, BM, BN>), gj, tj, 0, stream, a);  \
+  } while (0)
+  switch (pl.variant) {
+    case P_TILE_256: IGC_FFN_TILE(gemm_tile_kernel, 256, 256, 2); break;
+    case P_TILE_128: IGC_FFN_TILE(gemm_tile_kernel, 128, 128, 2); break;
+    case P_TILE_64: IGC_FFN_TILE(gemm_tile_kernel, 64, BN64, 4); break;
+    case P_ANY_128: IGC_FFN_TILE(gemm_any_kernel, 128, 128); break;
+    case P_ANY_64: IGC_FFN_TILE(gemm_any_kernel, 64, BN64); break;
+    default: return fail(IGC_EUNSUPPORTED, "internal: no kernel for variant %d", pl.variant);
+  }
+#undef IGC_FFN_TILE
   return launch_status();
 }
 

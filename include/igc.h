@@ -336,10 +336,9 @@ int conv2d_u8i8_zp_workspace_size(int Nb, int H, int W, int C, int Kout, int R, 
  *    described needs on the current device (`workspace` and `ws_bytes` are
  *    not read).  Forward calls may go without one (NULL: the reduction is
  *    then never split); backward calls and grad_clip need theirs when it
- *    is not 0.  It is 256-byte aligned, and its first IGC_WS_HEADER bytes are
- *    zero before its first use; every call leaves them zero.  Feed-forward
- *    calls of any kind and size may take turns with one workspace on one
- *    stream; the GEMM and convolution entry points above need their own.
+ *    is not 0.  It is 256-byte aligned; what it holds before and after a call
+ *    does not matter, so calls of any kind and size may take turns with one
+ *    workspace on one stream (the entry points above want theirs zeroed).
  *    Results do not depend on the order in which workgroups finish.
  *  - Outputs must not overlap inputs or one another (grad_clip may write in
  *    place).
@@ -361,8 +360,6 @@ int conv2d_u8i8_zp_workspace_size(int Nb, int H, int W, int C, int Kout, int R, 
 #define IGC_ACT_GELU_TANH 3
 #define IGC_ACT_SILU 4
 #define IGC_ACT_SIGMOID 5
-
-#define IGC_WS_HEADER 8192
 
 /*
  * linear_forward -- Z = X W^T + b;  Y = act(Z) + R.

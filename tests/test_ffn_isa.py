@@ -1,7 +1,6 @@
 """Checks on the gfx950 assembly of the feed-forward products (CPU only): the
 matrix instruction of their type, no scratch or memory wait of the compiler's
-in a K loop, the wait states of the inline-assembly loads, and the memory
-order of a split reduction's arrival count."""
+in a K loop, the wait states of the inline-assembly loads."""
 from __future__ import annotations
 
 import re
@@ -40,7 +39,7 @@ def _lines(body):
 
 def test_matrix_instruction_of_the_type(asm):
     for name, (body, _) in asm.items():
-        m = re.search(r"gemm_\w+_kernel<(true|false)", name)
+        m = re.search(r"gemm_(?:any|tile|skinny)_kernel<(true|false)", name)
         if not m:
             continue
         kinds = set(re.findall(r"v_mfma_\w+", body))
@@ -82,7 +81,7 @@ def test_wide_stores_keep_their_data(asm):
     isa.test_no_vector_write_of_a_wide_store_s_data_right_after_it({k: (cut(b), m) for k, (b, m) in asm.items()})
 
 
-def test_split_count_is_released_and_acquired_at_device_scope(asm):
-    found = {k: v for k, v in asm.items() if "global_atomic_add" in v[0]}
-    assert len(found) >= 16
-    isa.test_stream_k_count_is_released_and_acquired_at_device_scope(found)
+def test_no_atomics(asm):
+    """Results do not depend on the order in which workgroups finish."""
+    for name, (body, _) in asm.items():
+        assert "atomic" not in body, name

@@ -44,8 +44,8 @@ def igc(torch):
 
 @pytest.fixture(scope="module")
 def ws(torch):
-    """One workspace that every call of this file shares, zeroed once."""
-    return torch.zeros(256 << 20, dtype=torch.uint8, device="cuda")
+    """One workspace that every call of this file shares; NaN to begin with."""
+    return torch.full((256 << 20,), 255, dtype=torch.uint8, device="cuda")
 
 
 def _dt(torch, kind):
@@ -156,7 +156,6 @@ def _linear_forward(torch, igc, ws, size, kind, act, bias, residual, save, y, se
     if save:
         _check("Z", Z.t, z, ez + _store(kind, z.abs() + ez))
         assert Z.others_untouched()
-    assert int(ws[:igc.IGC_WS_HEADER].count_nonzero()) == 0
     return Y.t.clone()
 
 
@@ -217,7 +216,6 @@ def _linear_backward(torch, igc, ws, size, kind, act, want, seed=0):
         assert bool(db[N].isnan())
     for m, w in ((dX, "x"), (dW, "w")):
         assert m.others_untouched() if w in want else bool(m.flat.isnan().all())
-    assert int(ws[:igc.IGC_WS_HEADER].count_nonzero()) == 0
 
 
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
@@ -262,7 +260,6 @@ def _glu(torch, igc, ws, size, kind, act, bias, save, seed=0):
         _check("G", G.t, g, eg + _store(kind, g.abs() + eg))
         _check("U", Uo.t, u, eu + _store(kind, u.abs() + eu))
         assert G.others_untouched() and Uo.others_untouched()
-    assert int(ws[:igc.IGC_WS_HEADER].count_nonzero()) == 0
 
 
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
@@ -311,7 +308,6 @@ def _glu_backward(torch, igc, ws, size, kind, act, want, seed=0):
         assert bool(out[N].isnan())
     for m, c in ((dX, "x"), (dWg, "g"), (dWu, "u")):
         assert m.others_untouched() if c in want else bool(m.flat.isnan().all())
-    assert int(ws[:igc.IGC_WS_HEADER].count_nonzero()) == 0
 
 
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
@@ -400,7 +396,7 @@ def test_split_reduction_is_deterministic(torch, igc, ws):
 
 def test_another_stream_and_its_own_workspace(torch, igc, ws):
     s = torch.cuda.Stream()
-    own = torch.zeros(ws.numel(), dtype=torch.uint8, device="cuda")
+    own = torch.full_like(ws, 255)
     torch.cuda.synchronize()
     _linear_forward(torch, igc, own, (130, 200, 4096, 0, 0), "f16", "gelu", True, True, True, "f16", stream=s)
 
@@ -416,7 +412,7 @@ def test_graph_replays(torch, igc):
     H, G, Uo, Y, dH, dX = new(M, N), new(M, N), new(M, N), new(M, K), new(M, N), new(M, K)
     d1, d2, d3, db, norm = new(N, K), new(N, K), new(K, N), torch.empty(K, device="cuda"), torch.empty(1, device="cuda")
     clipped = [torch.empty_like(t) for t in (d1, d2, d3)]
-    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
 
     def step():
         igc.glu_forward(M, N, K, X, K, W1, K, W2, K, H, N, G=G, ldg=N, U=Uo, ldu=N, workspace=ws)
