@@ -23,7 +23,7 @@ LAUNCH_SOURCE = os.path.join(CSRC, "igc_launch.hip")
 LAUNCH_UNITS = 38  # the (kind, variant) pairs of IGC_LAUNCH_KINDS in igc_host.hpp
 FFN_SOURCE = os.path.join(CSRC, "ffn.hip")
 FFN_LAUNCH_SOURCE = os.path.join(CSRC, "ffn_launch.hip")
-FFN_LAUNCH_UNITS = 8  # the (type, layout) pairs of IGC_FFN_KINDS in ffn_host.hpp
+FFN_LAUNCH_UNITS = 10  # the (type, layout) pairs of IGC_FFN_KINDS in ffn_host.hpp, and both types' joint backward launch
 SOURCES = [ABI_SOURCE, LAUNCH_SOURCE, FFN_SOURCE, FFN_LAUNCH_SOURCE]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -72,12 +72,16 @@ GemmArgs product(long long M, long long N, long long R, const void* A, long long
 }
 
 // part: where the partial tiles of a split reduction go.
-template <int MODE>
-int run_product(GemmArgs& a, const Plan& pl, int type, uint8_t* part, hipStream_t stream) {
+void apply_plan(GemmArgs& a, const Plan& pl, uint8_t* part) {
   a.tiles_m = pl.tiles_m;
   a.tiles_n = pl.tiles_n;
   a.splits = pl.splits;
   a.part = reinterpret_cast<float*>(part);
+}
+
+template <int MODE>
+int run_product(GemmArgs& a, const Plan& pl, int type, uint8_t* part, hipStream_t stream) {
+  apply_plan(a, pl, part);
   return type == IGC_BF16 ? launch_product<true, MODE>(a, pl, stream) : launch_product<false, MODE>(a, pl, stream);
 }
 
@@ -173,12 +177,12 @@ struct Backward {
 };
 
 // Rows per workgroup of the element-wise kernel: enough workgroups to fill
-// the card, with at least 16 rows each so that the partial column sums stay
+// the card, with at least 8 rows each so that the partial column sums stay
 // small beside D.
 int act_rows(int M, int width, int cus) {
   const long long cols = ceil_div(width, 512);
   const long long want = std::max(1LL, 4LL * cus / cols);
-  return (int)std::max(16LL, ceil_div(M, want));
+  return (int)std::max(8LL, ceil_div(M, want));
 }
 
 template <bool BF>
@@ -200,8 +204,7 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
 
-  // workspace: D, column sums, partial tiles (the two products take
-  // turns with them)
+  // workspace: D, column sums, partial tiles
   const int rows = act_rows(b.M, std::max(width, 1), cus);
   const int blocks = (int)ceil_div(b.M, rows);
   const size_t d_bytes = make_d ? round256((size_t)b.M * np * width * 2) : 0;
@@ -214,7 +217,11 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   const bool x_ok = d_ok && dma_operand(b.W, b.ldw, b.K) && (!b.glu || (dma_operand(b.W2, b.ldw2, b.K) && b.ldw == b.ldw2));
   const Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red, x_ok, cus, true);
   const Plan pw = make_plan(igc_ffn::M_DW, red, b.K, b.M, d_ok && dma_operand(b.X, b.ldx, b.K), cus, true);
-  const size_t part = std::max(b.dX ? px.part_bytes : 0, b.dW || b.dW2 ? pw.part_bytes : 0);
+  // one launch for both where they want the same tile
+  const bool want_x = b.dX && b.M > 0 && b.K > 0, want_w = (b.dW || b.dW2) && b.N > 0 && b.K > 0;
+  const bool joint = want_x && want_w && px.variant == pw.variant && px.variant <= P_TILE_64;
+  const size_t x_part = want_x ? round256(px.part_bytes) : 0, w_part = want_w ? round256(pw.part_bytes) : 0;
+  const size_t part = joint ? x_part + w_part : std::max(x_part, w_part);
   const size_t need = d_bytes + s_bytes + part;
   if (query) {
     *query = need;
@@ -252,33 +259,34 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
       launch_act_back<false>(e, b.glu, grid, stream);
     if (int s = launch_status()) return s;
   }
-  if (sums && b.N > 0) {
-    igc_ffn::ColsumArgs f{part_sums, blocks, np, width, b.N, b.db, b.db2};
-    hipLaunchKernelGGL((igc_ffn::colsum_finish_kernel<0>), dim3((unsigned)ceil_div(b.N, 256), np), dim3(256), 0, stream, f);
+  const igc_ffn::ColsumArgs cs{part_sums, blocks, sums && b.N > 0 ? np : 0, width, b.N, b.db, b.db2};
+  if (cs.which_n && !joint) {
+    hipLaunchKernelGGL((igc_ffn::colsum_kernel<0>), dim3((unsigned)colsum_groups(cs)), dim3(256), 0, stream, cs);
     if (int s = launch_status()) return s;
   }
   const void* const A = make_d ? D : b.dY;
   const long long lda = make_d ? (long long)np * width : b.lddy;
-  if (b.dX && b.M > 0 && b.K > 0) {
-    GemmArgs a = product(b.M, b.K, red, A, lda, b.W, b.ldw, b.dX, b.lddx);
-    a.b_rows = b.N;
-    if (b.glu) {
-      a.B2 = static_cast<const uint8_t*>(b.W2);
-      a.ldb2 = b.ldw2;
-      a.r_split = width;
-    }
-    if (int s = run_product<igc_ffn::M_DX>(a, px, b.type, parts, stream)) return s;
+  GemmArgs ax = product(b.M, b.K, red, A, lda, b.W, b.ldw, b.dX, b.lddx);
+  ax.b_rows = b.N;
+  GemmArgs aw = product(red, b.K, b.M, A, lda, b.X, b.ldx, b.dW, b.lddw);
+  aw.m_rows = b.N;
+  if (b.glu) {
+    ax.B2 = static_cast<const uint8_t*>(b.W2);
+    ax.ldb2 = b.ldw2;
+    ax.r_split = width;
+    aw.Y2 = static_cast<uint8_t*>(b.dW2);
+    aw.ldy2 = b.lddw2;
+    aw.m_split = width;
   }
-  if ((b.dW || b.dW2) && b.N > 0 && b.K > 0) {
-    GemmArgs a = product(red, b.K, b.M, A, lda, b.X, b.ldx, b.dW, b.lddw);
-    a.m_rows = b.N;
-    if (b.glu) {
-      a.Y2 = static_cast<uint8_t*>(b.dW2);
-      a.ldy2 = b.lddw2;
-      a.m_split = width;
-    }
-    if (int s = run_product<igc_ffn::M_DW>(a, pw, b.type, parts, stream)) return s;
+  if (joint) {
+    apply_plan(ax, px, parts);
+    apply_plan(aw, pw, parts + x_part);
+    return b.type == IGC_BF16 ? launch_back<true>(ax, px, aw, pw, cs, stream) : launch_back<false>(ax, px, aw, pw, cs, stream);
   }
+  if (want_x)
+    if (int s = run_product<igc_ffn::M_DX>(ax, px, b.type, parts, stream)) return s;
+  if (want_w)
+    if (int s = run_product<igc_ffn::M_DW>(aw, pw, b.type, parts, stream)) return s;
   return IGC_OK;
 }
 

@@ -1,7 +1,7 @@
 // ffn_host.hpp -- host side of the feed-forward products: the launch plan
 // (tile, split, workspace bytes) and the launch on the caller's stream.
-// launch_product<BF, MODE> is instantiated in ffn_launch.hip, once per type
-// and operand layout, so that they compile in parallel; ffn.hip plans and
+// launch_product<BF, MODE> and launch_back<BF> are instantiated in
+// ffn_launch.hip, once per type and operand layout, so that they compile in parallel; ffn.hip plans and
 // calls it.
 #pragma once
 
@@ -121,10 +121,23 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
   X(6, false, igc_ffn::M_DW)     \
   X(7, true, igc_ffn::M_DW)
 
+// Both backward products, planned on one tile size, and the column sums
+// (s.which_n 0: none).
+template <bool BF>
+int launch_back(const igc_ffn::GemmArgs& x, const Plan& px, const igc_ffn::GemmArgs& w, const Plan& pw, const igc_ffn::ColsumArgs& s,
+                hipStream_t stream);
+extern template int launch_back<false>(const igc_ffn::GemmArgs&, const Plan&, const igc_ffn::GemmArgs&, const Plan&,
+                                       const igc_ffn::ColsumArgs&, hipStream_t);
+extern template int launch_back<true>(const igc_ffn::GemmArgs&, const Plan&, const igc_ffn::GemmArgs&, const Plan&,
+                                      const igc_ffn::ColsumArgs&, hipStream_t);
+
 #define IGC_FFN_EXTERN(n, BF, MODE) \
   extern template int launch_product<BF, MODE>(const igc_ffn::GemmArgs&, const Plan&, hipStream_t);
 IGC_FFN_KINDS(IGC_FFN_EXTERN)
 #undef IGC_FFN_EXTERN
+
+// workgroups of the column sums
+inline long long colsum_groups(const igc_ffn::ColsumArgs& s) { return s.which_n * ceil_div(s.N, 64); }
 
 inline int launch_status() {
   const hipError_t e = hipGetLastError();

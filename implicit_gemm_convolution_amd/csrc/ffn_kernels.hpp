@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
 constexpr int tile_lds(int bm, int bn, int depth) { return 128 * ((depth + 1) * bm + (depth == 2 ? 2 : depth + 1) * bn); }
 constexpr int tile_waves(int bm, int bn, int depth) { return 160 * 1024 / tile_lds(bm, bn, depth) > 1 ? 2 : 1; }  // per SIMD
 template <bool BF, int MODE, int BM, int BN, int DEPTH>
-__global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH)) gemm_tile_kernel(const GemmArgs p) {
+__device__ __forceinline__ void tile_product(const GemmArgs& p, const int block, uint8_t* const smem) {
   constexpr bool GLU = MODE == M_GLU, ACOL = MODE == M_DW, BCOL = MODE == M_DX || MODE == M_DW;
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   typedef LdsTile<BM, ACOL> TA;
@@ -812,14 +812,15 @@ __global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH)) gemm_tile_kern
   typedef DmaOperand<BM, ACOL, false> LoadA;
   typedef DmaOperand<BN, BCOL, GLU || MODE == M_DX> LoadB;
   constexpr int RA = DEPTH + 1, RB = DEPTH == 2 ? 2 : DEPTH + 1, UNR = RA == RB ? RA : RA * RB;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[RA * TA::BYTES + RB * TB::BYTES];
+  constexpr int LDS = RA * TA::BYTES + RB * TB::BYTES;
+  static_assert(LDS == tile_lds(BM, BN, DEPTH), "stages");
   auto stA = [&](auto u) -> uint8_t* { return smem + (decltype(u)::value % RA) * TA::BYTES; };
   auto stB = [&](auto u) -> uint8_t* { return smem + RA * TA::BYTES + (decltype(u)::value % RB) * TB::BYTES; };
   const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
-  int tile = blockIdx.x, split = 0;
+  int tile = block, split = 0;
   if (p.splits > 1) {
-    tile = blockIdx.x / p.splits;
-    split = blockIdx.x - tile * p.splits;
+    tile = block / p.splits;
+    split = block - tile * p.splits;
   }
   int tm, tn;
   tile_of(p, tile, tm, tn);
@@ -938,7 +939,60 @@ __global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH)) gemm_tile_kern
       for (int j = 0; j < FN; ++j) out[(i * FN + j) * 256] = acc[i][j];
     return;
   }
-  write_out<BF, MODE, FM, FN, sizeof(smem) / 4>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+  write_out<BF, MODE, FM, FN, LDS / 4>(p, acc, smem + wave * (LDS / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+}
+
+template <bool BF, int MODE, int BM, int BN, int DEPTH>
+__global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH)) gemm_tile_kernel(const GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_lds(BM, BN, DEPTH)];
+  tile_product<BF, MODE, BM, BN, DEPTH>(p, blockIdx.x, smem);
+}
+
+// Column sums of D over its row blocks: out[n] = sum over blocks of
+// sums[block][which][n], in a fixed order.  A workgroup takes 64 columns, each
+// of its waves every fourth block.
+struct ColsumArgs {
+  const float* sums;
+  int blocks, which_n, width, N;
+  float *out0, *out1;
+};
+__device__ __forceinline__ void colsum(const ColsumArgs& p, int group, float* lds) {
+  const int per = (p.N + 63) / 64, which = group / per;
+  const int n = (group - which * per) * 64 + (threadIdx.x & 63), wave = wave_id();
+  float* const out = which ? p.out1 : p.out0;
+  float s = 0.0f;
+  if (out && n < p.N) {
+    const float* const in = p.sums + (long long)which * p.width + n;
+    const long long step = (long long)p.which_n * p.width;
+#pragma unroll 8
+    for (int b = wave; b < p.blocks; b += 4) s += in[b * step];
+  }
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  if (wave == 0 && out && n < p.N) out[n] = (s + lds[64 + threadIdx.x]) + (lds[128 + threadIdx.x] + lds[192 + threadIdx.x]);
+}
+template <int NONE = 0>
+__global__ void __launch_bounds__(256) colsum_kernel(const ColsumArgs p) {
+  __shared__ float lds[256];
+  colsum(p, blockIdx.x, lds);
+}
+
+// Both backward products on one tile size, and the column sums, in one
+// launch: workgroups [0, x_blocks) work on dX, [x_pad, x_pad + w_blocks) on dW
+// (x_pad: a multiple of 8, so that dW's tiles keep their XCDs), the rest on the
+// sums.  What one leaves of the last round of compute units the next fills.
+template <bool BF, int BM, int BN, int DEPTH>
+__global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH))
+    gemm_back_kernel(const GemmArgs px, const GemmArgs pw, const ColsumArgs ps, int x_blocks, int x_pad, int w_blocks) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_lds(BM, BN, DEPTH)];
+  const int b = blockIdx.x;
+  if (b < x_pad) {
+    if (b < x_blocks) tile_product<BF, M_DX, BM, BN, DEPTH>(px, b, smem);
+  } else if (b < x_pad + w_blocks) {
+    tile_product<BF, M_DW, BM, BN, DEPTH>(pw, b - x_pad, smem);
+  } else {
+    colsum(ps, b - x_pad - w_blocks, reinterpret_cast<float*>(smem));
+  }
 }
 
 // The second launch of a split reduction: one wave for each wave of a tile.
@@ -978,10 +1032,13 @@ struct ActBackArgs {
   float* sums;     // out (NULL: none): column sums of each row block, [row blocks][1 or 2][width]
   int rows;        // rows per block
 };
-// A workgroup covers 512 columns (8 per lane) x `rows` rows, its four waves
-// taking rows in turn.  Streams its inputs once: bound by memory.
+// A workgroup covers 512 columns (8 per lane) x `rows` rows; its four waves
+// take rows in turn, UR at a time so that their loads fly together.  Streams
+// its inputs once: bound by memory (4096 x 8192 with gelu: 201 MB in 42 us;
+// the gated block at 4096 x 10944: 448 MB in 81 us).
 template <bool BF, bool GLU>
 __global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p) {
+  constexpr int UR = GLU ? 2 : 4;
   __shared__ float part[GLU ? 2 : 1][4][512];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int c = blockIdx.x * 512 + lane * 8;
@@ -991,38 +1048,52 @@ __global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) s1[e] = s2[e] = 0.0f;
   if (c < p.width) {
-    for (int r = r0 + wave; r < r1; r += 4) {
-      float dy[8], z[8], f[8], d[8];
-      unpack8<BF>(load8(p.dY + ((long long)r * p.lddy + c) * 2, left), dy);
-      if (p.Z) unpack8<BF>(load8(p.Z + ((long long)r * p.ldz + c) * 2, left), z);
-      if constexpr (GLU) {
-        float u[8], du[8];
-        unpack8<BF>(load8(p.U + ((long long)r * p.ldu + c) * 2, left), u);
-        act_n<true>(p.act, z, f, d);
+    for (int rb = r0 + wave; rb < r1; rb += 4 * UR) {
+      uint4 vy[UR], vz[UR], vu[UR];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          du[e] = dy[e] * f[e];
-          d[e] = dy[e] * u[e] * d[e];
-          if (e >= left) du[e] = d[e] = 0.0f;
-          s1[e] += d[e];
-          s2[e] += du[e];
-        }
-        if (p.D) {
-          store8(p.D + ((long long)r * p.ldd + c) * 2, pack8<BF>(d), 8);
-          store8(p.D + ((long long)r * p.ldd + p.width + c) * 2, pack8<BF>(du), 8);
-        }
-      } else {
-        if (p.Z) {
+      for (int q = 0; q < UR; ++q) {
+        const long long r = rb + 4 * q;
+        const int have = r < r1 ? left : 0;
+        vy[q] = load8(p.dY + (r * p.lddy + c) * 2, have);
+        vz[q] = p.Z ? load8(p.Z + (r * p.ldz + c) * 2, have) : make_uint4(0, 0, 0, 0);
+        if constexpr (GLU) vu[q] = load8(p.U + (r * p.ldu + c) * 2, have);
+      }
+#pragma unroll
+      for (int q = 0; q < UR; ++q) {
+        const long long r = rb + 4 * q;
+        if (r >= r1) break;
+        float dy[8], z[8], f[8], d[8];
+        unpack8<BF>(vy[q], dy);
+        unpack8<BF>(vz[q], z);
+        if constexpr (GLU) {
+          float u[8], du[8];
+          unpack8<BF>(vu[q], u);
           act_n<true>(p.act, z, f, d);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dy[e] *= d[e];
-        }
+          for (int e = 0; e < 8; ++e) {
+            du[e] = dy[e] * f[e];
+            d[e] = dy[e] * u[e] * d[e];
+            if (e >= left) du[e] = d[e] = 0.0f;
+            s1[e] += d[e];
+            s2[e] += du[e];
+          }
+          if (p.D) {
+            store8(p.D + (r * p.ldd + c) * 2, pack8<BF>(d), 8);
+            store8(p.D + (r * p.ldd + p.width + c) * 2, pack8<BF>(du), 8);
+          }
+        } else {
+          if (p.Z) {
+            act_n<true>(p.act, z, f, d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (e >= left) dy[e] = 0.0f;
-          s1[e] += dy[e];
+            for (int e = 0; e < 8; ++e) dy[e] *= d[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (e >= left) dy[e] = 0.0f;
+            s1[e] += dy[e];
+          }
+          if (p.D) store8(p.D + (r * p.ldd + c) * 2, pack8<BF>(dy), 8);
         }
-        if (p.D) store8(p.D + ((long long)r * p.ldd + c) * 2, pack8<BF>(dy), 8);
       }
     }
   }
@@ -1040,22 +1111,6 @@ __global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p) {
       p.sums[((long long)blockIdx.y * NP + which) * p.width + col] =
           (part[which][0][cc] + part[which][1][cc]) + (part[which][2][cc] + part[which][3][cc]);
   }
-}
-
-// out[n] = sum over row blocks of sums[block][which][n], in block order.
-struct ColsumArgs {
-  const float* sums;
-  int blocks, which_n, width, N;
-  float *out0, *out1;
-};
-template <int NONE = 0>
-__global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs p) {
-  const int n = blockIdx.x * 256 + threadIdx.x, which = blockIdx.y;
-  float* const out = which ? p.out1 : p.out0;
-  if (n >= p.N || !out) return;
-  float s = 0.0f;
-  for (int b = 0; b < p.blocks; ++b) s += p.sums[((long long)b * p.which_n + which) * p.width + n];
-  out[n] = s;
 }
 
 }  // namespace igc_ffn

@@ -1,6 +1,6 @@
 // ffn_launch.hip -- the kernels of the feed-forward products: launch_product
-// of ffn_host.hpp for the pairs of IGC_FFN_KINDS.  The build compiles this
-// file once per pair with -DIGC_FFN_UNIT=<n>.
+// of ffn_host.hpp for the pairs of IGC_FFN_KINDS, and launch_back for both
+// types.  The build compiles this file once for each with -DIGC_FFN_UNIT=<n>.
 #include "ffn_host.hpp"
 
 namespace igc_ffn_host {
@@ -49,6 +49,33 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
   return launch_status();
 }
 
+template <bool BF>
+int launch_back(const igc_ffn::GemmArgs& x, const Plan& px, const igc_ffn::GemmArgs& w, const Plan& pw, const igc_ffn::ColsumArgs& s,
+                hipStream_t stream) {
+  const long long nx = (long long)px.tiles_m * px.tiles_n * px.splits, nw = (long long)pw.tiles_m * pw.tiles_n * pw.splits;
+  const long long pad = ceil_div(nx, 8) * 8, grid = pad + nw + colsum_groups(s);
+  if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many tiles (%lld)", grid);
+  const dim3 g((unsigned)grid), t(256), tj(64);
+  const dim3 gx((unsigned)(px.tiles_m * px.tiles_n * 4)), gw((unsigned)(pw.tiles_m * pw.tiles_n * 4));
+#define IGC_FFN_BACK(BM, BN, DEPTH)                                                                                            \
+  do {                                                                                                                         \
+    hipLaunchKernelGGL((igc_ffn::gemm_back_kernel<BF, BM, BN, DEPTH>), g, t, 0, stream, x, w, s, (int)nx, (int)pad, (int)nw);     \
+    if (px.splits > 1) hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, igc_ffn::M_DX, BM, BN>), gx, tj, 0, stream, x);         \
+    if (pw.splits > 1) hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, igc_ffn::M_DW, BM, BN>), gw, tj, 0, stream, w);         \
+  } while (0)
+  switch (px.variant) {
+    case P_TILE_256: IGC_FFN_BACK(256, 256, 2); break;
+    case P_TILE_128: IGC_FFN_BACK(128, 128, 2); break;
+    case P_TILE_64: IGC_FFN_BACK(64, 64, 4); break;
+    default: return fail(IGC_EUNSUPPORTED, "internal: no joint kernel for variant %d", px.variant);
+  }
+#undef IGC_FFN_BACK
+  return launch_status();
+}
+#define IGC_FFN_DEFINE_BACK(BF)                                                                                       \
+  template int launch_back<BF>(const igc_ffn::GemmArgs&, const Plan&, const igc_ffn::GemmArgs&, const Plan&,          \
+                               const igc_ffn::ColsumArgs&, hipStream_t);
+
 #define IGC_FFN_DEFINE(BF, MODE) template int launch_product<BF, MODE>(const igc_ffn::GemmArgs&, const Plan&, hipStream_t);
 #if IGC_FFN_UNIT == 0
 IGC_FFN_DEFINE(false, igc_ffn::M_FWD)
@@ -66,8 +93,12 @@ IGC_FFN_DEFINE(true, igc_ffn::M_DX)
 IGC_FFN_DEFINE(false, igc_ffn::M_DW)
 #elif IGC_FFN_UNIT == 7
 IGC_FFN_DEFINE(true, igc_ffn::M_DW)
+#elif IGC_FFN_UNIT == 8
+IGC_FFN_DEFINE_BACK(false)
+#elif IGC_FFN_UNIT == 9
+IGC_FFN_DEFINE_BACK(true)
 #else
-#error "IGC_FFN_UNIT: 0 .. 7"
+#error "IGC_FFN_UNIT: 0 .. 9"
 #endif
 
 }  // namespace igc_ffn_host

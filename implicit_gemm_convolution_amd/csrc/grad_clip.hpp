@@ -37,10 +37,14 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // Runs f(tensor, first element, elements) for every chunk of this workgroup.
-template <class F>
+// REVERSE: from the last chunk to the first, so that the second pass begins
+// with what the first one read last and the memory-side cache (256 MB) still
+// holds.
+template <bool REVERSE, class F>
 __device__ __forceinline__ void clip_chunks(const ClipTable& p, F&& f) {
   const int chunks = p.first[p.count];
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+  for (int b = blockIdx.x; b < chunks; b += gridDim.x) {
+    const int c = REVERSE ? chunks - 1 - b : b;
     int lo = 0, hi = p.count - 1;  // the last tensor whose first chunk is <= c (empty tensors have none)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -106,7 +110,7 @@ template <int NONE = 0>
 __global__ void __launch_bounds__(256) clip_norm_kernel(const ClipTable p) {
   __shared__ double sm[4];
   double s = 0.0;
-  clip_chunks(p, [&](int t, long long e0, int n) {
+  clip_chunks<false>(p, [&](int t, long long e0, int n) {
     if (p.type[t] == T_F32)
       s += chunk_squares<T_F32>(p.in[t] + e0 * 4, n);
     else if (p.type[t] == T_BF16)
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(256) clip_scale_kernel(const ClipTable p) {
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
   const double ratio = (double)p.max_norm / (norm + 1e-6);
   const float scale = ratio > 1.0 ? 1.0f : (float)ratio;  // (NaN stays NaN)
-  clip_chunks(p, [&](int t, long long e0, int n) {
+  clip_chunks<true>(p, [&](int t, long long e0, int n) {
     if (p.type[t] == T_F32)
       chunk_scale<T_F32>(p.in[t] + e0 * 4, p.out[t] + e0 * 4, n, scale);
     else if (p.type[t] == T_BF16)
