@@ -75,6 +75,7 @@ GemmArgs product(long long M, long long N, long long R, const void* A, long long
 void apply_plan(GemmArgs& a, const Plan& pl, uint8_t* part) {
   a.tiles_m = pl.tiles_m;
   a.tiles_n = pl.tiles_n;
+  a.whole = (int)pl.whole;
   a.splits = pl.splits;
   a.part = reinterpret_cast<float*>(part);
 }
@@ -84,6 +85,40 @@ int run_product(GemmArgs& a, const Plan& pl, int type, uint8_t* part, hipStream_
   apply_plan(a, pl, part);
   return type == IGC_BF16 ? launch_product<true, MODE>(a, pl, stream) : launch_product<false, MODE>(a, pl, stream);
 }
+
+// Operands that are copied into padded rows of the workspace, in the order in
+// which they are added.
+struct Pads {
+  igc_ffn::PadArgs args;
+  size_t bytes = 0;       // workspace
+  long long moved = 0;    // bytes read and written
+  size_t at[igc_ffn::PAD_MOST] = {};
+  bool possible = true;
+  Pads() { std::memset(&args, 0, sizeof(args)); }
+  static long long padded(long long cols) { return ceil_div(cols, 8) * 8; }
+  int add(const void* p, long long ld, long long rows, long long cols) {
+    const int i = args.count++;
+    const long long chunks = rows * (padded(cols) / 8);
+    possible = possible && rows > 0 && cols >= 8 && chunks <= 0x7fffffffLL && padded(cols) <= (1 << 21) - 8;
+    args.src[i] = static_cast<const uint8_t*>(p);
+    args.ld[i] = ld * 2;
+    args.cols[i] = (int)cols;
+    args.chunks[i] = (uint32_t)chunks;
+    args.first[i + 1] = args.first[i] + (int)ceil_div(chunks, 1024);
+    at[i] = bytes;
+    bytes += round256((size_t)rows * padded(cols) * 2);
+    moved += 4 * rows * cols;
+    return i;
+  }
+  int groups() const { return args.first[args.count]; }
+  const uint8_t* place(int i, uint8_t* ws) {
+    args.dst[i] = ws + at[i];
+    return args.dst[i];
+  }
+};
+
+// What the copy takes in a launch of its own.
+inline float pad_us(const Pads& p) { return 4.0f + (float)p.moved / 5e6f; }
 
 // ---------------------------------------------------------------- forward
 template <int MODE>
@@ -95,16 +130,41 @@ int forward(GemmArgs& a, int type, void* ws, size_t ws_bytes, size_t* query, hip
   int dev;
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
-  const bool aligned = dma_operand(a.A, a.lda, a.R) && dma_operand(a.B, a.ldb, a.R) &&
-                       (MODE != igc_ffn::M_GLU || dma_operand(a.B2, a.ldb2, a.R));
-  const Plan pl = make_plan(MODE, a.M, a.N, a.R, aligned, cus, query || ws);
-  const size_t need = pl.part_bytes;
+  const bool may = query || ws;
+  const bool a_ok = dma_operand(a.A, a.lda, a.R), b_ok = dma_operand(a.B, a.ldb, a.R);
+  const bool b2_ok = MODE != igc_ffn::M_GLU || dma_operand(a.B2, a.ldb2, a.R);
+  Plan pl = make_plan(MODE, a.M, a.N, a.R, a_ok && b_ok && b2_ok, cus, may);
+  Pads pads;
+  // Operands of another alignment are copied into padded rows where the copy
+  // costs less than the faster kernel gains (bf16, us, without and with:
+  // 200 x 1000 x 257 7.4 and 9.5, 727 x 1344 x 6130 65 and 39, the gated block
+  // at 304 x 7200 x 5402 125 and 148, at 6900 x 2600 x 2201 260 and 170).
+  if (may && (pl.variant == P_ANY_128 || pl.variant == P_ANY_64)) {
+    const int ia = a_ok ? -1 : pads.add(a.A, a.lda, a.M, a.R), ib = b_ok ? -1 : pads.add(a.B, a.ldb, a.N, a.R);
+    const int ib2 = b2_ok ? -1 : pads.add(a.B2, a.ldb2, a.N, a.R);
+    const Plan aligned = make_plan(MODE, a.M, a.N, Pads::padded(a.R), true, cus, may);
+    if (pads.possible && pad_us(pads) + aligned.us < pl.us) {
+      pl = aligned;
+      uint8_t* const to = static_cast<uint8_t*>(ws);
+      if (ia >= 0) a.A = pads.place(ia, to), a.lda = Pads::padded(a.R);
+      if (ib >= 0) a.B = pads.place(ib, to), a.ldb = Pads::padded(a.R);
+      if (ib2 >= 0) a.B2 = pads.place(ib2, to), a.ldb2 = Pads::padded(a.R);
+      a.R = a.r_split = a.b_rows = (int)Pads::padded(a.R);
+    } else {
+      pads = Pads();
+    }
+  }
+  const size_t need = pads.bytes + pl.part_bytes;
   if (query) {
     *query = need;
     return IGC_OK;
   }
   if (int s = check_ws(ws, ws_bytes, need, false)) return s;
-  return run_product<MODE>(a, pl, type, static_cast<uint8_t*>(ws), stream);
+  if (pads.groups() > 0) {
+    hipLaunchKernelGGL((igc_ffn::pad_kernel<0>), dim3((unsigned)pads.groups()), dim3(256), 0, stream, pads.args);
+    if (int s = launch_status()) return s;
+  }
+  return run_product<MODE>(a, pl, type, static_cast<uint8_t*>(ws) + pads.bytes, stream);
 }
 
 int linear_forward_impl(const igc_linear_forward* d, size_t* query, hipStream_t stream) {
@@ -186,17 +246,50 @@ int act_rows(int M, int width, int cus) {
 }
 
 template <bool BF>
-void launch_act_back(const igc_ffn::ActBackArgs& e, bool glu, dim3 grid, hipStream_t stream) {
+void launch_act_back(const igc_ffn::ActBackArgs& e, bool glu, const igc_ffn::PadArgs& pads, dim3 grid, hipStream_t stream) {
   if (glu)
-    hipLaunchKernelGGL((igc_ffn::act_back_kernel<BF, true>), grid, dim3(256), 0, stream, e);
+    hipLaunchKernelGGL((igc_ffn::act_back_kernel<BF, true>), grid, dim3(256), 0, stream, e, pads);
   else
-    hipLaunchKernelGGL((igc_ffn::act_back_kernel<BF, false>), grid, dim3(256), 0, stream, e);
+    hipLaunchKernelGGL((igc_ffn::act_back_kernel<BF, false>), grid, dim3(256), 0, stream, e, pads);
+}
+
+// Both products in one launch, or each in its own: whichever is estimated
+// to be faster.  True for one launch (on one tile).
+bool plan_back(Plan& px, Plan& pw, long long M, long long K, long long red, bool sums, int cus) {
+  float best = px.us + pw.us + (sums ? 3.0f : 0.0f);
+  bool joint = false;
+  for (int v = P_TILE_256; v <= P_TILE_64; ++v) {
+    const TileCost& c = tile_cost(igc_ffn::M_DX, v);
+    const int places = tile_places(igc_ffn::M_DX, v);
+    const Plan sx = best_split(igc_ffn::M_DX, v, M, K, red, cus, true), sw = best_split(igc_ffn::M_DW, v, red, K, M, cus, true);
+    for (int i = 0; i < 4; ++i) {
+      if (((i & 1) && sx.splits == 1) || ((i & 2) && sw.splits == 1)) continue;
+      const Plan x = i & 1 ? sx : tile_plan(igc_ffn::M_DX, v, M, K), w = i & 2 ? sw : tile_plan(igc_ffn::M_DW, v, red, K);
+      // (the second product starts at a multiple of 8 workgroups; a whole
+      // round must not run over by those that keep it there)
+      const long long cx = ceil_div(workgroups(x), 8) * 8, cw = ceil_div(workgroups(w), 8) * 8;
+      // K tiles in all and of the longest workgroup
+      const float kx = (float)k_tiles(red) * (float)x.tiles_m * (float)x.tiles_n, kw = (float)k_tiles(M) * (float)w.tiles_m * (float)w.tiles_n;
+      const float nx = (float)k_tiles(red) / (float)(x.whole ? 1 : x.splits), nw = (float)k_tiles(M) / (float)(w.whole ? 1 : w.splits);
+      // (the longer ones come first: more than run at once take what the
+      // average does, or as long as the longest)
+      const float most = std::max(nx, nw), mean = (kx + kw) / (float)(cx + cw);
+      const bool several = cx + cw > (long long)places * cus;
+      const float run = rounds_us(c, places, several ? mean : most, cx + cw, cus);
+      const float us = c.launch + std::max(run, most * c.k1 + c.out) + join_us(c, x) + join_us(c, w);
+      if (us < best) {
+        best = us;
+        joint = true;
+        px = x;
+        pw = w;
+      }
+    }
+  }
+  return joint;
 }
 
 int backward(const Backward& b, size_t* query, hipStream_t stream) {
-  const bool products = b.dX || b.dW || b.dW2;
   const bool sums = b.db || b.db2;
-  const bool make_d = products && (b.glu || b.act != IGC_ACT_NONE);
   const int np = b.glu ? 2 : 1;
   const int width = (int)std::min<long long>(ceil_div(b.N, 64) * 64, 0x7fffffc0);
   if (b.glu && width > (1 << 30)) return fail(IGC_EUNSUPPORTED, "N too large");
@@ -204,25 +297,51 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
 
-  // workspace: D, column sums, partial tiles
+  const bool want_x = b.dX && b.M > 0 && b.K > 0, want_w = (b.dW || b.dW2) && b.N > 0 && b.K > 0;
+  const bool act = b.glu || b.act != IGC_ACT_NONE;
+  // What the direct loads take as it is.  D made here is padded with zeros
+  // to `width` columns.  (The two weights of the gated block take turns
+  // under one set of lane offsets, so they need one leading dimension.)
+  const bool d_fits = (long long)np * width <= (1 << 21) - 8;
+  bool make_d = act && (want_x || want_w);
+  bool d_ok = make_d ? d_fits : dma_operand(b.dY, b.lddy, b.N);
+  bool w_ok = dma_operand(b.W, b.ldw, b.K) && (!b.glu || (dma_operand(b.W2, b.ldw2, b.K) && b.ldw == b.ldw2));
+  bool x_ok = dma_operand(b.X, b.ldx, b.K);
+  auto red = [&]() { return make_d ? np * width : b.N; };  // columns of D
+
+  // Operands of another alignment are copied into padded rows, by the launch
+  // that makes D if there is one.  (Down the rows, loads of any alignment wait
+  // longest: dW of 72 x 601 x 400 9.2 us without and 9.0 with the copy,
+  // 600 x 1001 x 1000 25.6 and 12.7, 727 x 1345 x 6130 285 and 38.)
+  Pads pads;
+  int iw = -1, iw2 = -1, ix = -1;
+  const bool fix_x = want_x && !(d_ok && w_ok), fix_w = want_w && !(d_ok && x_ok);
+  if ((fix_x || fix_w) && b.M > 0 && b.N > 0 && d_fits) {
+    if (want_x && !w_ok) {
+      iw = pads.add(b.W, b.ldw, b.N, b.K);
+      if (b.glu) iw2 = pads.add(b.W2, b.ldw2, b.N, b.K);
+    }
+    if (want_w && !x_ok) ix = pads.add(b.X, b.ldx, b.M, b.K);
+    if (pads.possible) {
+      make_d = make_d || !d_ok;
+      d_ok = w_ok = x_ok = true;
+    } else {
+      pads = Pads();
+      iw = iw2 = ix = -1;
+    }
+  }
+  Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red(), d_ok && w_ok, cus, true);
+  Plan pw = make_plan(igc_ffn::M_DW, red(), b.K, b.M, d_ok && x_ok, cus, true);
+  const bool joint = want_x && want_w && d_ok && w_ok && x_ok && plan_back(px, pw, b.M, b.K, red(), sums, cus);
+
+  // workspace: D, column sums, padded operands, partial tiles
   const int rows = act_rows(b.M, std::max(width, 1), cus);
   const int blocks = (int)ceil_div(b.M, rows);
   const size_t d_bytes = make_d ? round256((size_t)b.M * np * width * 2) : 0;
   const size_t s_bytes = sums ? round256((size_t)blocks * np * width * 4) : 0;
-  // D made here is padded with zeros to `width` columns
-  const int red = make_d ? np * width : b.N;
-  // (the two weights of the gated block take turns under one set of lane
-  // offsets, so the direct loads need one leading dimension for both)
-  const bool d_ok = make_d ? (long long)np * width <= (1 << 21) - 8 : dma_operand(b.dY, b.lddy, b.N);
-  const bool x_ok = d_ok && dma_operand(b.W, b.ldw, b.K) && (!b.glu || (dma_operand(b.W2, b.ldw2, b.K) && b.ldw == b.ldw2));
-  const Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red, x_ok, cus, true);
-  const Plan pw = make_plan(igc_ffn::M_DW, red, b.K, b.M, d_ok && dma_operand(b.X, b.ldx, b.K), cus, true);
-  // one launch for both where they want the same tile
-  const bool want_x = b.dX && b.M > 0 && b.K > 0, want_w = (b.dW || b.dW2) && b.N > 0 && b.K > 0;
-  const bool joint = want_x && want_w && px.variant == pw.variant && px.variant <= P_TILE_64;
   const size_t x_part = want_x ? round256(px.part_bytes) : 0, w_part = want_w ? round256(pw.part_bytes) : 0;
   const size_t part = joint ? x_part + w_part : std::max(x_part, w_part);
-  const size_t need = d_bytes + s_bytes + part;
+  const size_t need = d_bytes + s_bytes + pads.bytes + part;
   if (query) {
     *query = need;
     return IGC_OK;
@@ -231,16 +350,23 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   uint8_t* const ws = static_cast<uint8_t*>(b.ws);
   uint8_t* const D = make_d ? ws : nullptr;
   float* const part_sums = sums ? reinterpret_cast<float*>(ws + d_bytes) : nullptr;
-  uint8_t* const parts = ws + d_bytes + s_bytes;
+  uint8_t* const padded = ws + d_bytes + s_bytes;
+  uint8_t* const parts = padded + pads.bytes;
 
-  if ((make_d || sums) && b.M > 0 && b.N > 0) {
+  const void *W = b.W, *W2 = b.W2, *X = b.X;
+  long long ldw = b.ldw, ldw2 = b.ldw2, ldx = b.ldx;
+  if (iw >= 0) W = pads.place(iw, padded), ldw = Pads::padded(b.K);
+  if (iw2 >= 0) W2 = pads.place(iw2, padded), ldw2 = Pads::padded(b.K);
+  if (ix >= 0) X = pads.place(ix, padded), ldx = Pads::padded(b.K);
+  const bool element = (make_d || sums) && b.M > 0 && b.N > 0;
+  if (element) {
     igc_ffn::ActBackArgs e;
     std::memset(&e, 0, sizeof(e));
     e.M = b.M;
     e.N = b.N;
     e.dY = static_cast<const uint8_t*>(b.dY);
     e.lddy = b.lddy;
-    if (b.glu || b.act != IGC_ACT_NONE) {
+    if (act) {
       e.Z = static_cast<const uint8_t*>(b.Z);
       e.ldz = b.ldz;
     }
@@ -252,11 +378,17 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
     e.width = width;
     e.sums = part_sums;
     e.rows = rows;
-    const dim3 grid((unsigned)ceil_div(width, 512), (unsigned)blocks);
+    e.groups = (int)ceil_div(width, 512);
+    e.blocks = blocks;
+    const long long grid = (long long)e.groups * blocks + pads.groups();
+    if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many workgroups (%lld)", grid);
     if (b.type == IGC_BF16)
-      launch_act_back<true>(e, b.glu, grid, stream);
+      launch_act_back<true>(e, b.glu, pads.args, dim3((unsigned)grid), stream);
     else
-      launch_act_back<false>(e, b.glu, grid, stream);
+      launch_act_back<false>(e, b.glu, pads.args, dim3((unsigned)grid), stream);
+    if (int s = launch_status()) return s;
+  } else if (pads.groups() > 0) {
+    hipLaunchKernelGGL((igc_ffn::pad_kernel<0>), dim3((unsigned)pads.groups()), dim3(256), 0, stream, pads.args);
     if (int s = launch_status()) return s;
   }
   const igc_ffn::ColsumArgs cs{part_sums, blocks, sums && b.N > 0 ? np : 0, width, b.N, b.db, b.db2};
@@ -266,13 +398,13 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   }
   const void* const A = make_d ? D : b.dY;
   const long long lda = make_d ? (long long)np * width : b.lddy;
-  GemmArgs ax = product(b.M, b.K, red, A, lda, b.W, b.ldw, b.dX, b.lddx);
+  GemmArgs ax = product(b.M, b.K, red(), A, lda, W, ldw, b.dX, b.lddx);
   ax.b_rows = b.N;
-  GemmArgs aw = product(red, b.K, b.M, A, lda, b.X, b.ldx, b.dW, b.lddw);
+  GemmArgs aw = product(red(), b.K, b.M, A, lda, X, ldx, b.dW, b.lddw);
   aw.m_rows = b.N;
   if (b.glu) {
-    ax.B2 = static_cast<const uint8_t*>(b.W2);
-    ax.ldb2 = b.ldw2;
+    ax.B2 = static_cast<const uint8_t*>(W2);
+    ax.ldb2 = ldw2;
     ax.r_split = width;
     aw.Y2 = static_cast<uint8_t*>(b.dW2);
     aw.ldy2 = b.lddw2;

@@ -38,8 +38,10 @@ enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_ANY_128, P_ANY_64, P_SKINNY_
 struct Plan {
   int variant = P_ANY_64;
   int tiles_m = 0, tiles_n = 0;
-  int splits = 1;
-  size_t part_bytes = 0;  // partial tiles of a split reduction
+  long long whole = 0;    // tiles [0, whole) have a workgroup each,
+  int splits = 1;         // the others this many that share the reduction
+  size_t part_bytes = 0;  // their partial tiles
+  float us = 0;           // estimate
 };
 
 inline void plan_tile(int mode, int variant, int& bm, int& bn) {
@@ -58,16 +60,115 @@ inline bool dma_operand(const void* p, long long ld, long long length) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0 && length > 0 && length % 8 == 0 && ld <= (1 << 21) - 8;
 }
 
-// A pure function of the problem and the device, so that the size queries and
-// the calls agree.  may_split: the call has (or the query assumes) a
-// workspace.  Times below: bf16 on MI355X, N = K = 4096 unless said.
-inline Plan make_plan(int mode, long long M, long long N, long long R, bool aligned, int cus, bool may_split) {
+// What a launch of the aligned tiles takes, in us, fitted to 2700 timings on
+// MI355X (bf16; 40 outputs of 16 x 4096 to 8192 x 8192, reductions of 512 to
+// 30000, one to sixteen splits).  Over those products the plan with the
+// smallest estimate takes 0.7% longer than the fastest one in the mean and 16%
+// at most (gated block 1.5% and 12%).  Tiles chosen by how many fill the card,
+// split only below one per compute unit: 5%, and 1.9 times as long at
+// 640 x 2432 x 27392.
+//   k0, k1, k2  a K tile of 64 in an empty card; with one workgroup on every
+//               compute unit (256 x 256: on half of them); with every place taken
+//   out         the prologue and the outputs of a workgroup
+//   join        the second launch of a split reduction: itself, for each MB
+//               of partial tiles, for each split
+struct TileCost {
+  float launch, k0, k1, k2, out, join, join_mb, join_split;
+};
+inline const TileCost& tile_cost(int mode, int variant) {
+  static constexpr TileCost one[3] = {{2.1f, 0.77f, 1.02f, 1.35f, 11.8f, 0.0f, 0.17f, 0.0f},
+                                      {2.4f, 0.35f, 0.51f, 0.91f, 2.3f, 2.1f, 0.15f, 0.32f},
+                                      {2.8f, 0.18f, 0.23f, 0.37f, 1.0f, 1.4f, 0.31f, 0.40f}};
+  static constexpr TileCost two[3] = {{2.6f, 0.96f, 1.07f, 1.40f, 10.2f, 0.0f, 0.20f, 0.0f},
+                                      {3.8f, 0.33f, 0.53f, 0.94f, 1.5f, 2.4f, 0.11f, 0.43f},
+                                      {3.0f, 0.19f, 0.24f, 0.30f, 2.3f, 1.2f, 0.64f, 0.0f}};
+  return (mode == igc_ffn::M_GLU ? two : one)[variant];
+}
+// workgroups of a tile that share a compute unit (160 KB of LDS)
+inline int tile_places(int mode, int variant) {
+  return variant == P_TILE_256 || (variant == P_TILE_64 && mode == igc_ffn::M_GLU) ? 1 : 2;
+}
+// `count` workgroups of n K tiles each
+inline float rounds_us(const TileCost& c, int places, float n, long long count, int cus) {
+  const long long cap = (long long)places * cus;
+  auto round = [&](long long w) {
+    const float f = 2.0f * (float)w / (float)cap;
+    float k = c.k0 + (c.k1 - c.k0) * f;
+    // (two to a compute unit: the first pair is half the way there)
+    if (f > 1.0f) k = c.k1 + (c.k2 - c.k1) * (places == 1 ? f - 1.0f : 0.5f * f);
+    return n * k + c.out * (f > 1.0f ? (float)places : 1.0f);
+  };
+  return (float)(count / cap) * round(cap) + (count % cap ? round(count % cap) : 0.0f);
+}
+inline float join_us(const TileCost& c, const Plan& pl) {
+  return pl.splits > 1 ? c.join + c.join_mb * (float)pl.part_bytes * 1e-6f + c.join_split * (float)pl.splits : 0.0f;
+}
+
+inline long long workgroups(const Plan& pl) {
+  return pl.whole + ((long long)pl.tiles_m * pl.tiles_n - pl.whole) * pl.splits;
+}
+inline Plan tile_plan(int mode, int variant, long long M, long long N, long long whole = 0, int splits = 1) {
   Plan pl;
   int bm, bn;
+  plan_tile(mode, variant, bm, bn);
+  pl.variant = variant;
+  pl.tiles_m = (int)ceil_div(M, bm);
+  pl.tiles_n = (int)ceil_div(N, bn);
+  pl.whole = whole;
+  pl.splits = splits;
+  if (splits > 1) pl.part_bytes = (size_t)((long long)pl.tiles_m * pl.tiles_n - whole) * splits * bm * bn * (mode == igc_ffn::M_GLU ? 8 : 4);
+  return pl;
+}
+inline long long k_tiles(long long R) { return std::max(1LL, ceil_div(R, 64)); }
+
+// The best plan on one of the aligned tiles.  Where the last round of
+// workgroups does not fill the card, its tiles may be split: into at most 16
+// parts of at least four K tiles, and into no more workgroups than run at once.
+inline Plan best_split(int mode, int variant, long long M, long long N, long long R, int cus, bool may_split) {
+  const TileCost& c = tile_cost(mode, variant);
+  const int places = tile_places(mode, variant);
+  const long long cap = (long long)places * cus;
+  const float nk = (float)k_tiles(R);
+  Plan best = tile_plan(mode, variant, M, N);
+  const long long tiles = (long long)best.tiles_m * best.tiles_n, whole = tiles / cap * cap;
+  best.us = c.launch + rounds_us(c, places, nk, tiles, cus);
+  for (int s = 2; may_split && s <= 16 && (float)s <= nk / 4 && (tiles - whole) * s <= cap; ++s) {
+    Plan pl = tile_plan(mode, variant, M, N, whole, s);
+    pl.us = c.launch + rounds_us(c, places, nk, whole, cus) + rounds_us(c, places, nk / (float)s, (tiles - whole) * s, cus) + join_us(c, pl);
+    if (pl.us + (best.splits == 1 ? 1.0f : 0.0f) < best.us) best = pl;  // (to gain 1 us at least)
+  }
+  return best;
+}
+
+// The plan on one of the tiles for any operands, whose K loop waits for its
+// loads: so many us for a K tile, or for each K tile of each workgroup where
+// there are many.  (bf16, 128 x 128 | 64 x 64, rows of odd length:
+// 136 x 4000 x 2001 42 | 27 us, 2000 x 2000 x 2001 46 | 50,
+// 6900 x 2600 x 2201 156 | 203.)  A second launch and the partial tiles'
+// traffic cost about 20 K tiles' time.
+inline Plan any_plan(int mode, int variant, long long M, long long N, long long R, int cus, bool may_split) {
+  Plan pl = tile_plan(mode, variant, M, N);
+  const long long count = (long long)pl.tiles_m * pl.tiles_n, nk = k_tiles(R);
+  const bool large = variant == P_ANY_128, glu = mode == igc_ffn::M_GLU;
+  const float alone = large ? (glu ? 1.25f : 1.2f) : (glu ? 1.0f : 0.75f);
+  const float each = large ? (glu ? 3.2e-3f : 3.6e-3f) : (glu ? 2.2e-3f : 1.45e-3f);
+  if (may_split && count > 0) {
+    const long long s = std::min(nk / 8, (long long)cus / count);
+    if (s > 1 && nk - nk / s > 24) pl = tile_plan(mode, variant, M, N, 0, (int)s);
+  }
+  pl.us = 3.0f + (float)nk / (float)pl.splits * std::max(alone, each * (float)(count * pl.splits)) + (pl.splits > 1 ? 4.0f : 0.0f);
+  return pl;
+}
+
+// A pure function of the problem and the device, so that the size queries and
+// the calls agree.  may_split: the call has (or the query assumes) a
+// workspace.
+inline Plan make_plan(int mode, long long M, long long N, long long R, bool aligned, int cus, bool may_split) {
+  Plan pl;
   // Few rows: streaming the weights into registers beats 64-row tiles up to
-  // 16 rows (12 rows 10.0 us against 11.9) and, on short reductions, up to 32
-  // (24x2048x1024 5.1 against 6.3; 32 rows 14.0 against 12.3).  Rows of any
-  // alignment have no better kernel up to 64.
+  // 16 rows (12 x 4096 x 4096 10.0 us against 11.9) and, on short reductions,
+  // up to 32 (24x2048x1024 5.1 against 6.3; 32 x 4096 x 4096 14.0 against
+  // 12.3).  Rows of any alignment have no better kernel up to 64.
   if ((mode == igc_ffn::M_FWD || mode == igc_ffn::M_GLU) && (M <= 16 || (M <= 32 && R <= 1024) || (M <= 64 && !aligned))) {
     // 32 weight rows share the loads of X; 16 where there would be too few workgroups
     pl.variant = mode == igc_ffn::M_GLU || N >= 32LL * cus ? P_SKINNY_32 : P_SKINNY_16;
@@ -75,35 +176,16 @@ inline Plan make_plan(int mode, long long M, long long N, long long R, bool alig
     pl.tiles_n = (int)ceil_div(N, pl.variant == P_SKINNY_32 && mode == igc_ffn::M_FWD ? 32 : 16);
     return pl;
   }
-  // The largest tile that fills the card: 256 x 256 from three quarters of
-  // the compute units (M = 4096: 102 us against 118 on 128 x 128 tiles; at
-  // half of them, M = 2048, 93 against 66), 128 x 128 likewise (M = 1024
-  // 37 us against 53 on 64 x 64; M = 512 29.4 against 28.4).
-  auto tiles = [&](int variant) {
-    plan_tile(mode, variant, bm, bn);
-    return ceil_div(M, bm) * ceil_div(N, bn);
-  };
-  if (aligned && 4 * tiles(P_TILE_256) >= 3 * cus)
-    pl.variant = P_TILE_256;
-  else if (4 * tiles(P_TILE_128) >= 3 * cus)
-    pl.variant = aligned ? P_TILE_128 : P_ANY_128;
-  else
-    pl.variant = aligned ? P_TILE_64 : P_ANY_64;
-  plan_tile(mode, pl.variant, bm, bn);
-  pl.tiles_m = (int)ceil_div(M, bm);
-  pl.tiles_n = (int)ceil_div(N, bn);
-  const long long count = (long long)pl.tiles_m * pl.tiles_n;
-  const long long nk = std::max(1LL, ceil_div(R, 64));
-  // Splitting the reduction costs a second launch and the partial tiles'
-  // traffic, about 20 K tiles' time: 64 tiles of 64 K tiles (M = 64) in four
-  // splits 12.5 us against 15.4, 128 tiles (M = 128) in two 13.8 against
-  // 16.0, but 64 tiles of 32 K tiles in two 11.8 against 9.7.
-  if (may_split && count > 0) {
-    const long long s = std::min(nk / 8, (long long)cus / count);
-    if (s > 1 && nk - nk / s > 24) {
-      pl.splits = (int)s;
-      pl.part_bytes = (size_t)count * pl.splits * bm * bn * (mode == igc_ffn::M_GLU ? 8 : 4);
+  if (aligned) {
+    for (int v = P_TILE_256; v <= P_TILE_64; ++v) {
+      const Plan q = best_split(mode, v, M, N, R, cus, may_split);
+      if (v == P_TILE_256 || q.us < pl.us) pl = q;
     }
+    return pl;
+  }
+  for (int v = P_ANY_128; v <= P_ANY_64; ++v) {
+    const Plan q = any_plan(mode, v, M, N, R, cus, may_split);
+    if (v == P_ANY_128 || q.us < pl.us) pl = q;
   }
   return pl;
 }

@@ -279,7 +279,8 @@ struct GemmArgs {
   int m_split, m_rows;
   // work split
   int tiles_m, tiles_n;
-  int splits;  // workgroups that share a tile's reduction
+  int whole;    // tiles [0, whole) have a workgroup each
+  int splits;   // workgroups that share the reduction of each tile after those
   float* part;  // their partial tiles
 };
 
@@ -395,7 +396,8 @@ struct RegOperand {
 //  along the row; the lanes past R are moved out of range when the last K
 //  tile comes up.
 //  COL: the descriptor moves down the rows, with the rows that are left as
-//  its size.
+//  its size.  Columns go up to the next multiple of 8 (what a padded copy
+//  holds as zeros; other operands have no more columns than that).
 template <int W, bool COL, bool TWO>
 struct DmaOperand {
   typedef LdsTile<W, COL> Tile;
@@ -436,7 +438,7 @@ struct DmaOperand {
       p2 = ptr2;
       ldb = l * 2;
       o0 = o;
-      extent = ext;
+      extent = (ext + 7) & ~7;
       r_split = split;
       r_rows = rows;
 #pragma unroll
@@ -558,14 +560,26 @@ struct Epilogue {
   }
 };
 
-// A reduction split between workgroups: each leaves its accumulators in lane
+// A reduction split between workgroups (of every tile, or of those that are
+// left when the others have filled the card a whole number of times): each leaves its accumulators in lane
 // order, and a second launch adds them in split order and runs the epilogue.
 // (Joined in the same launch by the last workgroup to arrive, every arrival
 // writes its XCD's L2 back and every join drops it: 256 x 4096 x 4096 on
 // 64 x 64 tiles in two splits took 51 us so, against 23 unsplit.)
 template <int NQ>
 __device__ __forceinline__ f32x4* partial(const GemmArgs& p, int tile, int split, int thread) {
-  return reinterpret_cast<f32x4*>(p.part) + ((long long)tile * p.splits + split) * NQ * 256 + thread;
+  return reinterpret_cast<f32x4*>(p.part) + ((long long)(tile - p.whole) * p.splits + split) * NQ * 256 + thread;
+}
+// Workgroup b's tile and split.  (One split after the other, so that the
+// workgroups of an XCD keep neighbouring tiles of one split.)
+__device__ __forceinline__ void split_of(const GemmArgs& p, int b, int& tile, int& split) {
+  tile = b;
+  split = 0;
+  if (b >= p.whole && p.splits > 1) {
+    const int rest = p.tiles_m * p.tiles_n - p.whole;
+    split = (b - p.whole) / rest;
+    tile = b - split * rest;
+  }
 }
 
 // The accumulators of a wave (FM x FN blocks, each transposed by the matrix
@@ -622,8 +636,8 @@ __global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
   typedef LdsTile<BN, BCOL> TB;
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * (TA::BYTES + TB::BYTES)];
   const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
-  const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-  int tm, tn;
+  int tile, split, tm, tn;
+  split_of(p, blockIdx.x, tile, split);
   tile_of(p, tile, tm, tn);
   constexpr int ON = GLU ? BN / 2 : BN;  // output columns of a tile
   const int m0 = tm * BM, n0 = tn * ON;
@@ -817,18 +831,15 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const int block,
   auto stA = [&](auto u) -> uint8_t* { return smem + (decltype(u)::value % RA) * TA::BYTES; };
   auto stB = [&](auto u) -> uint8_t* { return smem + RA * TA::BYTES + (decltype(u)::value % RB) * TB::BYTES; };
   const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
-  int tile = block, split = 0;
-  if (p.splits > 1) {
-    tile = block / p.splits;
-    split = block - tile * p.splits;
-  }
-  int tm, tn;
+  int tile, split, tm, tn;
+  split_of(p, block, tile, split);
+  const bool shared = p.splits > 1 && tile >= p.whole;
   tile_of(p, tile, tm, tn);
   constexpr int ON = GLU ? BN / 2 : BN;
   const int m0 = tm * BM, n0 = tn * ON;
   const int nk = max(1, (p.R + 63) / 64);
   int k0 = 0, k1 = nk;
-  if (p.splits > 1) {
+  if (shared) {
     k0 = (int)((long long)nk * split / p.splits);
     k1 = (int)((long long)nk * (split + 1) / p.splits);
   }
@@ -931,7 +942,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const int block,
   // loads past the last tile may still be writing LDS
   wait_vmcnt_lgkm0<0>();
   lds_barrier();
-  if (p.splits > 1) {
+  if (shared) {
     f32x4* const out = partial<FM * FN>(p, tile, split, threadIdx.x);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -978,44 +989,46 @@ __global__ void __launch_bounds__(256) colsum_kernel(const ColsumArgs p) {
 }
 
 // Both backward products on one tile size, and the column sums, in one
-// launch: workgroups [0, x_blocks) work on dX, [x_pad, x_pad + w_blocks) on dW
-// (x_pad: a multiple of 8, so that dW's tiles keep their XCDs), the rest on the
-// sums.  What one leaves of the last round of compute units the next fills.
+// launch: the product with the longer workgroups first (x_first: dX), then, at
+// a multiple of 8 so that its tiles keep their XCDs, the other, then the sums.
+// What one leaves of the last round of compute units the next fills.
 template <bool BF, int BM, int BN, int DEPTH>
 __global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH))
-    gemm_back_kernel(const GemmArgs px, const GemmArgs pw, const ColsumArgs ps, int x_blocks, int x_pad, int w_blocks) {
+    gemm_back_kernel(const GemmArgs px, const GemmArgs pw, const ColsumArgs ps, int x_first, int first, int second) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[tile_lds(BM, BN, DEPTH)];
-  const int b = blockIdx.x;
-  if (b < x_pad) {
-    if (b < x_blocks) tile_product<BF, M_DX, BM, BN, DEPTH>(px, b, smem);
-  } else if (b < x_pad + w_blocks) {
-    tile_product<BF, M_DW, BM, BN, DEPTH>(pw, b - x_pad, smem);
+  const int pad = (first + 7) & ~7, b = blockIdx.x;
+  if (b >= pad + second) {
+    colsum(ps, b - pad - second, reinterpret_cast<float*>(smem));
+  } else if ((b < pad) == (x_first != 0)) {
+    if (b < first || b >= pad) tile_product<BF, M_DX, BM, BN, DEPTH>(px, b < pad ? b : b - pad, smem);
   } else {
-    colsum(ps, b - x_pad - w_blocks, reinterpret_cast<float*>(smem));
+    if (b < first || b >= pad) tile_product<BF, M_DW, BM, BN, DEPTH>(pw, b < pad ? b : b - pad, smem);
   }
 }
 
-// The second launch of a split reduction: one wave for each wave of a tile.
+// The second launch of a split reduction: one wave for each block row of each
+// wave of a tile (one wave for all its block rows keeps too little in flight:
+// 16 tiles of 256 x 256 in two splits 30 us).
+constexpr int join_waves(int bm) { return 4 * (bm / 2 / 16); }  // per tile
 template <bool BF, int MODE, int BM, int BN>
 __global__ void __launch_bounds__(64) gemm_join_kernel(const GemmArgs p) {
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   constexpr int ON = MODE == M_GLU ? BN / 2 : BN;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[(FM > 4 ? FM / 2 : FM) * 16 * TN * 4];
-  const int tile = blockIdx.x >> 2, wave = blockIdx.x & 3, wm = wave >> 1, wn = wave & 1;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[16 * TN * 4];
+  const int tile = p.whole + blockIdx.x / (4 * FM), rest = blockIdx.x % (4 * FM);
+  const int wave = rest / FM, i = rest % FM, wm = wave >> 1, wn = wave & 1;
   int tm, tn;
   tile_of(p, tile, tm, tn);
-  f32x4 acc[FM][FN];
+  f32x4 acc[1][FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) acc[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
-    const f32x4* const in = partial<FM * FN>(p, tile, s, wave * 64 + threadIdx.x);
+    const f32x4* const in = partial<FM * FN>(p, tile, s, wave * 64 + threadIdx.x) + (long long)i * FN * 256;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const f32x4 v = in[(i * FN + j) * 256];
-        acc[i][j] = s == 0 ? v : acc[i][j] + v;
-      }
+    for (int j = 0; j < FN; ++j) acc[0][j] += in[j * 256];
   }
-  write_out<BF, MODE, FM, FN, sizeof(smem)>(p, acc, smem, tm * BM + wm * TM, tn * ON + wn * (ON / 2));
+  write_out<BF, MODE, 1, FN, sizeof(smem)>(p, acc, smem, tm * BM + wm * TM + i * 16, tn * ON + wn * (ON / 2));
 }
 
 // ---------------------------------------------------------------------------
@@ -1031,19 +1044,67 @@ struct ActBackArgs {
   int width;       // N rounded up to a multiple of 64; columns past N are written as zeros
   float* sums;     // out (NULL: none): column sums of each row block, [row blocks][1 or 2][width]
   int rows;        // rows per block
+  int groups, blocks;  // workgroups across the columns and down the rows
 };
+
+// Rows of any alignment and at least 8 elements, copied into rows of whole
+// 16-byte chunks (zeros past the end) so that the product can load them
+// straight into LDS.  One thread takes four chunks; a row's last chunk is
+// loaded as the row's last 8 elements and shifted, so that no lane branches
+// between the loads.  Bound by memory.
+constexpr int PAD_MOST = 3;  // operands per launch
+struct PadArgs {
+  int count;
+  const uint8_t* src[PAD_MOST];
+  long long ld[PAD_MOST];   // bytes
+  int cols[PAD_MOST];
+  uint32_t chunks[PAD_MOST];  // rows x chunks per row
+  uint8_t* dst[PAD_MOST];
+  int first[PAD_MOST + 1];  // first workgroup of each operand; [count]: all of them
+};
+__device__ __forceinline__ void pad_rows(const PadArgs& p, int block) {
+  int op = 0;
+  while (op + 1 < p.count && block >= p.first[op + 1]) ++op;
+  const uint8_t* const src = p.src[op];
+  const long long ld = p.ld[op];
+  const int cols = p.cols[op];
+  const uint32_t per = (uint32_t)(cols + 7) / 8, end = p.chunks[op];
+  const uint32_t i0 = (uint32_t)(block - p.first[op]) * 1024 + threadIdx.x;
+  unsigned __int128 v[4];
+  int back[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t i = min(i0 + 256 * j, end - 1), row = i / per, c = (i - row * per) * 8;
+    back[j] = max((int)c + 8 - cols, 0);
+    __builtin_memcpy(&v[j], src + row * ld + (long long)((int)c - back[j]) * 2, 16);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] >>= 16 * back[j];
+    if (i0 + 256 * j < end) __builtin_memcpy(p.dst[op] + (long long)(i0 + 256 * j) * 16, &v[j], 16);
+  }
+}
+template <int NONE = 0>
+__global__ void __launch_bounds__(256) pad_kernel(const PadArgs p) {
+  pad_rows(p, blockIdx.x);
+}
+
 // A workgroup covers 512 columns (8 per lane) x `rows` rows; its four waves
 // take rows in turn, UR at a time so that their loads fly together.  Streams
 // its inputs once: bound by memory (4096 x 8192 with gelu: 201 MB in 42 us;
-// the gated block at 4096 x 10944: 448 MB in 81 us).
+// the gated block at 4096 x 10944: 448 MB in 81 us).  Workgroups past its own
+// pad the operands of the products that follow.
 template <bool BF, bool GLU>
-__global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p) {
+__global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p, const PadArgs pad) {
   constexpr int UR = GLU ? 2 : 4;
   __shared__ float part[GLU ? 2 : 1][4][512];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const int c = blockIdx.x * 512 + lane * 8;
+  const int act_blocks = p.groups * p.blocks;
+  if ((int)blockIdx.x >= act_blocks) return pad_rows(pad, blockIdx.x - act_blocks);
+  const int by = blockIdx.x / p.groups, bx = blockIdx.x - by * p.groups;
+  const int c = bx * 512 + lane * 8;
   const int left = p.N - c;
-  const int r0 = blockIdx.y * p.rows, r1 = min(p.M, r0 + p.rows);
+  const int r0 = by * p.rows, r1 = min(p.M, r0 + p.rows);
   float s1[8], s2[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s1[e] = s2[e] = 0.0f;
@@ -1106,9 +1167,9 @@ __global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p) {
   __syncthreads();
   constexpr int NP = GLU ? 2 : 1;
   for (int i = threadIdx.x; i < NP * 512; i += 256) {
-    const int which = i / 512, cc = i % 512, col = blockIdx.x * 512 + cc;
+    const int which = i / 512, cc = i % 512, col = bx * 512 + cc;
     if (col < p.width)
-      p.sums[((long long)blockIdx.y * NP + which) * p.width + col] =
+      p.sums[((long long)by * NP + which) * p.width + col] =
           (part[which][0][cc] + part[which][1][cc]) + (part[which][2][cc] + part[which][3][cc]);
   }
 }

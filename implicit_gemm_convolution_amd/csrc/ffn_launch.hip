@@ -13,9 +13,13 @@ void launch_skinny(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
     hipLaunchKernelGGL((igc_ffn::gemm_skinny_kernel<BF, MODE, MB, 1, 16>), dim3((unsigned)pl.tiles_n), dim3(1024), 0, stream, a);
 }
 
+inline dim3 join_grid(const Plan& pl, int bm) {
+  return dim3((unsigned)(((long long)pl.tiles_m * pl.tiles_n - pl.whole) * igc_ffn::join_waves(bm)));
+}
+
 template <bool BF, int MODE>
 int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t stream) {
-  const long long grid = (long long)pl.tiles_m * pl.tiles_n * pl.splits;
+  const long long grid = workgroups(pl);
   if (grid == 0) return IGC_OK;
   if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many tiles (%lld)", grid);
   constexpr int BN64 = MODE == igc_ffn::M_GLU ? 128 : 64;
@@ -31,11 +35,12 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
     }
   }
   const dim3 g((unsigned)grid), t(256);
-  const dim3 gj((unsigned)(pl.tiles_m * pl.tiles_n * 4)), tj(64);
+  const dim3 tj(64);
 #define IGC_FFN_TILE(kernel, BM, BN, ...)                                                                       \
   do {                                                                                                          \
     hipLaunchKernelGGL((igc_ffn::kernel<BF, MODE, BM, BN, ##__VA_ARGS__>), g, t, 0, stream, a);                  \
-    if (pl.splits > 1) hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, MODE, BM, BN>), gj, tj, 0, stream, a);  \
+    if (pl.splits > 1)                                                                                          \
+      hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, MODE, BM, BN>), join_grid(pl, BM), tj, 0, stream, a);    \
   } while (0)
   switch (pl.variant) {
     case P_TILE_256: IGC_FFN_TILE(gemm_tile_kernel, 256, 256, 2); break;
@@ -52,16 +57,21 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
 template <bool BF>
 int launch_back(const igc_ffn::GemmArgs& x, const Plan& px, const igc_ffn::GemmArgs& w, const Plan& pw, const igc_ffn::ColsumArgs& s,
                 hipStream_t stream) {
-  const long long nx = (long long)px.tiles_m * px.tiles_n * px.splits, nw = (long long)pw.tiles_m * pw.tiles_n * pw.splits;
-  const long long pad = ceil_div(nx, 8) * 8, grid = pad + nw + colsum_groups(s);
+  const long long nx = workgroups(px), nw = workgroups(pw);
+  // K tiles of the longest workgroup of each
+  const long long kx = k_tiles(x.R) / (px.whole ? 1 : px.splits), kw = k_tiles(w.R) / (pw.whole ? 1 : pw.splits);
+  const bool x_first = kx >= kw;
+  const long long first = x_first ? nx : nw, second = x_first ? nw : nx;
+  const long long grid = ceil_div(first, 8) * 8 + second + colsum_groups(s);
   if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many tiles (%lld)", grid);
   const dim3 g((unsigned)grid), t(256), tj(64);
-  const dim3 gx((unsigned)(px.tiles_m * px.tiles_n * 4)), gw((unsigned)(pw.tiles_m * pw.tiles_n * 4));
 #define IGC_FFN_BACK(BM, BN, DEPTH)                                                                                            \
   do {                                                                                                                         \
-    hipLaunchKernelGGL((igc_ffn::gemm_back_kernel<BF, BM, BN, DEPTH>), g, t, 0, stream, x, w, s, (int)nx, (int)pad, (int)nw);     \
-    if (px.splits > 1) hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, igc_ffn::M_DX, BM, BN>), gx, tj, 0, stream, x);         \
-    if (pw.splits > 1) hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, igc_ffn::M_DW, BM, BN>), gw, tj, 0, stream, w);         \
+    hipLaunchKernelGGL((igc_ffn::gemm_back_kernel<BF, BM, BN, DEPTH>), g, t, 0, stream, x, w, s, (int)x_first, (int)first, (int)second); \
+    if (px.splits > 1)                                                                                                         \
+      hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, igc_ffn::M_DX, BM, BN>), join_grid(px, BM), tj, 0, stream, x);         \
+    if (pw.splits > 1)                                                                                                         \
+      hipLaunchKernelGGL((igc_ffn::gemm_join_kernel<BF, igc_ffn::M_DW, BM, BN>), join_grid(pw, BM), tj, 0, stream, w);         \
   } while (0)
   switch (px.variant) {
     case P_TILE_256: IGC_FFN_BACK(256, 256, 2); break;

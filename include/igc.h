@@ -331,11 +331,12 @@ int conv2d_u8i8_zp_workspace_size(int Nb, int H, int W, int C, int Kout, int R, 
  *  - Matrices are row-major with any leading dimension >= their row length
  *    and any alignment their element type allows.  16-byte aligned operands
  *    with leading dimensions and row lengths that are multiples of 8 take
- *    the fast path.
+ *    the fast path; others are first copied into padded rows of the
+ *    workspace where the product is large enough to gain by it.
  *  - Workspace.  <entry>_workspace_size() returns the bytes that the call
- *    described needs on the current device (`workspace` and `ws_bytes` are
- *    not read).  Forward calls may go without one (NULL: the reduction is
- *    then never split); backward calls and grad_clip need theirs when it
+ *    described (its sizes, leading dimensions and addresses) needs on the
+ *    current device (`workspace` and `ws_bytes` are not read).  Forward calls may go without one (NULL: the reduction is
+ *    then never split and no row padded); backward calls and grad_clip need theirs when it
  *    is not 0.  It is 256-byte aligned; what it holds before and after a call
  *    does not matter, so calls of any kind and size may take turns with one
  *    workspace on one stream (the entry points above want theirs zeroed).

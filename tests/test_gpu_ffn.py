@@ -320,6 +320,50 @@ def test_glu_backward(torch, igc, ws, size, kind):
         _glu_backward(torch, igc, ws, size, kind, ACTS[(i + j) % 6], want, seed=i)
 
 
+# Outputs (rows, columns) and reductions that take each tile, whole, in splits,
+# and with the last round of tiles in splits.
+PRODUCTS = [(136, 10960, 72), (72, 4280, 3520), (4632, 1696, 840), (912, 12344, 336), (392, 8208, 3336), (1440, 11224, 1384), (72, 208, 1448)]
+PRODUCTS_GLU = [(72, 2384, 3424), (280, 11312, 1176), (424, 12488, 408), (136, 2704, 14288), (1464, 5464, 1296), (72, 8208, 2456), (72, 208, 840)]
+# Rows that the direct loads do not take: odd lengths, and a start off the 16 bytes.
+UNALIGNED = [(200, 1000, 2049, 0, 0), (727, 1345, 1531, 0, 0), (300, 1001, 2001, 2, 1), (1000, 1500, 1500, 0, 4), (520, 2000, 1000, 8, 1),
+             (96, 999, 1601, 0, 0), (2100, 1300, 260, 0, 2), (70, 2049, 2047, 3, 0)]
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("size", PRODUCTS, ids=str)
+def test_linear_products(torch, igc, ws, size, kind):
+    m, n, r = size
+    _linear_forward(torch, igc, ws, (m, n, r, 0, 0), kind, "silu", True, True, True, "f32" if kind == "f16" else kind)
+    _linear_backward(torch, igc, ws, (m, r, n, 0, 0), kind, "relu", "x")
+    _linear_backward(torch, igc, ws, (r, m, n, 0, 0), kind, "none", "w")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("size", PRODUCTS_GLU, ids=str)
+def test_glu_products(torch, igc, ws, size, kind):
+    m, n, r = size
+    _glu(torch, igc, ws, (m, n, r, 0, 0), kind, "silu", True, True)
+
+
+@pytest.mark.parametrize("size", [(520, 4104, 1024), (632, 4096, 2432), (1000, 8192, 1000), (40, 8192, 1024), (4104, 520, 1032)], ids=str)
+def test_both_products_of_a_layer(torch, igc, ws, size):
+    _linear_backward(torch, igc, ws, size + (0, 0), "bf16", "gelu", "xwb")
+    _linear_backward(torch, igc, ws, size + (0, 0), "f16", "none", "xw")
+    _glu_backward(torch, igc, ws, size + (0, 0), "f16", "silu", "xgub")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("size", UNALIGNED, ids=str)
+def test_rows_that_are_padded(torch, igc, ws, size, kind):
+    _linear_forward(torch, igc, ws, size, kind, "gelu", True, True, True, "f32")
+    _glu(torch, igc, ws, size, kind, "silu", True, True)
+    _linear_backward(torch, igc, ws, size, kind, "none", "xw")
+    _linear_backward(torch, igc, ws, size, kind, "none", "x")
+    _linear_backward(torch, igc, ws, size, kind, "silu", "xwb")
+    _glu_backward(torch, igc, ws, size, kind, "silu", "xgubc")
+    _glu_backward(torch, igc, ws, size, kind, "gelu", "u")
+
+
 def test_empty_batch_sets_weight_gradients_to_zero(torch, igc, ws):
     dW, db = torch.full((24, 16), float("nan"), dtype=torch.bfloat16, device="cuda"), torch.full((24,), float("nan"), device="cuda")
     igc.linear_backward(0, 24, 16, None, 24, Z=None, ldz=24, X=None, ldx=16, dW=dW, lddw=16, dbias=db, act=igc.IGC_ACT_SILU, workspace=ws)
