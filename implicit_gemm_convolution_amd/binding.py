@@ -7,15 +7,16 @@ a raw ``hipStream_t`` (int) or a ``torch.cuda.Stream``.  When no stream is
 given, torch's current stream is used if torch is loaded, else the null
 stream.
 
+The feed-forward entry points fill their descriptors in a small extension
+module (``_marshal``, csrc/marshal.cpp) where torch is installed.
+
 The library must already be built (``python -m implicit_gemm_convolution_amd.build``
 or ``__graft_entry__.build()``); a missing library raises, there is no
 fallback path.
 """
 from __future__ import annotations
 
-import array
 import ctypes
-import operator
 import os
 import sys
 
@@ -111,6 +112,13 @@ class GradClip(ctypes.Structure):
     _fields_ = _fields("count:i grads:p outs:p sizes:p types:p max_norm:f norm:p workspace:p ws_bytes:z")
 
 
+# The entry points that take a descriptor: its structure, and for _marshal
+# its fields before the workspace.
+_DESCRIPTORS = {"linear_forward": LinearForward, "linear_backward": LinearBackward, "glu_forward": GluForward,
+                "glu_backward": GluBackward, "grad_clip": GradClip}
+_FORMATS = {name: "".join("i" if kind is ctypes.c_int else "p" for _, kind in desc._fields_[:-2])
+            for name, desc in _DESCRIPTORS.items()}
+
 _lib = None
 
 
@@ -151,8 +159,7 @@ def load() -> ctypes.CDLL:
         getattr(L, name).restype = i
     L.u8i8_colsum.argtypes = [i, i, p, i, p, p]
     L.u8i8_colsum.restype = i
-    for name, desc in (("linear_forward", LinearForward), ("linear_backward", LinearBackward),
-                       ("glu_forward", GluForward), ("glu_backward", GluBackward), ("grad_clip", GradClip)):
+    for name, desc in _DESCRIPTORS.items():
         getattr(L, name).argtypes = [ctypes.POINTER(desc), p]
         getattr(L, name).restype = i
         getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(desc), pz]
@@ -340,136 +347,121 @@ def conv2d_u8i8_zp(Nb, H, W, C, Kout, R, S, stride_h, stride_w, pad_h, pad_w, x,
 # arguments (but for workspace and stream) and returns the bytes that the
 # call needs.
 # ---------------------------------------------------------------------------
-def _linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, type, act, y_type, bias, R, ldr, Z, ldz, workspace, ws_bytes):
-    return LinearForward(M, N, K, type, act, type if y_type is None else y_type, _addr(X), ldx, _addr(W), ldw, _addr(bias),
-                         _addr(R), ldr, _addr(Y), ldy, _addr(Z), ldz, _addr(workspace), _ws_bytes(workspace, ws_bytes))
+_native = None   # the _marshal module; False without torch
+_entries = None  # (the library, addresses of its entry points)
+
+
+def _marshal():
+    global _native
+    if _native is None:
+        load()
+        try:
+            import torch  # noqa: F401
+        except ImportError:
+            _native = False
+        else:
+            from . import _marshal as native
+            _native = native
+    return _native
+
+
+def _entry(name) -> int:
+    """An entry point's address."""
+    global _entries
+    L = load()
+    if _entries is None or _entries[0] is not L:
+        _entries = L, {n + q: ctypes.cast(getattr(L, n + q), ctypes.c_void_p).value
+                       for n in _DESCRIPTORS for q in ("", "_workspace_size")}
+    return _entries[1][name]
+
+
+def _describe(name, fields, workspace, ws_bytes):
+    """The entry point's descriptor."""
+    values = [_addr(v) if kind == "p" else v for kind, v in zip(_FORMATS[name], fields)]
+    return _DESCRIPTORS[name](*values, _addr(workspace), _ws_bytes(workspace, ws_bytes))
+
+
+def _call(name, check, stream, workspace, ws_bytes, *fields) -> int:
+    native = _native if _native is not None else _marshal()
+    if native:
+        st = native.call(_entry(name), _FORMATS[name], _stream(stream), workspace, ws_bytes, *fields)
+    else:
+        st = getattr(load(), name)(_describe(name, fields, workspace, ws_bytes), _stream(stream))
+    return _check(st, name) if check else st
+
+
+def _query(name, *fields) -> int:
+    return _ws_query(name + "_workspace_size", _describe(name, fields, None, 0))
 
 
 def linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, *, type=IGC_BF16, act=IGC_ACT_NONE, y_type=None, bias=None, R=None, ldr=0,
                    Z=None, ldz=0, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
     """Z = X W^T + bias; Y = act(Z) + R (y_type None: the operands' type)."""
-    d = _linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, type, act, y_type, bias, R, ldr, Z, ldz, workspace, ws_bytes)
-    st = load().linear_forward(d, _stream(stream))
-    return _check(st, "linear_forward") if check else st
+    return _call("linear_forward", check, stream, workspace, ws_bytes,
+                 M, N, K, type, act, type if y_type is None else y_type, X, ldx, W, ldw, bias, R, ldr, Y, ldy, Z, ldz)
 
 
 def linear_forward_workspace_size(M, N, K, X, ldx, W, ldw, Y, ldy, *, type=IGC_BF16, act=IGC_ACT_NONE, y_type=None, bias=None,
                                   R=None, ldr=0, Z=None, ldz=0) -> int:
-    return _ws_query("linear_forward_workspace_size",
-                     _linear_forward(M, N, K, X, ldx, W, ldw, Y, ldy, type, act, y_type, bias, R, ldr, Z, ldz, None, 0))
-
-
-def _linear_backward(M, N, K, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias, type, act, workspace, ws_bytes):
-    return LinearBackward(M, N, K, type, act, _addr(dY), lddy, _addr(Z), ldz, _addr(X), ldx, _addr(W), ldw, _addr(dX), lddx,
-                          _addr(dW), lddw, _addr(dbias), _addr(workspace), _ws_bytes(workspace, ws_bytes))
+    return _query("linear_forward", M, N, K, type, act, type if y_type is None else y_type, X, ldx, W, ldw, bias, R, ldr,
+                  Y, ldy, Z, ldz)
 
 
 def linear_backward(M, N, K, dY, lddy, *, Z=None, ldz=0, X=None, ldx=0, W=None, ldw=0, dX=None, lddx=0, dW=None, lddw=0,
                     dbias=None, type=IGC_BF16, act=IGC_ACT_NONE, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
     """D = dY act'(Z); dX = D W; dW = D^T X; dbias = column sums of D (any subset)."""
-    d = _linear_backward(M, N, K, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias, type, act, workspace, ws_bytes)
-    st = load().linear_backward(d, _stream(stream))
-    return _check(st, "linear_backward") if check else st
+    return _call("linear_backward", check, stream, workspace, ws_bytes,
+                 M, N, K, type, act, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias)
 
 
 def linear_backward_workspace_size(M, N, K, dY, lddy, *, Z=None, ldz=0, X=None, ldx=0, W=None, ldw=0, dX=None, lddx=0, dW=None,
                                    lddw=0, dbias=None, type=IGC_BF16, act=IGC_ACT_NONE) -> int:
-    return _ws_query("linear_backward_workspace_size",
-                     _linear_backward(M, N, K, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias, type, act, None, 0))
-
-
-def _glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, bias_g, bias_u, G, ldg, U, ldu, type, act, workspace, ws_bytes):
-    return GluForward(M, N, K, type, act, _addr(X), ldx, _addr(Wg), ldwg, _addr(Wu), ldwu, _addr(bias_g), _addr(bias_u),
-                      _addr(H), ldh, _addr(G), ldg, _addr(U), ldu, _addr(workspace), _ws_bytes(workspace, ws_bytes))
+    return _query("linear_backward", M, N, K, type, act, dY, lddy, Z, ldz, X, ldx, W, ldw, dX, lddx, dW, lddw, dbias)
 
 
 def glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, *, bias_g=None, bias_u=None, G=None, ldg=0, U=None, ldu=0,
                 type=IGC_BF16, act=IGC_ACT_SILU, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
     """G = X Wg^T + bias_g; U = X Wu^T + bias_u; H = act(G) U."""
-    d = _glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, bias_g, bias_u, G, ldg, U, ldu, type, act, workspace, ws_bytes)
-    st = load().glu_forward(d, _stream(stream))
-    return _check(st, "glu_forward") if check else st
+    return _call("glu_forward", check, stream, workspace, ws_bytes,
+                 M, N, K, type, act, X, ldx, Wg, ldwg, Wu, ldwu, bias_g, bias_u, H, ldh, G, ldg, U, ldu)
 
 
 def glu_forward_workspace_size(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, *, bias_g=None, bias_u=None, G=None, ldg=0, U=None,
                                ldu=0, type=IGC_BF16, act=IGC_ACT_SILU) -> int:
-    return _ws_query("glu_forward_workspace_size",
-                     _glu_forward(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, bias_g, bias_u, G, ldg, U, ldu, type, act, None, 0))
-
-
-def _glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg, dWu, lddwu, dbias_g,
-                  dbias_u, type, act, workspace, ws_bytes):
-    return GluBackward(M, N, K, type, act, _addr(dH), lddh, _addr(G), ldg, _addr(U), ldu, _addr(X), ldx, _addr(Wg), ldwg,
-                       _addr(Wu), ldwu, _addr(dX), lddx, _addr(dWg), lddwg, _addr(dWu), lddwu, _addr(dbias_g), _addr(dbias_u),
-                       _addr(workspace), _ws_bytes(workspace, ws_bytes))
+    return _query("glu_forward", M, N, K, type, act, X, ldx, Wg, ldwg, Wu, ldwu, bias_g, bias_u, H, ldh, G, ldg, U, ldu)
 
 
 def glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, *, X=None, ldx=0, Wg=None, ldwg=0, Wu=None, ldwu=0, dX=None, lddx=0,
                  dWg=None, lddwg=0, dWu=None, lddwu=0, dbias_g=None, dbias_u=None, type=IGC_BF16, act=IGC_ACT_SILU,
                  stream=None, workspace=None, ws_bytes=None, check=True) -> int:
     """dU = dH act(G), dG = dH U act'(G); dX = dG Wg + dU Wu; dW* = d*^T X; dbias_* = column sums (any subset)."""
-    d = _glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg, dWu, lddwu, dbias_g,
-                      dbias_u, type, act, workspace, ws_bytes)
-    st = load().glu_backward(d, _stream(stream))
-    return _check(st, "glu_backward") if check else st
+    return _call("glu_backward", check, stream, workspace, ws_bytes,
+                 M, N, K, type, act, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg, dWu, lddwu,
+                 dbias_g, dbias_u)
 
 
 def glu_backward_workspace_size(M, N, K, dH, lddh, G, ldg, U, ldu, *, X=None, ldx=0, Wg=None, ldwg=0, Wu=None, ldwu=0, dX=None,
                                 lddx=0, dWg=None, lddwg=0, dWu=None, lddwu=0, dbias_g=None, dbias_u=None, type=IGC_BF16,
                                 act=IGC_ACT_SILU) -> int:
-    return _ws_query("glu_backward_workspace_size",
-                     _glu_backward(M, N, K, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg, dWu,
-                                   lddwu, dbias_g, dbias_u, type, act, None, 0))
+    return _query("glu_backward", M, N, K, type, act, dH, lddh, G, ldg, U, ldu, X, ldx, Wg, ldwg, Wu, ldwu, dX, lddx, dWg, lddwg,
+                  dWu, lddwu, dbias_g, dbias_u)
 
 
-_DTYPES = {}  # torch's dtypes, filled at the first call
-
-
-def _tensor_types(dtypes):
-    if not _DTYPES:
-        import torch
-
-        _DTYPES.update({torch.float16: IGC_F16, torch.bfloat16: IGC_BF16, torch.float32: IGC_F32})
-    try:
-        return array.array("i", [_DTYPES[t] for t in dtypes])
-    except KeyError as e:
-        raise TypeError(f"grad_clip takes float16, bfloat16 and float32 tensors, not {e.args[0]}") from None
-
-
-_dtype = operator.attrgetter("dtype")
-
-
-def _grad_clip(grads, max_norm, norm, out, workspace, ws_bytes):
-    # (a model has hundreds of gradients: one C-level pass per property)
-    from torch import Tensor
-
-    _contiguous, _numel, _data_ptr = Tensor.is_contiguous, Tensor.numel, Tensor.data_ptr
-    n = len(grads)
-    if out is not None and len(out) != n:
-        raise ValueError(f"{n} gradients but {len(out)} outputs")
-    if not all(map(_contiguous, grads)) or (out is not None and not all(map(_contiguous, out))):
-        raise ValueError("grad_clip takes contiguous tensors")
-    dtypes, sizes = list(map(_dtype, grads)), array.array("q", map(_numel, grads))
-    if out is not None and (dtypes != list(map(_dtype, out)) or sizes != array.array("q", map(_numel, out))):
-        raise ValueError("an output differs from its gradient in type or size")
-    types, ptrs = _tensor_types(dtypes), array.array("Q", map(_data_ptr, grads))
-    outs = None if out is None else array.array("Q", map(_data_ptr, out))
-    d = GradClip(n, ptrs.buffer_info()[0], outs and outs.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0],
-                 float(max_norm), _addr(norm), _addr(workspace), _ws_bytes(workspace, ws_bytes))
-    return d, (ptrs, outs, sizes, types)  # (the arrays live until the call returns)
+def _clip(entry, query, stream, workspace, ws_bytes, grads, out, max_norm, norm):
+    native = _marshal()
+    if not native:
+        raise RuntimeError("grad_clip takes torch tensors, and torch is not installed")
+    return native.clip(_entry(entry), query, stream, workspace, ws_bytes, grads, out, max_norm, norm)
 
 
 def grad_clip(grads, max_norm, norm, *, out=None, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
     """norm = the global norm of `grads` (contiguous fp16 / bf16 / fp32 tensors); out = grads * min(1, max_norm / (norm + 1e-6)),
     in place without `out`."""
-    d, keep = _grad_clip(grads, max_norm, norm, out, workspace, ws_bytes)
-    st = load().grad_clip(d, _stream(stream))
-    del keep
+    st = _clip("grad_clip", False, _stream(stream), workspace, ws_bytes, grads, out, max_norm, norm)
     return _check(st, "grad_clip") if check else st
 
 
 def grad_clip_workspace_size(grads, max_norm, norm, *, out=None) -> int:
-    d, keep = _grad_clip(grads, max_norm, norm, out, None, 0)
-    size = _ws_query("grad_clip_workspace_size", d)
-    del keep
+    st, size = _clip("grad_clip_workspace_size", True, None, None, None, grads, out, max_norm, norm)
+    _check(st, "grad_clip_workspace_size")
     return size

@@ -1,4 +1,5 @@
-"""Build libigc.so (the HIP kernels and the C ABI) in-tree with hipcc for gfx950.
+"""Build libigc.so (the HIP kernels and the C ABI) in-tree with hipcc for gfx950,
+and _marshal.so (the Python binding's marshalling, host code only) with g++.
 
 The C ABI (csrc/igc.hip, csrc/ffn.hip) and the kernel instantiations
 (csrc/igc_launch.hip and csrc/ffn_launch.hip, compiled once per kernel kind
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -24,6 +26,8 @@ LAUNCH_UNITS = 38  # the (kind, variant) pairs of IGC_LAUNCH_KINDS in igc_host.h
 FFN_SOURCE = os.path.join(CSRC, "ffn.hip")
 FFN_LAUNCH_SOURCE = os.path.join(CSRC, "ffn_launch.hip")
 FFN_LAUNCH_UNITS = 10  # the (type, layout) pairs of IGC_FFN_KINDS in ffn_host.hpp, and both types' joint backward launch
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 SOURCES = [ABI_SOURCE, LAUNCH_SOURCE, FFN_SOURCE, FFN_LAUNCH_SOURCE]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -59,11 +63,24 @@ def _jobs() -> int:
     return max(1, min(n, 16, LAUNCH_UNITS + 1))
 
 
+def marshal_command(out: str) -> list:
+    """The command that compiles _marshal.so against the installed Python and torch."""
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + sysconfig.get_paths()["include"],
+            *("-I" + p for p in cpp_extension.include_paths()), MARSHAL_SOURCE, "-o", out,
+            "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Compile every HIP source and link libigc.so next to this file; returns its path."""
+    """Compile every source; libigc.so and _marshal.so go next to this file.  Returns libigc.so's path."""
     tmpdir = tempfile.mkdtemp(prefix="igc_build_")
     try:
-        cmds = []
+        marshal = os.path.join(tmpdir, "_marshal.so")
+        cmds = [marshal_command(marshal)]  # (among the longest: first)
         for src, defs, obj in _units():
             cmds.append([HIPCC, *HIP_FLAGS, *extra_flags, *defs, "-c", src, "-o", os.path.join(tmpdir, obj)])
 
@@ -79,6 +96,8 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         link = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
         run(link)
         os.replace(tmp, LIB_PATH)
+        shutil.copyfile(marshal, MARSHAL_PATH + ".tmp")
+        os.replace(MARSHAL_PATH + ".tmp", MARSHAL_PATH)
     finally:
         shutil.rmtree(tmpdir, ignore_errors=True)
     return LIB_PATH
