@@ -210,8 +210,10 @@ __device__ __forceinline__ void act_one(float z, float& f, float& d) {
     f = z * c;
     if constexpr (SLOPE) d = __builtin_fmaf(z * 0.39894228040143268f, e, c);
   } else if constexpr (ACT == ACT_GELU_TANH) {
+    // (the sigmoid's exponent -2a log2(e), its constants folded)
     const float z2 = z * z;
-    const float s = sigmoid_f(2.0f * kGeluC * z * __builtin_fmaf(kGeluA, z2, 1.0f));
+    const float w = __builtin_fmaf(z2, -2.0f * kGeluC * kGeluA * 1.44269504088896341f, -2.0f * kGeluC * 1.44269504088896341f);
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * w));
     f = z * s;
     if constexpr (SLOPE) d = s + f * (1.0f - s) * (2.0f * kGeluC) * __builtin_fmaf(3.0f * kGeluA, z2, 1.0f);
   } else {
@@ -493,9 +495,9 @@ __device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& 
   tm = first + in - tn * rows;
 }
 
-// V consecutive sums of one row (`f`, and `u` of the second product) leave for
-// the outputs.
-template <bool BF, int MODE, int V>
+// U rows of V consecutive sums (`f`, and `u` of the second product) leave for
+// the outputs.  FULL: every lane has V columns.
+template <bool BF, int MODE, int V, int U, bool FULL>
 struct Epilogue {
   const GemmArgs& p;
   int col;       // this lane's first column
@@ -507,54 +509,88 @@ struct Epilogue {
     if constexpr (MODE == M_FWD || MODE == M_GLU) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        b1[e] = p.bias && e < left ? p.bias[col + e] : 0.0f;
-        b2[e] = MODE == M_GLU && p.bias2 && e < left ? p.bias2[col + e] : 0.0f;
+        b1[e] = p.bias && e < have() ? p.bias[col + e] : 0.0f;
+        b2[e] = MODE == M_GLU && p.bias2 && e < have() ? p.bias2[col + e] : 0.0f;
       }
     }
   }
-  __device__ __forceinline__ void put(uint8_t* base, long long ld, int row, const float (&f)[V]) const {
-    store_n<BF, V>(base + ((long long)row * ld + col) * 2, left, f);
+  __device__ __forceinline__ int have() const { return FULL ? V : left; }
+  // row q of the U rows
+  __device__ __forceinline__ void put(uint8_t* base, long long ld, int row, const float (&f)[U * V], int q) const {
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = f[q * V + e];
+    store_n<BF, V>(base + ((long long)row * ld + col) * 2, have(), v);
   }
-  __device__ __forceinline__ void operator()(int row, float (&f)[V], float (&u)[V]) const {
-    if (row >= p.M || left <= 0) return;
-    if constexpr (MODE == M_DX) {
-      put(p.Y, p.ldy, row, f);
-    } else if constexpr (MODE == M_DW) {
-      const bool second = row >= p.m_split;
-      const int r = second ? row - p.m_split : row;
-      uint8_t* const y = second ? p.Y2 : p.Y;  // (either may be left out)
-      if (y && r < p.m_rows) put(y, second ? p.ldy2 : p.ldy, r, f);
-    } else {
-      float y[V], unused[V];
-      if (has_bias) {
+  // rows row0, row0 + step, ...
+  __device__ __forceinline__ void operator()(int row0, int step, float (&f)[U * V], float (&u)[U * V]) const {
+    if (!FULL && left <= 0) return;
+    if constexpr (MODE == M_DX || MODE == M_DW) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[e] += b1[e];
-        if constexpr (MODE == M_GLU) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) u[e] += b2[e];
+      for (int q = 0; q < U; ++q) {
+        const int row = row0 + q * step;
+        if (row >= p.M) continue;
+        if constexpr (MODE == M_DX) {
+          put(p.Y, p.ldy, row, f, q);
+        } else {
+          const bool second = row >= p.m_split;
+          const int r = second ? row - p.m_split : row;
+          uint8_t* const y = second ? p.Y2 : p.Y;  // (either may be left out)
+          if (y && r < p.m_rows) put(y, second ? p.ldy2 : p.ldy, r, f, q);
         }
       }
-      if (p.Z) put(p.Z, p.ldz, row, f);
-      act_n<false>(p.act, f, y, unused);
-      if constexpr (MODE == M_GLU) {
-        if (p.U) put(p.U, p.ldu, row, u);
+    } else {
+      float res[U * V], y[U * V], unused[U * V];
+      if (MODE == M_FWD && p.res) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) y[e] *= u[e];
-        put(p.Y, p.ldy, row, y);
-      } else {
-        if (p.res) {
+        for (int q = 0; q < U; ++q) {
+          const int row = row0 + q * step;
+          const int n = row < p.M ? have() : 0;
           float r[V];
           if (p.y_f32)
-            load_f32(reinterpret_cast<const float*>(p.res) + (long long)row * p.ldr + col, left, r);
+            load_f32(reinterpret_cast<const float*>(p.res) + (long long)row * p.ldr + col, n, r);
           else
-            load_n<BF, V>(p.res + ((long long)row * p.ldr + col) * 2, left, r);
+            load_n<BF, V>(p.res + ((long long)row * p.ldr + col) * 2, n, r);
 #pragma unroll
-          for (int e = 0; e < V; ++e) y[e] += r[e];
+          for (int e = 0; e < V; ++e) res[q * V + e] = r[e];
         }
-        if (p.y_f32)
-          store_f32(reinterpret_cast<float*>(p.Y) + (long long)row * p.ldy + col, left, y);
-        else
-          put(p.Y, p.ldy, row, y);
+      }
+      if (has_bias) {
+#pragma unroll
+        for (int e = 0; e < U * V; ++e) f[e] += b1[e % V];
+        if constexpr (MODE == M_GLU) {
+#pragma unroll
+          for (int e = 0; e < U * V; ++e) u[e] += b2[e % V];
+        }
+      }
+      if (p.Z) {
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+          if (row0 + q * step < p.M) put(p.Z, p.ldz, row0 + q * step, f, q);
+      }
+      act_n<false>(p.act, f, y, unused);
+      if constexpr (MODE == M_GLU) {
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+          if (p.U && row0 + q * step < p.M) put(p.U, p.ldu, row0 + q * step, u, q);
+#pragma unroll
+        for (int e = 0; e < U * V; ++e) y[e] *= u[e];
+      } else if (p.res) {
+#pragma unroll
+        for (int e = 0; e < U * V; ++e) y[e] += res[e];
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const int row = row0 + q * step;
+        if (row >= p.M) continue;
+        if (MODE == M_FWD && p.y_f32) {
+          float v[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[e] = y[q * V + e];
+          store_f32(reinterpret_cast<float*>(p.Y) + (long long)row * p.ldy + col, have(), v);
+        } else {
+          put(p.Y, p.ldy, row, y, q);
+        }
       }
     }
   }
@@ -600,30 +636,46 @@ __device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[
   constexpr int XM = TN / 4 < 16 ? TN / 4 - 1 : 15;
   const int lane = threadIdx.x & 63;
   const int wr = lane & 15, rr = lane / LPR, rc = lane % LPR;
-  const Epilogue<BF, MODE, 8> out(p, col0 + rc * 8);
   auto quad = [&](int r, int q) { return r * (TN * 4) + ((q ^ (r & XM)) << 4); };  // 4 columns of a staged row
-  auto read8 = [&](int r, int c, float (&f)[8]) {
-    const uint4 a = lds_read16(lds, quad(r, c >> 2)), b = lds_read16(lds, quad(r, (c >> 2) + 1));
-    __builtin_memcpy(f, &a, 16);
-    __builtin_memcpy(f + 4, &b, 16);
-  };
-  static_for<FM / GR>([&](auto g) {
-    constexpr int G0 = decltype(g)::value * GR;
-    asm volatile("" ::: "memory");
-    static_for<GR>([&](auto i) {
-      constexpr int I = decltype(i)::value;
+  constexpr int U = GR * 16 / RPP > 1 ? 2 : 1;  // rows per lane and turn, so that their latencies overlap
+  auto turns = [&](const auto& out, int row) {
+    for (int r = rr; r < GR * 16; r += RPP * U) {
+      float f[U * 8], u[U * 8];
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        lds_write16(lds, quad(I * 16 + wr, j * 4 + (lane >> 4)), __builtin_bit_cast(uint4, acc[G0 + I][j]));
-    });
-    asm volatile("" ::: "memory");
-    for (int r = 0; r < GR * 16; r += RPP) {
-      float f[8], u[8];
-      read8(r + rr, rc * 8, f);
-      if constexpr (GLU) read8(r + rr, OUT + rc * 8, u);
-      out(row0 + G0 * 16 + r + rr, f, u);
+      for (int q = 0; q < U; ++q) {
+        const int at = r + q * RPP, c = rc * 2;
+        uint4 v = lds_read16(lds, quad(at, c));
+        __builtin_memcpy(f + q * 8, &v, 16);
+        v = lds_read16(lds, quad(at, c + 1));
+        __builtin_memcpy(f + q * 8 + 4, &v, 16);
+        if constexpr (GLU) {
+          v = lds_read16(lds, quad(at, OUT / 4 + c));
+          __builtin_memcpy(u + q * 8, &v, 16);
+          v = lds_read16(lds, quad(at, OUT / 4 + c + 1));
+          __builtin_memcpy(u + q * 8 + 4, &v, 16);
+        }
+      }
+      out(row + r, RPP, f, u);
     }
-  });
+  };
+  auto rows = [&](const auto& out) {
+    static_for<FM / GR>([&](auto g) {
+      constexpr int G0 = decltype(g)::value * GR;
+      asm volatile("" ::: "memory");
+      static_for<GR>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          lds_write16(lds, quad(I * 16 + wr, j * 4 + (lane >> 4)), __builtin_bit_cast(uint4, acc[G0 + I][j]));
+      });
+      asm volatile("" ::: "memory");
+      turns(out, row0 + G0 * 16);
+    });
+  };
+  if (col0 + OUT <= p.N)
+    rows(Epilogue<BF, MODE, 8, U, true>(p, col0 + rc * 8));
+  else
+    rows(Epilogue<BF, MODE, 8, U, false>(p, col0 + rc * 8));
 }
 
 // The simple product: K tiles go through registers into two LDS stages.
@@ -792,8 +844,8 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
       if constexpr (GLU) u4 += red[q][PB * MB + b][l];
     }
     float f[4] = {f4[0], f4[1], f4[2], f4[3]}, u[4] = {u4[0], u4[1], u4[2], u4[3]};
-    const Epilogue<BF, MODE, 4> out(p, n0 + (b / MB) * 16 + 4 * (l >> 4));
-    out((b % MB) * 16 + (l & 15), f, u);
+    const Epilogue<BF, MODE, 4, 1, false> out(p, n0 + (b / MB) * 16 + 4 * (l >> 4));
+    out((b % MB) * 16 + (l & 15), 0, f, u);
   }
 }
 
