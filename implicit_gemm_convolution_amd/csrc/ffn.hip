@@ -117,8 +117,9 @@ struct Pads {
   }
 };
 
-// What the copy takes in a launch of its own.
-inline float pad_us(const Pads& p) { return 4.0f + (float)p.moved / 5e6f; }
+// What the copy takes in a launch of its own: 5 to 6 TB/s (130 + 4096 rows of
+// 4093 11.8 us).
+inline float pad_us(const Pads& p) { return 4.0f + (float)p.moved / 5.7e6f; }
 
 // ---------------------------------------------------------------- forward
 template <int MODE>
@@ -131,18 +132,19 @@ int forward(GemmArgs& a, int type, void* ws, size_t ws_bytes, size_t* query, hip
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
   const bool may = query || ws;
-  const bool a_ok = dma_operand(a.A, a.lda, a.R), b_ok = dma_operand(a.B, a.ldb, a.R);
-  const bool b2_ok = MODE != igc_ffn::M_GLU || dma_operand(a.B2, a.ldb2, a.R);
-  Plan pl = make_plan(MODE, a.M, a.N, a.R, a_ok && b_ok && b2_ok, cus, may);
+  const int a_al = row_align(a.A, a.lda, a.R), b_al = row_align(a.B, a.ldb, a.R);
+  const int b2_al = MODE == igc_ffn::M_GLU ? row_align(a.B2, a.ldb2, a.R) : 16;
+  const bool a_ok = a_al == 16, b_ok = b_al == 16, b2_ok = b2_al == 16;
+  Plan pl = make_plan(MODE, a.M, a.N, a.R, std::min(a_al, std::min(b_al, b2_al)), cus, may);
   Pads pads;
   // Operands of another alignment are copied into padded rows where the copy
   // costs less than the faster kernel gains (bf16, us, without and with:
   // 200 x 1000 x 257 7.4 and 9.5, 727 x 1344 x 6130 65 and 39, the gated block
   // at 304 x 7200 x 5402 125 and 148, at 6900 x 2600 x 2201 260 and 170).
-  if (may && (pl.variant == P_ANY_128 || pl.variant == P_ANY_64)) {
+  if (may && !(a_ok && b_ok && b2_ok)) {
     const int ia = a_ok ? -1 : pads.add(a.A, a.lda, a.M, a.R), ib = b_ok ? -1 : pads.add(a.B, a.ldb, a.N, a.R);
     const int ib2 = b2_ok ? -1 : pads.add(a.B2, a.ldb2, a.N, a.R);
-    const Plan aligned = make_plan(MODE, a.M, a.N, Pads::padded(a.R), true, cus, may);
+    const Plan aligned = make_plan(MODE, a.M, a.N, Pads::padded(a.R), 16, cus, may);
     if (pads.possible && pad_us(pads) + aligned.us < pl.us) {
       pl = aligned;
       uint8_t* const to = static_cast<uint8_t*>(ws);
@@ -330,8 +332,8 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
       iw = iw2 = ix = -1;
     }
   }
-  Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red(), d_ok && w_ok, cus, true);
-  Plan pw = make_plan(igc_ffn::M_DW, red(), b.K, b.M, d_ok && x_ok, cus, true);
+  Plan px = make_plan(igc_ffn::M_DX, b.M, b.K, red(), d_ok && w_ok ? 16 : 2, cus, true);
+  Plan pw = make_plan(igc_ffn::M_DW, red(), b.K, b.M, d_ok && x_ok ? 16 : 2, cus, true);
   const bool joint = want_x && want_w && d_ok && w_ok && x_ok && plan_back(px, pw, b.M, b.K, red(), sums, cus);
 
   // workspace: D, column sums, padded operands, partial tiles

@@ -53,6 +53,13 @@ inline void plan_tile(int mode, int variant, int& bm, int& bn) {
   }
 }
 
+// What every row of an operand starts at a multiple of, of 2, 4 and (as below)
+// 16 bytes.
+inline bool dma_operand(const void* p, long long ld, long long length);
+inline int row_align(const void* p, long long ld, long long length) {
+  return dma_operand(p, ld, length) ? 16 : (reinterpret_cast<uintptr_t>(p) & 3u) || (ld & 1) ? 2 : 4;
+}
+
 // Operands of the direct-to-LDS loaders: 16-byte aligned rows, lengths in
 // whole 16-byte chunks (at least one), and a tile's worth of rows within a descriptor (256
 // rows below 2^30 bytes).
@@ -160,33 +167,51 @@ inline Plan any_plan(int mode, int variant, long long M, long long N, long long 
   return pl;
 }
 
-// A pure function of the problem and the device, so that the size queries and
-// the calls agree.  may_split: the call has (or the query assumes) a
-// workspace.
-inline Plan make_plan(int mode, long long M, long long N, long long R, bool aligned, int cus, bool may_split) {
+// The plan on one of the kernels for few rows (at most 64): every wave loads
+// its part of the reduction in batches, so the time goes with the reduction's
+// length and, more weakly, with the rows that share it; rows at odd multiples
+// of 2 bytes load 3.4 times as long.  bf16, us, 16 | 32 weight rows | 64-row
+// tiles: 1x4096x4096 8.5 | 11.4 | 11.0, 16x11008x4096 28 | 30 | 18,
+// 32x512x512 4.3 | 6.2 | 5.3, 32x16384x1024 16 | 11 | 8; the gated block at
+// 1x11008x4096 - | 37 | 40, 16x11008x4096 - | 46 | 41, 16x2048x1024 - | 5.7 | 7.8.
+inline Plan skinny_plan(int mode, int variant, long long M, long long N, long long R, int align, int cus) {
   Plan pl;
-  // Few rows: streaming the weights into registers beats 64-row tiles up to
-  // 16 rows (12 x 4096 x 4096 10.0 us against 11.9) and, on short reductions,
-  // up to 32 (24x2048x1024 5.1 against 6.3; 32 x 4096 x 4096 14.0 against
-  // 12.3).  Rows of any alignment have no better kernel up to 64.
-  if ((mode == igc_ffn::M_FWD || mode == igc_ffn::M_GLU) && (M <= 16 || (M <= 32 && R <= 1024) || (M <= 64 && !aligned))) {
-    // 32 weight rows share the loads of X; 16 where there would be too few workgroups
-    pl.variant = mode == igc_ffn::M_GLU || N >= 32LL * cus ? P_SKINNY_32 : P_SKINNY_16;
-    pl.tiles_m = 1;
-    pl.tiles_n = (int)ceil_div(N, pl.variant == P_SKINNY_32 && mode == igc_ffn::M_FWD ? 32 : 16);
-    return pl;
+  const bool two = variant == P_SKINNY_32, glu = mode == igc_ffn::M_GLU;
+  pl.variant = variant;
+  pl.tiles_m = 1;
+  pl.tiles_n = (int)ceil_div(N, two && !glu ? 32 : 16);
+  const float per_k = ((two ? 1.8f : 0.9f) + 0.05f * (float)M) * (align < 4 ? 3.4f : 1.0f);  // us per 1024 of the reduction
+  const float fill = (float)pl.tiles_n / (float)cus * (!two ? 1.3f : glu ? 1.45f : 1.5f) - (two ? 0.0f : 0.15f);
+  const float each = two ? 0.0f : 0.5f;  // joining sixteen waves' sums instead of eight
+  const float run = (per_k * (float)R / 1024.0f + each) * std::max(1.0f, fill) - each;
+  pl.us = 3.6f + std::max(run, (float)N * (float)R * (glu ? 4.0f : 2.0f) / 5.2e6f + 0.05f * run);  // (the weights, once)
+  return pl;
+}
+
+// A pure function of the problem and the device, so that the size queries and
+// the calls agree.  align: the bytes (2, 4 or 16) that every row of the
+// operands starts at a multiple of; may_split: the call has (or the query
+// assumes) a workspace.
+inline Plan make_plan(int mode, long long M, long long N, long long R, int align, int cus, bool may_split) {
+  Plan pl;
+  auto take = [&](const Plan& q) {
+    if (pl.tiles_m == 0 || q.us < pl.us) pl = q;
+  };
+  if ((mode == igc_ffn::M_FWD || mode == igc_ffn::M_GLU) && M <= 64) {
+    if (mode == igc_ffn::M_FWD) take(skinny_plan(mode, P_SKINNY_16, M, N, R, align, cus));
+    take(skinny_plan(mode, P_SKINNY_32, M, N, R, align, cus));
   }
-  if (aligned) {
+  if (align == 16) {
+    // (streaming the operands, no faster than 5 TB/s)
+    const float least = 4.5f + ((float)M + (float)N * (mode == igc_ffn::M_GLU ? 2.0f : 1.0f)) * (float)R * 2.0f / 5e6f;
     for (int v = P_TILE_256; v <= P_TILE_64; ++v) {
-      const Plan q = best_split(mode, v, M, N, R, cus, may_split);
-      if (v == P_TILE_256 || q.us < pl.us) pl = q;
+      Plan q = best_split(mode, v, M, N, R, cus, may_split);
+      if (M <= 64) q.us = std::max(q.us, least + 0.05f * q.us);  // (the faster tile still comes first)
+      take(q);
     }
     return pl;
   }
-  for (int v = P_ANY_128; v <= P_ANY_64; ++v) {
-    const Plan q = any_plan(mode, v, M, N, R, cus, may_split);
-    if (v == P_ANY_128 || q.us < pl.us) pl = q;
-  }
+  for (int v = P_ANY_128; v <= P_ANY_64; ++v) take(any_plan(mode, v, M, N, R, cus, may_split));
   return pl;
 }
 
