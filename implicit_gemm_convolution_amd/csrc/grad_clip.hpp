@@ -36,25 +36,42 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// Runs f(tensor, first element, elements) for every chunk of this workgroup.
-// REVERSE: from the last chunk to the first, so that the second pass begins
-// with what the first one read last and the memory-side cache (256 MB) still
-// holds.
+// Lane i of every wave holds tensor i of the table, so that all of it is on its
+// way at once (looked up entry by entry, each dependent read of the arguments
+// waits for host memory).
+struct ClipEntry {
+  uint64_t in, out;
+  long long size;
+  int first, type;
+  __device__ __forceinline__ explicit ClipEntry(const ClipTable& p) {
+    static_assert(CLIP_TENSORS == 64, "a tensor for each lane");
+    const int i = threadIdx.x & 63, t = min(i, max(p.count - 1, 0));
+    in = reinterpret_cast<uint64_t>(p.in[t]);
+    out = reinterpret_cast<uint64_t>(p.out[t]);
+    size = p.size[t];
+    type = p.type[t];
+    first = i < p.count ? p.first[t] : 0x7fffffff;
+  }
+};
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// Runs f(in, out, type, first element, elements) for every chunk of this
+// workgroup.  REVERSE: from the last chunk to the first, so that the second
+// pass begins with what the first one read last and the memory-side cache
+// (256 MB) still holds.
 template <bool REVERSE, class F>
-__device__ __forceinline__ void clip_chunks(const ClipTable& p, F&& f) {
+__device__ __forceinline__ void clip_chunks(const ClipTable& p, const ClipEntry& e, F&& f) {
   const int chunks = p.first[p.count];
   for (int b = blockIdx.x; b < chunks; b += gridDim.x) {
     const int c = REVERSE ? chunks - 1 - b : b;
-    int lo = 0, hi = p.count - 1;  // the last tensor whose first chunk is <= c (empty tensors have none)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.first[mid] <= c)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const long long e0 = (long long)(c - p.first[lo]) * CLIP_CHUNK;
-    f(lo, e0, (int)min((long long)CLIP_CHUNK, p.size[lo] - e0));
+    // the last tensor whose first chunk is <= c (empty tensors have none)
+    const int t = 63 - __builtin_clzll(__builtin_amdgcn_ballot_w64(e.first <= c));
+    const long long e0 = (long long)(c - (int)__builtin_amdgcn_readlane(e.first, t)) * CLIP_CHUNK;
+    f(reinterpret_cast<const uint8_t*>(of_lane(e.in, t)), reinterpret_cast<uint8_t*>(of_lane(e.out, t)),
+      (int)__builtin_amdgcn_readlane(e.type, t), e0, (int)min((long long)CLIP_CHUNK, (long long)of_lane(e.size, t) - e0));
   }
 }
 
@@ -110,13 +127,13 @@ template <int NONE = 0>
 __global__ void __launch_bounds__(256) clip_norm_kernel(const ClipTable p) {
   __shared__ double sm[4];
   double s = 0.0;
-  clip_chunks<false>(p, [&](int t, long long e0, int n) {
-    if (p.type[t] == T_F32)
-      s += chunk_squares<T_F32>(p.in[t] + e0 * 4, n);
-    else if (p.type[t] == T_BF16)
-      s += chunk_squares<T_BF16>(p.in[t] + e0 * 2, n);
+  clip_chunks<false>(p, ClipEntry(p), [&](const uint8_t* in, uint8_t*, int type, long long e0, int n) {
+    if (type == T_F32)
+      s += chunk_squares<T_F32>(in + e0 * 4, n);
+    else if (type == T_BF16)
+      s += chunk_squares<T_BF16>(in + e0 * 2, n);
     else
-      s += chunk_squares<T_F16>(p.in[t] + e0 * 2, n);
+      s += chunk_squares<T_F16>(in + e0 * 2, n);
   });
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) sm[wave_id()] = s;
@@ -127,6 +144,7 @@ __global__ void __launch_bounds__(256) clip_norm_kernel(const ClipTable p) {
 template <int NONE = 0>
 __global__ void __launch_bounds__(256) clip_scale_kernel(const ClipTable p) {
   __shared__ double sm[4];
+  const ClipEntry entry(p);
   double s = 0.0;
   for (int i = threadIdx.x; i < p.partials; i += 256) s += p.part[i];
   s = wave_sum(s);
@@ -136,13 +154,13 @@ __global__ void __launch_bounds__(256) clip_scale_kernel(const ClipTable p) {
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
   const double ratio = (double)p.max_norm / (norm + 1e-6);
   const float scale = ratio > 1.0 ? 1.0f : (float)ratio;  // (NaN stays NaN)
-  clip_chunks<true>(p, [&](int t, long long e0, int n) {
-    if (p.type[t] == T_F32)
-      chunk_scale<T_F32>(p.in[t] + e0 * 4, p.out[t] + e0 * 4, n, scale);
-    else if (p.type[t] == T_BF16)
-      chunk_scale<T_BF16>(p.in[t] + e0 * 2, p.out[t] + e0 * 2, n, scale);
+  clip_chunks<true>(p, entry, [&](const uint8_t* in, uint8_t* out, int type, long long e0, int n) {
+    if (type == T_F32)
+      chunk_scale<T_F32>(in + e0 * 4, out + e0 * 4, n, scale);
+    else if (type == T_BF16)
+      chunk_scale<T_BF16>(in + e0 * 2, out + e0 * 2, n, scale);
     else
-      chunk_scale<T_F16>(p.in[t] + e0 * 2, p.out[t] + e0 * 2, n, scale);
+      chunk_scale<T_F16>(in + e0 * 2, out + e0 * 2, n, scale);
   });
 }
 
