@@ -181,7 +181,9 @@ inline Plan skinny_plan(int mode, int variant, long long M, long long N, long lo
   pl.tiles_m = 1;
   pl.tiles_n = (int)ceil_div(N, two && !glu ? 32 : 16);
   const float per_k = ((two ? 1.8f : 0.9f) + 0.05f * (float)M) * (align < 4 ? 3.4f : 1.0f);  // us per 1024 of the reduction
-  const float fill = (float)pl.tiles_n / (float)cus * (!two ? 1.3f : glu ? 1.45f : 1.5f) - (two ? 0.0f : 0.15f);
+  // (rounds of workgroups: those of aligned rows share the memory's rate)
+  const float rounds = (float)pl.tiles_n / (float)cus;
+  const float fill = align < 4 ? rounds * (two && !glu ? 1.3f : 1.13f) : rounds * (!two ? 1.3f : glu ? 1.45f : 1.5f) - (two ? 0.0f : 0.15f);
   const float each = two ? 0.0f : 0.5f;  // joining sixteen waves' sums instead of eight
   const float run = (per_k * (float)R / 1024.0f + each) * std::max(1.0f, fill) - each;
   pl.us = 3.6f + std::max(run, (float)N * (float)R * (glu ? 4.0f : 2.0f) / 5.2e6f + 0.05f * run);  // (the weights, once)
