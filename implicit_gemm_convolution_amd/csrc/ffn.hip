@@ -135,7 +135,9 @@ int forward(GemmArgs& a, int type, void* ws, size_t ws_bytes, size_t* query, hip
   const int a_al = row_align(a.A, a.lda, a.R), b_al = row_align(a.B, a.ldb, a.R);
   const int b2_al = MODE == igc_ffn::M_GLU ? row_align(a.B2, a.ldb2, a.R) : 16;
   const bool a_ok = a_al == 16, b_ok = b_al == 16, b2_ok = b2_al == 16;
-  Plan pl = make_plan(MODE, a.M, a.N, a.R, std::min(a_al, std::min(b_al, b2_al)), cus, may);
+  const int align = std::min(a_al, std::min(b_al, b2_al));
+  a.odd_rows = align < 4;
+  Plan pl = make_plan(MODE, a.M, a.N, a.R, align, cus, may);
   Pads pads;
   // Operands of another alignment are copied into padded rows where the copy
   // costs less than the faster kernel gains (bf16, us, without and with:

@@ -170,23 +170,25 @@ inline Plan any_plan(int mode, int variant, long long M, long long N, long long 
 // The plan on one of the kernels for few rows (at most 64): every wave loads
 // its part of the reduction in batches, so the time goes with the reduction's
 // length and, more weakly, with the rows that share it; rows at odd multiples
-// of 2 bytes load 3.4 times as long.  bf16, us, 16 | 32 weight rows | 64-row
+// of 2 bytes take two loads for one.  bf16, us, 16 | 32 weight rows | 64-row
 // tiles: 1x4096x4096 8.5 | 11.4 | 11.0, 16x11008x4096 28 | 30 | 18,
 // 32x512x512 4.3 | 6.2 | 5.3, 32x16384x1024 16 | 11 | 8; the gated block at
-// 1x11008x4096 - | 37 | 40, 16x11008x4096 - | 46 | 41, 16x2048x1024 - | 5.7 | 7.8.
+// 1x11008x4096 - | 37 | 40, 16x11008x4096 - | 46 | 41, 16x2048x1024 - | 5.7 |
+// 7.8.  Odd rows, and the tiles for any rows: 1x4096x4097 11 | 19 | 22,
+// 32x2048x1025 6.7 | 8.0 | 11, 16x2048x8193 26 | 35 | 22.
 inline Plan skinny_plan(int mode, int variant, long long M, long long N, long long R, int align, int cus) {
   Plan pl;
-  const bool two = variant == P_SKINNY_32, glu = mode == igc_ffn::M_GLU;
+  const bool two = variant == P_SKINNY_32, glu = mode == igc_ffn::M_GLU, odd = align < 4;
   pl.variant = variant;
   pl.tiles_m = 1;
   pl.tiles_n = (int)ceil_div(N, two && !glu ? 32 : 16);
-  const float per_k = ((two ? 1.8f : 0.9f) + 0.05f * (float)M) * (align < 4 ? 3.4f : 1.0f);  // us per 1024 of the reduction
-  // (rounds of workgroups: those of aligned rows share the memory's rate)
+  const float per_k = ((two ? 1.8f : 0.9f) + 0.05f * (float)M) * (!odd ? 1.0f : glu ? 1.75f : 1.5f);  // us per 1024 of the reduction
   const float rounds = (float)pl.tiles_n / (float)cus;
-  const float fill = align < 4 ? rounds * (two && !glu ? 1.3f : 1.13f) : rounds * (!two ? 1.3f : glu ? 1.45f : 1.5f) - (two ? 0.0f : 0.15f);
+  const float fill = odd ? 1.45f * rounds : rounds * (!two ? 1.3f : glu ? 1.45f : 1.5f) - (two ? 0.0f : 0.15f);
   const float each = two ? 0.0f : 0.5f;  // joining sixteen waves' sums instead of eight
   const float run = (per_k * (float)R / 1024.0f + each) * std::max(1.0f, fill) - each;
-  pl.us = 3.6f + std::max(run, (float)N * (float)R * (glu ? 4.0f : 2.0f) / 5.2e6f + 0.05f * run);  // (the weights, once)
+  const float weights = (float)N * (float)R * (glu ? 4.0f : 2.0f) / (odd ? 3.0e6f : 5.2e6f);
+  pl.us = 3.6f + std::max(run, weights + 0.05f * run);
   return pl;
 }
 

@@ -5,12 +5,19 @@
 
 namespace igc_ffn_host {
 
-template <bool BF, int MODE, int MB>
+template <bool BF, int MODE, int MB, bool ODD>
 void launch_skinny(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t stream) {
   if (pl.variant == P_SKINNY_32)
-    hipLaunchKernelGGL((igc_ffn::gemm_skinny_kernel<BF, MODE, MB, 2, 8>), dim3((unsigned)pl.tiles_n), dim3(512), 0, stream, a);
+    hipLaunchKernelGGL((igc_ffn::gemm_skinny_kernel<BF, MODE, MB, 2, 8, ODD>), dim3((unsigned)pl.tiles_n), dim3(512), 0, stream, a);
   else if constexpr (MODE == igc_ffn::M_FWD)
-    hipLaunchKernelGGL((igc_ffn::gemm_skinny_kernel<BF, MODE, MB, 1, 16>), dim3((unsigned)pl.tiles_n), dim3(1024), 0, stream, a);
+    hipLaunchKernelGGL((igc_ffn::gemm_skinny_kernel<BF, MODE, MB, 1, 16, ODD>), dim3((unsigned)pl.tiles_n), dim3(1024), 0, stream, a);
+}
+template <bool BF, int MODE, int MB>
+void launch_skinny(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t stream) {
+  if (a.odd_rows)
+    launch_skinny<BF, MODE, MB, true>(a, pl, stream);
+  else
+    launch_skinny<BF, MODE, MB, false>(a, pl, stream);
 }
 
 inline dim3 join_grid(const Plan& pl, int bm) {
