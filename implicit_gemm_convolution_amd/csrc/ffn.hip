@@ -73,6 +73,10 @@ GemmArgs product(long long M, long long N, long long R, const void* A, long long
 
 // part: where the partial tiles of a split reduction go.
 void apply_plan(GemmArgs& a, const Plan& pl, uint8_t* part) {
+  auto lines = [](const void* p, long long ld, int bytes) {  // (an output that is left out has no say)
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 127u) == 0 && ld * bytes % 128 == 0);
+  };
+  a.stream = lines(a.Y, a.ldy, a.y_f32 ? 4 : 2) && lines(a.Z, a.ldz, 2) && lines(a.U, a.ldu, 2) && lines(a.Y2, a.ldy2, 2);
   a.tiles_m = pl.tiles_m;
   a.tiles_n = pl.tiles_n;
   a.whole = (int)pl.whole;

@@ -294,6 +294,7 @@ struct GemmArgs {
   uint8_t* Y2;
   long long ldy2;
   int m_split, m_rows;
+  int stream;  // the rows of every output are whole 128-byte lines: written past the caches
   // work split
   int tiles_m, tiles_n;
   int whole;    // tiles [0, whole) have a workgroup each
@@ -512,8 +513,11 @@ __device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& 
 }
 
 // U rows of V consecutive sums (`f`, and `u` of the second product) leave for
-// the outputs.  FULL: every lane has V columns.
-template <bool BF, int MODE, int V, int U, bool FULL>
+// the outputs.  FULL: every lane has V columns.  STREAM: whole lines, written
+// past the caches (8192 x 16384 x 4096 with kept sums 811 -> 803 us, 5728 x 5120 x
+// 1088 74 -> 71; parts of lines must meet in the caches: 1000 x 32003 in fp32 81
+// -> 100 us streamed).
+template <bool BF, int MODE, int V, int U, bool FULL, bool STREAM>
 struct Epilogue {
   const GemmArgs& p;
   int col;       // this lane's first column
@@ -532,11 +536,29 @@ struct Epilogue {
   }
   __device__ __forceinline__ int have() const { return FULL ? V : left; }
   // row q of the U rows
-  __device__ __forceinline__ void put(uint8_t* base, long long ld, int row, const float (&f)[U * V], int q) const {
+  template <class T>
+  __device__ __forceinline__ void write(uint8_t* base, long long ld, int row, const float (&f)[U * V], int q) const {
     float v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = f[q * V + e];
-    store_n<BF, V>(base + ((long long)row * ld + col) * 2, have(), v);
+    uint8_t* const to = base + ((long long)row * ld + col) * sizeof(T);
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    if constexpr (STREAM && sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        u32x4 w;
+        __builtin_memcpy(&w, v + e, 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(to + e * 4));
+      }
+    } else if constexpr (STREAM) {
+      static_assert(V == 8, "16-byte stores");
+      const uint4 w = pack8<BF>(v);
+      __builtin_nontemporal_store(u32x4{w.x, w.y, w.z, w.w}, reinterpret_cast<u32x4*>(to));
+    } else if constexpr (sizeof(T) == 4) {
+      store_f32(reinterpret_cast<float*>(to), have(), v);
+    } else {
+      store_n<BF, V>(to, have(), v);
+    }
   }
   // rows row0, row0 + step, ...
   __device__ __forceinline__ void operator()(int row0, int step, float (&f)[U * V], float (&u)[U * V]) const {
@@ -547,12 +569,12 @@ struct Epilogue {
         const int row = row0 + q * step;
         if (row >= p.M) continue;
         if constexpr (MODE == M_DX) {
-          put(p.Y, p.ldy, row, f, q);
+          write<uint16_t>(p.Y, p.ldy, row, f, q);
         } else {
           const bool second = row >= p.m_split;
           const int r = second ? row - p.m_split : row;
           uint8_t* const y = second ? p.Y2 : p.Y;  // (either may be left out)
-          if (y && r < p.m_rows) put(y, second ? p.ldy2 : p.ldy, r, f, q);
+          if (y && r < p.m_rows) write<uint16_t>(y, second ? p.ldy2 : p.ldy, r, f, q);
         }
       }
     } else {
@@ -582,13 +604,13 @@ struct Epilogue {
       if (p.Z) {
 #pragma unroll
         for (int q = 0; q < U; ++q)
-          if (row0 + q * step < p.M) put(p.Z, p.ldz, row0 + q * step, f, q);
+          if (row0 + q * step < p.M) write<uint16_t>(p.Z, p.ldz, row0 + q * step, f, q);
       }
       act_n<false>(p.act, f, y, unused);
       if constexpr (MODE == M_GLU) {
 #pragma unroll
         for (int q = 0; q < U; ++q)
-          if (p.U && row0 + q * step < p.M) put(p.U, p.ldu, row0 + q * step, u, q);
+          if (p.U && row0 + q * step < p.M) write<uint16_t>(p.U, p.ldu, row0 + q * step, u, q);
 #pragma unroll
         for (int e = 0; e < U * V; ++e) y[e] *= u[e];
       } else if (p.res) {
@@ -599,14 +621,10 @@ struct Epilogue {
       for (int q = 0; q < U; ++q) {
         const int row = row0 + q * step;
         if (row >= p.M) continue;
-        if (MODE == M_FWD && p.y_f32) {
-          float v[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) v[e] = y[q * V + e];
-          store_f32(reinterpret_cast<float*>(p.Y) + (long long)row * p.ldy + col, have(), v);
-        } else {
-          put(p.Y, p.ldy, row, y, q);
-        }
+        if (MODE == M_FWD && p.y_f32)
+          write<float>(p.Y, p.ldy, row, y, q);
+        else
+          write<uint16_t>(p.Y, p.ldy, row, y, q);
       }
     }
   }
@@ -688,10 +706,12 @@ __device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[
       turns(out, row0 + G0 * 16);
     });
   };
-  if (col0 + OUT <= p.N)
-    rows(Epilogue<BF, MODE, 8, U, true>(p, col0 + rc * 8));
+  if (col0 + OUT > p.N)
+    rows(Epilogue<BF, MODE, 8, U, false, false>(p, col0 + rc * 8));
+  else if (p.stream)
+    rows(Epilogue<BF, MODE, 8, U, true, true>(p, col0 + rc * 8));
   else
-    rows(Epilogue<BF, MODE, 8, U, false>(p, col0 + rc * 8));
+    rows(Epilogue<BF, MODE, 8, U, true, false>(p, col0 + rc * 8));
 }
 
 // The simple product: K tiles go through registers into two LDS stages.
@@ -862,7 +882,7 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
       if constexpr (GLU) u4 += red[q][PB * MB + b][l];
     }
     float f[4] = {f4[0], f4[1], f4[2], f4[3]}, u[4] = {u4[0], u4[1], u4[2], u4[3]};
-    const Epilogue<BF, MODE, 4, 1, false> out(p, n0 + (b / MB) * 16 + 4 * (l >> 4));
+    const Epilogue<BF, MODE, 4, 1, false, false> out(p, n0 + (b / MB) * 16 + 4 * (l >> 4));
     out((b % MB) * 16 + (l & 15), 0, f, u);
   }
 }
