@@ -97,6 +97,12 @@ __device__ __forceinline__ double chunk_squares(const uint8_t* in, int n) {
   return s;
 }
 
+// 16 bytes past the caches, at any address of the element type's alignment.
+__device__ __forceinline__ void stream16(uint8_t* p, const uint4& v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
+}
+
 template <int T>
 __device__ __forceinline__ void chunk_scale(const uint8_t* in, uint8_t* out, int n, float scale) {
   constexpr int EB = T == T_F32 ? 4 : 2, V = 16 / EB;
@@ -108,7 +114,9 @@ __device__ __forceinline__ void chunk_scale(const uint8_t* in, uint8_t* out, int
         __builtin_memcpy(f, in + (long long)e * 4, 16);
 #pragma unroll
         for (int q = 0; q < 4; ++q) f[q] *= scale;
-        __builtin_memcpy(out + (long long)e * 4, f, 16);
+        uint4 w;
+        __builtin_memcpy(&w, f, 16);
+        stream16(out + (long long)e * 4, w);
       } else {
         for (int q = 0; q < 4; ++q)
           if (e + q < n) reinterpret_cast<float*>(out)[e + q] = reinterpret_cast<const float*>(in)[e + q] * scale;
@@ -118,7 +126,10 @@ __device__ __forceinline__ void chunk_scale(const uint8_t* in, uint8_t* out, int
       unpack8<T == T_BF16>(load8(in + (long long)e * 2, n - e), f);
 #pragma unroll
       for (int q = 0; q < 8; ++q) f[q] *= scale;
-      store8(out + (long long)e * 2, pack8<T == T_BF16>(f), n - e);
+      if (n - e >= 8)
+        stream16(out + (long long)e * 2, pack8<T == T_BF16>(f));
+      else
+        store8(out + (long long)e * 2, pack8<T == T_BF16>(f), n - e);
     }
   }
 }
