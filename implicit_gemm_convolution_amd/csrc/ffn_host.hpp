@@ -30,10 +30,10 @@ inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // The kernels of a product, by output tile (the gated block's tiles hold two
 // products: half as many output columns).
-// P_TILE_*: aligned operands, straight into LDS; P_ANY_*: any operand,
+// P_TILE_*: aligned operands, straight into LDS (P_TILE_32: 64 x 32); P_ANY_*: any operand,
 // through registers; P_SKINNY_*: few rows, any operand, 16 or 32 weight rows
 // per workgroup.
-enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_ANY_128, P_ANY_64, P_SKINNY_16, P_SKINNY_32 };
+enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_TILE_32, P_ANY_128, P_ANY_64, P_SKINNY_16, P_SKINNY_32 };
 
 struct Plan {
   int variant = P_ANY_64;
@@ -49,6 +49,7 @@ inline void plan_tile(int mode, int variant, int& bm, int& bn) {
     case P_TILE_256: bm = 256; bn = mode == igc_ffn::M_GLU ? 128 : 256; return;
     case P_TILE_128:
     case P_ANY_128: bm = 128; bn = mode == igc_ffn::M_GLU ? 64 : 128; return;
+    case P_TILE_32: bm = 64; bn = 32; return;
     default: bm = 64; bn = 64; return;
   }
 }
@@ -75,7 +76,8 @@ inline bool dma_operand(const void* p, long long ld, long long length) {
 // split only below one per compute unit: 5%, and 1.9 times as long at
 // 640 x 2432 x 27392.
 //   k0, k1, k2  a K tile of 64 in an empty card; with one workgroup on every
-//               compute unit (256 x 256: on half of them); with every place taken
+//               compute unit (where there is one place: on half of them); with
+//               every place taken
 //   out         the prologue and the outputs of a workgroup
 //   join        the second launch of a split reduction: itself, for each MB
 //               of partial tiles, for each split
@@ -83,17 +85,20 @@ struct TileCost {
   float launch, k0, k1, k2, out, join, join_mb, join_split;
 };
 inline const TileCost& tile_cost(int mode, int variant) {
-  static constexpr TileCost one[3] = {{2.1f, 0.77f, 1.02f, 1.35f, 11.8f, 0.0f, 0.17f, 0.0f},
+  static constexpr TileCost one[4] = {{2.1f, 0.77f, 1.02f, 1.35f, 11.8f, 0.0f, 0.17f, 0.0f},
                                       {2.4f, 0.35f, 0.51f, 0.91f, 2.3f, 2.1f, 0.15f, 0.32f},
-                                      {2.8f, 0.18f, 0.23f, 0.37f, 1.0f, 1.4f, 0.31f, 0.40f}};
-  static constexpr TileCost two[3] = {{2.6f, 0.96f, 1.07f, 1.40f, 10.2f, 0.0f, 0.20f, 0.0f},
+                                      {2.8f, 0.18f, 0.23f, 0.37f, 1.0f, 1.4f, 0.31f, 0.40f},
+                                      {2.8f, 0.11f, 0.14f, 0.18f, 1.0f, 1.4f, 0.31f, 0.40f}};
+  static constexpr TileCost two[4] = {{2.6f, 0.96f, 1.07f, 1.40f, 10.2f, 0.0f, 0.20f, 0.0f},
                                       {3.8f, 0.33f, 0.53f, 0.94f, 1.5f, 2.4f, 0.11f, 0.43f},
-                                      {3.0f, 0.19f, 0.24f, 0.30f, 2.3f, 1.2f, 0.64f, 0.0f}};
+                                      {3.0f, 0.19f, 0.24f, 0.30f, 2.3f, 1.2f, 0.64f, 0.0f},
+                                      {3.0f, 0.13f, 0.19f, 0.47f, 1.0f, 1.2f, 0.64f, 0.0f}};
   return (mode == igc_ffn::M_GLU ? two : one)[variant];
 }
 // workgroups of a tile that share a compute unit (160 KB of LDS)
 inline int tile_places(int mode, int variant) {
-  return variant == P_TILE_256 || (variant == P_TILE_64 && mode == igc_ffn::M_GLU) ? 1 : 2;
+  const bool glu = mode == igc_ffn::M_GLU;
+  return variant == P_TILE_256 || (variant == P_TILE_64 && glu) || (variant == P_TILE_32 && !glu) ? 1 : 2;
 }
 // `count` workgroups of n K tiles each
 inline float rounds_us(const TileCost& c, int places, float n, long long count, int cus) {
@@ -208,7 +213,7 @@ inline Plan make_plan(int mode, long long M, long long N, long long R, int align
   if (align == 16) {
     // (streaming the operands, no faster than 5 TB/s)
     const float least = 4.5f + ((float)M + (float)N * (mode == igc_ffn::M_GLU ? 2.0f : 1.0f)) * (float)R * 2.0f / 5e6f;
-    for (int v = P_TILE_256; v <= P_TILE_64; ++v) {
+    for (int v = P_TILE_256; v <= (mode == igc_ffn::M_DW ? P_TILE_64 : P_TILE_32); ++v) {
       Plan q = best_split(mode, v, M, N, R, cus, may_split);
       if (M <= 64) q.us = std::max(q.us, least + 0.05f * q.us);  // (the faster tile still comes first)
       take(q);

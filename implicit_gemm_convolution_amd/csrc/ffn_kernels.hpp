@@ -324,6 +324,7 @@ struct LdsTile {
   static constexpr int ROWB = W * 2;  // COL: bytes per reduction row
   __device__ static __forceinline__ int gran(int kr) {  // COL: the granule XOR of reduction row kr
     if constexpr (W >= 128) return (kr & 3) | (((kr >> 3) & 1) << 2);
+    if constexpr (W == 32) return (kr >> 3) & 1;
     return ((kr >> 1) & 1) | (((kr >> 3) & 1) << 1);
   }
   // byte offset of 16-byte chunk c of (ROW) row r / (COL) reduction row r
@@ -666,7 +667,7 @@ __device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[
   constexpr int TN = FN * 16, OUT = GLU ? TN / 2 : TN;  // staged columns, output columns
   constexpr int LPR = OUT / 8, RPP = 64 / LPR;          // lanes per row, rows per pass
   constexpr int FIT = REGION / (16 * TN * 4), GR = FIT >= FM ? FM : FM / 2;  // block rows staged at a time
-  static_assert(RPP <= 16 && FIT >= GR && FM % GR == 0, "staging");
+  static_assert(FIT >= GR && FM % GR == 0, "staging");
   constexpr int XM = TN / 4 < 16 ? TN / 4 - 1 : 15;
   const int lane = threadIdx.x & 63;
   const int wr = lane & 15, rr = lane / LPR, rc = lane % LPR;
@@ -904,7 +905,9 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
 // K tile, of which they take 2048).  128 x 128 at depth 2, two workgroups per
 // compute unit.  64 x 64 at depth 4 (80 KB: two workgroups), where a compute
 // unit's loads in flight are the bound: 64 x 4096 x 4096 unsplit 26.7 us at
-// depth 2, 15.4 at 4, 15.5 at 6.
+// depth 2, 15.4 at 4, 15.5 at 6.  64 x 32 at depth 6 spreads the loads of small
+// outputs over twice as many compute units: 24 x 8192 x 2048 9.0 -> 8.0 us,
+// 500 x 1024 x 1024 of the gated block 8.0 -> 6.6.
 constexpr int tile_lds(int bm, int bn, int depth) { return 128 * ((depth + 1) * bm + (depth == 2 ? 2 : depth + 1) * bn); }
 constexpr int tile_waves(int bm, int bn, int depth) { return 160 * 1024 / tile_lds(bm, bn, depth) > 1 ? 2 : 1; }  // per SIMD
 template <bool BF, int MODE, int BM, int BN, int DEPTH>

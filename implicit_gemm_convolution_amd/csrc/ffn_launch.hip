@@ -53,6 +53,12 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
     case P_TILE_256: IGC_FFN_TILE(gemm_tile_kernel, 256, 256, 2); break;
     case P_TILE_128: IGC_FFN_TILE(gemm_tile_kernel, 128, 128, 2); break;
     case P_TILE_64: IGC_FFN_TILE(gemm_tile_kernel, 64, BN64, 4); break;
+    case P_TILE_32:
+      if constexpr (MODE == igc_ffn::M_GLU)
+        IGC_FFN_TILE(gemm_tile_kernel, 64, 64, 4);
+      else if constexpr (MODE != igc_ffn::M_DW)
+        IGC_FFN_TILE(gemm_tile_kernel, 64, 32, 6);
+      break;
     case P_ANY_128: IGC_FFN_TILE(gemm_any_kernel, 128, 128); break;
     case P_ANY_64: IGC_FFN_TILE(gemm_any_kernel, 64, BN64); break;
     default: return fail(IGC_EUNSUPPORTED, "internal: no kernel for variant %d", pl.variant);
