@@ -322,8 +322,10 @@ def test_glu_backward(torch, igc, ws, size, kind):
 
 # Outputs (rows, columns) and reductions that take each tile, whole, in splits,
 # and with the last round of tiles in splits.
-PRODUCTS = [(136, 10960, 72), (72, 4280, 3520), (4632, 1696, 840), (912, 12344, 336), (392, 8208, 3336), (1440, 11224, 1384), (72, 208, 1448)]
-PRODUCTS_GLU = [(72, 2384, 3424), (280, 11312, 1176), (424, 12488, 408), (136, 2704, 14288), (1464, 5464, 1296), (72, 8208, 2456), (72, 208, 840)]
+PRODUCTS = [(136, 10960, 72), (72, 4280, 3520), (4632, 1696, 840), (912, 12344, 336), (392, 8208, 3336), (1440, 11224, 1384), (72, 208, 1448),
+            (72, 208, 3384), (544, 13128, 1128), (520, 512, 8192), (104, 2048, 520), (520, 4096, 1024)]
+PRODUCTS_GLU = [(72, 2384, 3424), (280, 11312, 1176), (424, 12488, 408), (136, 2704, 14288), (1464, 5464, 1296), (72, 8208, 2456), (72, 208, 840),
+                (72, 208, 1864), (72, 1400, 9120), (280, 11008, 1456), (72, 7176, 72), (136, 2904, 14288)]
 # Rows that the direct loads do not take: odd lengths, and a start off the 16 bytes.
 UNALIGNED = [(200, 1000, 2049, 0, 0), (727, 1345, 1531, 0, 0), (300, 1001, 2001, 2, 1), (1000, 1500, 1500, 0, 4), (520, 2000, 1000, 8, 1),
              (96, 999, 1601, 0, 0), (2100, 1300, 260, 0, 2), (70, 2049, 2047, 3, 0)]
