@@ -69,11 +69,11 @@ inline bool dma_operand(const void* p, long long ld, long long length) {
 }
 
 // What a launch of the aligned tiles takes, in us, fitted to 2700 timings on
-// MI355X (bf16; 40 outputs of 16 x 4096 to 8192 x 8192, reductions of 512 to
+// MI355X (bf16; 55 outputs of 16 x 4096 to 8192 x 8192, reductions of 300 to
 // 30000, one to sixteen splits).  Over those products the plan with the
-// smallest estimate takes 0.7% longer than the fastest one in the mean and 16%
-// at most (gated block 1.5% and 12%).  Tiles chosen by how many fill the card,
-// split only below one per compute unit: 5%, and 1.9 times as long at
+// smallest estimate takes 1.1% longer than the fastest one in the mean and 19%
+// at most (gated block 0.3% and 19%).  Tiles chosen by how many fill the card,
+// split only below one per compute unit: 5%, and twice as long at
 // 640 x 2432 x 27392.
 //   k0, k1, k2  a K tile of 64 in an empty card; with one workgroup on every
 //               compute unit (where there is one place: on half of them); with

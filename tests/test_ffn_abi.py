@@ -122,3 +122,35 @@ def test_grad_clip_binding_checks_its_tensors(igc):
         igc.grad_clip([a, b], 1.0, norm, out=[a, torch.zeros(3)])
     with pytest.raises(TypeError, match="float64"):
         igc.grad_clip([a.double()], 1.0, norm)
+
+
+def test_arguments_of_every_kind(igc):
+    """Addresses as ints, tensors, None or anything with data_ptr(); whole numbers that fit; nothing else."""
+    import torch
+
+    class Holder:
+        def data_ptr(self):
+            return P
+
+    good = dict(M=0, N=6, K=8, X=P, ldx=8, W=P, ldw=8, Y=None, ldy=6, stream=0)
+    for x in (P, None, torch.zeros(4), Holder()):
+        assert igc.linear_forward(**{**good, "X": x}) == igc.IGC_OK
+    with pytest.raises(TypeError, match="address or a tensor"):
+        igc.linear_forward(**{**good, "X": "text"})
+    with pytest.raises(TypeError):
+        igc.linear_forward(**{**good, "M": 1.5})
+    with pytest.raises(OverflowError):
+        igc.linear_forward(**{**good, "ldx": 1 << 40})
+    with pytest.raises(RuntimeError):  # a tensor without memory of its own
+        igc.linear_forward(**{**good, "X": torch.sparse_coo_tensor(size=(2, 2))})
+    with pytest.raises(TypeError, match="tensors"):
+        igc.grad_clip([1, 2], 1.0, None, stream=0)
+
+
+def test_without_torch_the_descriptors_go_through_ctypes(igc, monkeypatch):
+    good = dict(M=4, N=6, K=8, X=P, ldx=8, W=P, ldw=8, Y=P, ldy=6, type=igc.IGC_F16, act=igc.IGC_ACT_GELU, stream=0)
+    monkeypatch.setattr(igc.binding, "_native", False)
+    assert igc.linear_forward(**{**good, "M": 0, "X": None, "Y": None}) == igc.IGC_OK
+    _rejects(igc, igc.linear_forward, good, [dict(ldx=7), dict(W=None), dict(Y=P + 1), dict(Z=P, ldz=5), dict(R=P, ldr=5)])
+    with pytest.raises(RuntimeError, match="torch"):
+        igc.grad_clip([], 1.0, P, stream=0)
