@@ -568,3 +568,54 @@ def test_clip_not_finite(torch, igc, ws):
     g[17] = float("-inf")
     igc.grad_clip([g], 1.0, norm, workspace=ws)
     assert bool(norm.isinf()) and bool(g[17].isnan()) and int(g.nan_to_num(0.0).count_nonzero()) == 0
+
+
+def test_offsets_past_32_bits(torch, igc, ws):
+    """Rows that start more than 2^32 bytes into their matrices: the tiles (70000 rows of a leading dimension of 40000), the
+    streaming kernel and the copies into padded rows (a few rows, 2^30 apart)."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GiB")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    M, N, K, ld = 70000, 96, 128, 40000
+    big = lambda cols: torch.empty(M, ld, dtype=torch.float16, device="cuda")[:, :cols]  # noqa: E731
+    X, Y, Z, dY, dX = big(K), big(N), big(N), big(N), big(K)
+    X.copy_(torch.randn(M, K, generator=gen, device="cuda"))
+    dY.copy_(torch.randn(M, N, generator=gen, device="cuda"))
+    W = (torch.randn(N, K, generator=gen, device="cuda") * K ** -0.5).half()
+    igc.linear_forward(M, N, K, X, ld, W, K, Y, ld, type=igc.IGC_F16, act=igc.IGC_ACT_SILU, Z=Z, ldz=ld, workspace=ws)
+    dW, db = torch.empty_like(W), torch.empty(N, device="cuda")
+    igc.linear_backward(M, N, K, dY, ld, Z=Z, ldz=ld, X=X, ldx=ld, W=W, ldw=K, dX=dX, lddx=ld, dW=dW, lddw=K, dbias=db,
+                        type=igc.IGC_F16, act=igc.IGC_ACT_SILU, workspace=ws)
+    rows = slice(M - 3000, M)
+    x, w = X[rows].double(), W.double()
+    z, s = x @ w.T, x.abs() @ w.abs().T
+    ez = (K + 2) * U * s
+    _check("Z", Z[rows], z, ez + _store("f16", z.abs() + ez))
+    f = _f("silu", z)[0]
+    _check("Y", Y[rows], f, 1.13 * ez + 8 * U * (z.abs() + 1) + _store("f16", f.abs() + ez))
+    d = dY.double() * _f("silu", Z.double())[1]
+    ed = 8 * U * dY.double().abs() * (1 + Z.double().abs())
+    er = ed + _store("f16", d.abs() + ed)
+    e = er[rows] @ w.abs() + (N + 2) * U * (d[rows].abs() @ w.abs())
+    _check("dX", dX[rows], d[rows] @ w, e + _store("f16", (d[rows] @ w).abs() + e))
+    ref = d.T @ X.double()
+    e = (er + (M + 2) * U * d.abs()).T @ X.double().abs()
+    _check("dW", dW, ref, e + _store("f16", ref.abs() + e))
+    _check("db", db, d.sum(0), ed.sum(0) + (M + 2) * U * d.abs().sum(0) + TINY["f32"])
+    del X, Y, Z, dY, dX, d, ed, er
+    torch.cuda.empty_cache()
+    far = 1 << 30
+    for rows, cols, outs in ((3, 521, 40), (70, 1200, 300)):  # the streaming kernel; padded or any rows
+        if rows * far * 2 > 16 << 30:
+            far = (8 << 30) // rows // 2 * 2 + 1  # elements: 16 GiB in all, odd rows
+        flat = torch.empty(rows * far, dtype=torch.bfloat16, device="cuda")
+        X = flat.view(rows, far)[:, :cols]
+        X.copy_(torch.randn(rows, cols, generator=gen, device="cuda"))
+        W = (torch.randn(outs, cols, generator=gen, device="cuda") * cols ** -0.5).bfloat16()
+        Y = torch.empty(rows, outs, device="cuda")
+        igc.linear_forward(rows, outs, cols, X, far, W, cols, Y, outs, y_type=igc.IGC_F32, workspace=ws)
+        ref, s = X.double() @ W.double().T, X.double().abs() @ W.double().abs().T
+        _check("Y", Y, ref, (cols + 4) * U * s + 8 * U * (ref.abs() + 1) + _store("f32", ref.abs()))
+        del flat, X
+        torch.cuda.empty_cache()
