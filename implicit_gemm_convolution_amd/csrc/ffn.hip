@@ -342,14 +342,19 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   Plan pw = make_plan(igc_ffn::M_DW, red(), b.K, b.M, d_ok && x_ok ? 16 : 2, cus, true);
   const bool joint = want_x && want_w && d_ok && w_ok && x_ok && plan_back(px, pw, b.M, b.K, red(), sums, cus);
 
-  // workspace: D, column sums, padded operands, partial tiles
+  // workspace: D, column sums, D's largest elements and scale, padded operands, partial tiles
   const int rows = act_rows(b.M, std::max(width, 1), cus);
   const int blocks = (int)ceil_div(b.M, rows);
   const size_t d_bytes = make_d ? round256((size_t)b.M * np * width * 2) : 0;
   const size_t s_bytes = sums ? round256((size_t)blocks * np * width * 4) : 0;
   const size_t x_part = want_x ? round256(px.part_bytes) : 0, w_part = want_w ? round256(pw.part_bytes) : 0;
   const size_t part = joint ? x_part + w_part : std::max(x_part, w_part);
-  const size_t need = d_bytes + s_bytes + pads.bytes + part;
+  const bool element = (make_d || sums) && b.M > 0 && b.N > 0;
+  // (relu's D is dY or 0: fp16 holds it as it is)
+  const bool scaled = b.type == IGC_F16 && (b.glu || (act && b.act != IGC_ACT_RELU)) && make_d && element;
+  const long long act_blocks = ceil_div(width, 512) * blocks;
+  const size_t m_bytes = scaled ? round256((act_blocks + 1) * sizeof(float)) : 0;
+  const size_t need = d_bytes + s_bytes + m_bytes + pads.bytes + part;
   if (query) {
     *query = need;
     return IGC_OK;
@@ -358,7 +363,8 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   uint8_t* const ws = static_cast<uint8_t*>(b.ws);
   uint8_t* const D = make_d ? ws : nullptr;
   float* const part_sums = sums ? reinterpret_cast<float*>(ws + d_bytes) : nullptr;
-  uint8_t* const padded = ws + d_bytes + s_bytes;
+  float* const most = scaled ? reinterpret_cast<float*>(ws + d_bytes + s_bytes) : nullptr;
+  uint8_t* const padded = ws + d_bytes + s_bytes + m_bytes;
   uint8_t* const parts = padded + pads.bytes;
 
   const void *W = b.W, *W2 = b.W2, *X = b.X;
@@ -366,7 +372,6 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   if (iw >= 0) W = pads.place(iw, padded), ldw = Pads::padded(b.K);
   if (iw2 >= 0) W2 = pads.place(iw2, padded), ldw2 = Pads::padded(b.K);
   if (ix >= 0) X = pads.place(ix, padded), ldx = Pads::padded(b.K);
-  const bool element = (make_d || sums) && b.M > 0 && b.N > 0;
   if (element) {
     igc_ffn::ActBackArgs e;
     std::memset(&e, 0, sizeof(e));
@@ -388,13 +393,25 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
     e.rows = rows;
     e.groups = (int)ceil_div(width, 512);
     e.blocks = blocks;
-    const long long grid = (long long)e.groups * blocks + pads.groups();
+    const long long grid = act_blocks + pads.groups();
     if (grid > 0x7fffffffLL) return fail(IGC_EUNSUPPORTED, "too many workgroups (%lld)", grid);
+    if (scaled) {
+      e.most = most;
+      e.undo = most + act_blocks;
+    }
     if (b.type == IGC_BF16)
       launch_act_back<true>(e, b.glu, pads.args, dim3((unsigned)grid), stream);
     else
       launch_act_back<false>(e, b.glu, pads.args, dim3((unsigned)grid), stream);
     if (int s = launch_status()) return s;
+    if (scaled) {
+      const dim3 again((unsigned)std::min(act_blocks, 2LL * cus));
+      if (b.glu)
+        hipLaunchKernelGGL((igc_ffn::act_again_kernel<true>), again, dim3(256), 0, stream, e);
+      else
+        hipLaunchKernelGGL((igc_ffn::act_again_kernel<false>), again, dim3(256), 0, stream, e);
+      if (int s = launch_status()) return s;
+    }
   } else if (pads.groups() > 0) {
     hipLaunchKernelGGL((igc_ffn::pad_kernel<0>), dim3((unsigned)pads.groups()), dim3(256), 0, stream, pads.args);
     if (int s = launch_status()) return s;
@@ -408,8 +425,10 @@ int backward(const Backward& b, size_t* query, hipStream_t stream) {
   const long long lda = make_d ? (long long)np * width : b.lddy;
   GemmArgs ax = product(b.M, b.K, red(), A, lda, W, ldw, b.dX, b.lddx);
   ax.b_rows = b.N;
+  ax.undo = scaled ? most + act_blocks : nullptr;
   GemmArgs aw = product(red(), b.K, b.M, A, lda, X, ldx, b.dW, b.lddw);
   aw.m_rows = b.N;
+  aw.undo = ax.undo;
   if (b.glu) {
     ax.B2 = static_cast<const uint8_t*>(W2);
     ax.ldb2 = ldw2;

@@ -10,11 +10,16 @@
 //
 // Every product accumulates in fp32 on the 16x16x32 matrix instructions, and
 // bias, activation and residual are applied to the fp32 sums: one rounding,
-// at the store.  The backward products take D rounded to the operands' type,
-// as the matrix cores do: each term is then off by at most half a step of
-// that type, independently of the others, so a sum over r terms is off by
-// less than its own final rounding once r is more than a few.  db sums the
-// unrounded fp32 values.
+// at the store.  db sums fp32 values.  The backward products take D rounded to
+// the operands' type, which is what the matrix cores multiply; in fp32 D would
+// take them two products for one.  Each term is then off by up to half a step
+// of that type relative to itself, independently of the others, so relative to
+// its size a sum is off by about as much as its own final rounding, whatever
+// its length: the error of dX and dW is that of unrounded D times the square
+// root of 2 (bf16 2.3e-3 for 1.7e-3).  bf16 has the range of fp32.  In fp16 D
+// could leave the range although every input and every gradient is inside it,
+// so D is scaled by a power of two, which the epilogue takes back: both exact.
+// act_back_kernel has the scales.
 #pragma once
 
 #include "igc_kernels.hpp"
@@ -295,6 +300,7 @@ struct GemmArgs {
   long long ldy2;
   int m_split, m_rows;
   int stream;  // the rows of every output are whole 128-byte lines: written past the caches
+  const float* undo;  // (DX and DW of fp16) what takes D's scale back, or NULL
   // work split
   int tiles_m, tiles_n;
   int whole;    // tiles [0, whole) have a workgroup each
@@ -525,7 +531,9 @@ struct Epilogue {
   int left;      // columns from there to the end
   float b1[V], b2[V];
   bool has_bias;
+  float undo;
   __device__ __forceinline__ Epilogue(const GemmArgs& args, int c) : p(args), col(c), left(args.N - c) {
+    if constexpr (!BF && (MODE == M_DX || MODE == M_DW)) undo = p.undo ? *p.undo : 1.0f;
     has_bias = (MODE == M_FWD && p.bias) || (MODE == M_GLU && (p.bias || p.bias2));
     if constexpr (MODE == M_FWD || MODE == M_GLU) {
 #pragma unroll
@@ -565,6 +573,10 @@ struct Epilogue {
   __device__ __forceinline__ void operator()(int row0, int step, float (&f)[U * V], float (&u)[U * V]) const {
     if (!FULL && left <= 0) return;
     if constexpr (MODE == M_DX || MODE == M_DW) {
+      if constexpr (!BF) {
+#pragma unroll
+        for (int e = 0; e < U * V; ++e) f[e] *= undo;
+      }
 #pragma unroll
       for (int q = 0; q < U; ++q) {
         const int row = row0 + q * step;
@@ -1138,6 +1150,9 @@ struct ActBackArgs {
   float* sums;     // out (NULL: none): column sums of each row block, [row blocks][1 or 2][width]
   int rows;        // rows per block
   int groups, blocks;  // workgroups across the columns and down the rows
+  // fp16 (NULL: D is not scaled): the largest finite |D| of each block, and
+  // what takes D's scale back
+  float *most, *undo;
 };
 
 // Rows of any alignment and at least 8 elements, copied into rows of whole
@@ -1182,76 +1197,147 @@ __global__ void __launch_bounds__(256) pad_kernel(const PadArgs p) {
   pad_rows(p, blockIdx.x);
 }
 
-// A workgroup covers 512 columns (8 per lane) x `rows` rows; its four waves
-// take rows in turn, UR at a time so that their loads fly together.  Streams
-// its inputs once: bound by memory (4096 x 8192 with gelu: 201 MB in 42 us;
-// the gated block at 4096 x 10944: 448 MB in 81 us).  Workgroups past its own
-// pad the operands of the products that follow.
+// Block b of the element-wise work: 512 columns (8 per lane) x `rows` rows; the
+// four waves take rows in turn, UR at a time so that their loads fly together.
+// Calls f(row, column, d, du) with D (dG and dU) in fp32, zeros past N.
+template <bool BF, bool GLU, class F>
+__device__ __forceinline__ void act_rows(const ActBackArgs& p, int b, F&& f) {
+  constexpr int UR = GLU ? 2 : 4;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int by = b / p.groups, bx = b - by * p.groups;
+  const int c = bx * 512 + lane * 8;
+  const int left = p.N - c;
+  const int r0 = by * p.rows, r1 = min(p.M, r0 + p.rows);
+  if (c >= p.width) return;
+  for (int rb = r0 + wave; rb < r1; rb += 4 * UR) {
+    uint4 vy[UR], vz[UR], vu[UR];
+#pragma unroll
+    for (int q = 0; q < UR; ++q) {
+      const long long r = rb + 4 * q;
+      const int have = r < r1 ? left : 0;
+      vy[q] = load8(p.dY + (r * p.lddy + c) * 2, have);
+      vz[q] = p.Z ? load8(p.Z + (r * p.ldz + c) * 2, have) : make_uint4(0, 0, 0, 0);
+      if constexpr (GLU) vu[q] = load8(p.U + (r * p.ldu + c) * 2, have);
+    }
+#pragma unroll
+    for (int q = 0; q < UR; ++q) {
+      const long long r = rb + 4 * q;
+      if (r >= r1) break;
+      float dy[8], z[8], fz[8], d[8], du[8];
+      unpack8<BF>(vy[q], dy);
+      unpack8<BF>(vz[q], z);
+      if constexpr (GLU) {
+        float u[8];
+        unpack8<BF>(vu[q], u);
+        act_n<true>(p.act, z, fz, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          du[e] = dy[e] * fz[e];
+          d[e] = dy[e] * u[e] * d[e];
+          if (e >= left) du[e] = d[e] = 0.0f;
+        }
+      } else {
+        if (p.Z) {
+          act_n<true>(p.act, z, fz, d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dy[e] *= d[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = e >= left ? 0.0f : dy[e];
+      }
+      f(r, c, d, du);
+    }
+  }
+}
+
+// The scale of D in fp16.  2^10 to begin with: every |D| below 32 fits, an
+// element from 2^-24 up keeps all its bits, and a smaller one is off by at most
+// 2^-35, which is 2^-10 of the smallest step of the gradients themselves.
+// Where the largest |D| is not in [2^-18, 2^5), act_again_kernel makes D anew
+// at the scale that takes the largest to [2^14, 2^15): elements down to 2^-28
+// of it keep all their bits.  (A search for the largest before D is made, in
+// every call: 777 x 1001 x 1128 with silu 17.0 -> 22.1 us, 4096 x 8192 x 4096
+// 437 -> 478.)
+constexpr float ACT_SCALE = 1024.0f, ACT_LEAST = 0x1p-18f, ACT_MOST = 0x1p5f;
+__device__ __forceinline__ void most_of(float& m, float v) {  // (neither infinities nor NaN)
+  const float a = __builtin_fabsf(v);
+  if (a <= 3.402823466e38f) m = __builtin_fmaxf(m, a);
+}
+__device__ __forceinline__ float group_max(float m, float* sm) {  // in every thread of the workgroup
+#pragma unroll
+  for (int o = 32; o; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) sm[wave_id()] = m;
+  __syncthreads();
+  return __builtin_fmaxf(__builtin_fmaxf(sm[0], sm[1]), __builtin_fmaxf(sm[2], sm[3]));
+}
+template <bool GLU>
+__global__ void __launch_bounds__(256) act_again_kernel(const ActBackArgs p) {
+  __shared__ float sm[4];
+  const int all = p.groups * p.blocks;
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < all; i += 256) m = __builtin_fmaxf(m, p.most[i]);
+  m = group_max(m, sm);
+  if (m == 0.0f || (m >= ACT_LEAST && m < ACT_MOST)) return;
+  // (2^100 at most: where the largest is less than 2^-86, no product of D is left in fp16)
+  const int n = min(14 - ((int)(__builtin_bit_cast(uint32_t, m) >> 23) - 127), 100);
+  const float scale = __builtin_bit_cast(float, (uint32_t)(127 + n) << 23);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.undo = __builtin_bit_cast(float, (uint32_t)(127 - n) << 23);
+  for (int b = blockIdx.x; b < all; b += gridDim.x)
+    act_rows<false, GLU>(p, b, [&](long long r, int c, float (&d)[8], float (&du)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d[e] *= scale;
+        if constexpr (GLU) du[e] *= scale;
+      }
+      store8(p.D + (r * p.ldd + c) * 2, pack8<false>(d), 8);
+      if constexpr (GLU) store8(p.D + (r * p.ldd + p.width + c) * 2, pack8<false>(du), 8);
+    });
+}
+
+// D and its column sums: every block a workgroup.  Streams its inputs once:
+// bound by memory (bf16, 4096 x 8192 with gelu: 201 MB in 42 us; the gated
+// block at 4096 x 10944: 448 MB in 81 us).  Workgroups past its own pad the
+// operands of the products that follow.
 template <bool BF, bool GLU>
 __global__ void __launch_bounds__(256) act_back_kernel(const ActBackArgs p, const PadArgs pad) {
-  constexpr int UR = GLU ? 2 : 4;
   __shared__ float part[GLU ? 2 : 1][4][512];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int act_blocks = p.groups * p.blocks;
   if ((int)blockIdx.x >= act_blocks) return pad_rows(pad, blockIdx.x - act_blocks);
-  const int by = blockIdx.x / p.groups, bx = blockIdx.x - by * p.groups;
-  const int c = bx * 512 + lane * 8;
-  const int left = p.N - c;
-  const int r0 = by * p.rows, r1 = min(p.M, r0 + p.rows);
+  const float scale = !BF && p.undo ? ACT_SCALE : 1.0f;
+  float m = 0.0f;
   float s1[8], s2[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s1[e] = s2[e] = 0.0f;
-  if (c < p.width) {
-    for (int rb = r0 + wave; rb < r1; rb += 4 * UR) {
-      uint4 vy[UR], vz[UR], vu[UR];
+  act_rows<BF, GLU>(p, blockIdx.x, [&](long long r, int c, float (&d)[8], float (&du)[8]) {
 #pragma unroll
-      for (int q = 0; q < UR; ++q) {
-        const long long r = rb + 4 * q;
-        const int have = r < r1 ? left : 0;
-        vy[q] = load8(p.dY + (r * p.lddy + c) * 2, have);
-        vz[q] = p.Z ? load8(p.Z + (r * p.ldz + c) * 2, have) : make_uint4(0, 0, 0, 0);
-        if constexpr (GLU) vu[q] = load8(p.U + (r * p.ldu + c) * 2, have);
-      }
-#pragma unroll
-      for (int q = 0; q < UR; ++q) {
-        const long long r = rb + 4 * q;
-        if (r >= r1) break;
-        float dy[8], z[8], f[8], d[8];
-        unpack8<BF>(vy[q], dy);
-        unpack8<BF>(vz[q], z);
+    for (int e = 0; e < 8; ++e) {
+      s1[e] += d[e];
+      if constexpr (GLU) s2[e] += du[e];
+      if constexpr (!BF) {
+        most_of(m, d[e]);
+        d[e] *= scale;
         if constexpr (GLU) {
-          float u[8], du[8];
-          unpack8<BF>(vu[q], u);
-          act_n<true>(p.act, z, f, d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            du[e] = dy[e] * f[e];
-            d[e] = dy[e] * u[e] * d[e];
-            if (e >= left) du[e] = d[e] = 0.0f;
-            s1[e] += d[e];
-            s2[e] += du[e];
-          }
-          if (p.D) {
-            store8(p.D + (r * p.ldd + c) * 2, pack8<BF>(d), 8);
-            store8(p.D + (r * p.ldd + p.width + c) * 2, pack8<BF>(du), 8);
-          }
-        } else {
-          if (p.Z) {
-            act_n<true>(p.act, z, f, d);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dy[e] *= d[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (e >= left) dy[e] = 0.0f;
-            s1[e] += dy[e];
-          }
-          if (p.D) store8(p.D + (r * p.ldd + c) * 2, pack8<BF>(dy), 8);
+          most_of(m, du[e]);
+          du[e] *= scale;
         }
       }
     }
+    if (p.D) {
+      store8(p.D + (r * p.ldd + c) * 2, pack8<BF>(d), 8);
+      if constexpr (GLU) store8(p.D + (r * p.ldd + p.width + c) * 2, pack8<BF>(du), 8);
+    }
+  });
+  if constexpr (!BF) {
+    __shared__ float sm[4];
+    if (p.undo) {
+      m = group_max(m, sm);
+      if (threadIdx.x == 0) p.most[blockIdx.x] = m;
+      if (threadIdx.x == 0 && blockIdx.x == 0) *p.undo = 1.0f / ACT_SCALE;
+    }
   }
   if (!p.sums) return;
+  const int by = blockIdx.x / p.groups, bx = blockIdx.x - by * p.groups;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     part[0][wave][lane * 8 + e] = s1[e];

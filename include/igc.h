@@ -327,7 +327,11 @@ int conv2d_u8i8_zp_workspace_size(int Nb, int H, int W, int C, int Kout, int R, 
  *  - `type` is the type of the operands, of D and of every output that names
  *    no other: IGC_F16 or IGC_BF16.  Products accumulate in fp32; bias,
  *    activation and residual are applied to the fp32 sums, rounded once.
- *    The backward products take D (below) rounded to `type`.
+ *    The backward products take D (below) rounded to `type`, which adds to
+ *    the error of dX and dW about as much as their own rounding.  In fp16 D
+ *    (of the gated block: dG and dU together) is scaled by a power of two that
+ *    fits its largest element and is taken back exactly, so gradients that
+ *    fp16 holds are not lost where D itself would leave its range.
  *  - Matrices are row-major with any leading dimension >= their row length
  *    and any alignment their element type allows.  16-byte aligned operands
  *    with leading dimensions and row lengths that are multiples of 8 take
