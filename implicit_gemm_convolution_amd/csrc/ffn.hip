@@ -39,6 +39,16 @@ struct Checker {
     fail_if(M < 0 || N < 0 || K < 0, "negative size");
     fail_if(type != IGC_F16 && type != IGC_BF16, "type must be IGC_F16 or IGC_BF16");
     fail_if(act < IGC_ACT_NONE || act > IGC_ACT_SIGMOID, "unknown activation");
+    extent("M", M, MOST);
+    extent("N", N, MOST);
+    extent("K", K, MOST);
+  }
+  // The kernels index rows, columns and the reduction in 32 bits and step past
+  // the end by a tile, a batch of K tiles or (the element-wise rows) four
+  // workgroups per compute unit: all less than 4096.
+  static constexpr int MOST = 0x7fffffff - 4095;
+  void extent(const char* name, int n, int most) {
+    if (ok() && n > most) status = fail(IGC_EUNSUPPORTED, "%s = %d > %d", name, n, most);
   }
 };
 
@@ -299,8 +309,7 @@ bool plan_back(Plan& px, Plan& pw, long long M, long long K, long long red, bool
 int backward(const Backward& b, size_t* query, hipStream_t stream) {
   const bool sums = b.db || b.db2;
   const int np = b.glu ? 2 : 1;
-  const int width = (int)std::min<long long>(ceil_div(b.N, 64) * 64, 0x7fffffc0);
-  if (b.glu && width > (1 << 30)) return fail(IGC_EUNSUPPORTED, "N too large");
+  const int width = (int)ceil_div(b.N, 64) * 64;
   int dev;
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
@@ -473,6 +482,7 @@ int glu_backward_impl(const igc_glu_backward* d, size_t* query, hipStream_t stre
   c.fail_if(!d, "descriptor is NULL");
   if (!c.ok()) return c.status;
   c.problem(d->M, d->N, d->K, d->type, d->act);
+  c.extent("N", d->N, Checker::MOST / 2);  // (dG and dU lie side by side)
   c.fail_if(!d->dX && !d->dWg && !d->dWu && !d->dbias_g && !d->dbias_u, "no output requested");
   c.matrix("dH", d->dH, d->lddh, d->M, d->N, 2, false);
   c.matrix("G", d->G, d->ldg, d->M, d->N, 2, false);

@@ -345,6 +345,8 @@ int conv2d_u8i8_zp_workspace_size(int Nb, int H, int W, int C, int Kout, int R, 
  *    does not matter, so calls of any kind and size may take turns with one
  *    workspace on one stream (the entry points above want theirs zeroed).
  *    Results do not depend on the order in which workgroups finish.
+ *  - M, N and K go up to 2^31 - 4096, N of glu_backward up to 2^30 - 2048;
+ *    larger ones return IGC_EUNSUPPORTED.
  *  - Outputs must not overlap inputs or one another (grad_clip may write in
  *    place).
  *  - Activations, with f' as its derivative:
@@ -377,7 +379,8 @@ int conv2d_u8i8_zp_workspace_size(int Nb, int H, int W, int C, int Kout, int R, 
  *         backward pass, or NULL
  * Errors: IGC_EINVAL (NULL descriptor or operand, negative size, leading
  * dimension below the row length, unknown type or activation, misaligned
- * pointer, workspace too small), IGC_ENODEV, IGC_EHIP.
+ * pointer, workspace too small), IGC_EUNSUPPORTED (too large), IGC_ENODEV,
+ * IGC_EHIP.
  */
 typedef struct igc_linear_forward {
   int M, N, K;

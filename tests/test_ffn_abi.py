@@ -154,3 +154,24 @@ def test_without_torch_the_descriptors_go_through_ctypes(igc, monkeypatch):
     _rejects(igc, igc.linear_forward, good, [dict(ldx=7), dict(W=None), dict(Y=P + 1), dict(Z=P, ldz=5), dict(R=P, ldr=5)])
     with pytest.raises(RuntimeError, match="torch"):
         igc.grad_clip([], 1.0, P, stream=0)
+
+
+def test_sizes_past_the_index_arithmetic(igc):
+    """Extents within a tile of 2^31 (2^30 where two matrices lie side by side) are refused, by the calls and the queries."""
+    most = 2 ** 31 - 4096
+    ld = 2 ** 31 - 1
+    lin = dict(M=4, N=6, K=8, dY=P, lddy=ld, Z=P, ldz=ld, X=P, ldx=ld, W=P, ldw=ld, dX=P, lddx=ld, dW=P, lddw=ld, dbias=P, act=igc.IGC_ACT_SILU)
+    fwd = dict(M=4, N=6, K=8, X=P, ldx=ld, W=P, ldw=ld, Y=P, ldy=ld)
+    glu = dict(M=4, N=6, K=8, X=P, ldx=ld, Wg=P, ldwg=ld, Wu=P, ldwu=ld, H=P, ldh=ld)
+    back = dict(M=4, N=6, K=8, dH=P, lddh=ld, G=P, ldg=ld, U=P, ldu=ld, X=P, ldx=ld, Wg=P, ldwg=ld, Wu=P, ldwu=ld, dX=P, lddx=ld,
+                dWg=P, lddwg=ld, dWu=P, lddwu=ld)
+    for name, good in (("linear_forward", fwd), ("linear_backward", lin), ("glu_forward", glu), ("glu_backward", back)):
+        call, query = getattr(igc, name), getattr(igc, name + "_workspace_size")
+        for axis in "MNK":
+            top = 2 ** 30 - 2048 if (name, axis) == ("glu_backward", "N") else most
+            for n in (top + 1, 2 ** 31 - 64, 2 ** 31 - 1):
+                bad = {**good, axis: n}
+                assert call(**bad, check=False) == igc.IGC_EUNSUPPORTED, (name, axis, n)
+                with pytest.raises(igc.IGCError, match=axis) as e:
+                    query(**bad)
+                assert e.value.status == igc.IGC_EUNSUPPORTED
