@@ -168,6 +168,7 @@ int forward(GemmArgs& a, int type, void* ws, size_t ws_bytes, size_t* query, hip
       if (ib >= 0) a.B = pads.place(ib, to), a.ldb = Pads::padded(a.R);
       if (ib2 >= 0) a.B2 = pads.place(ib2, to), a.ldb2 = Pads::padded(a.R);
       a.R = a.r_split = a.b_rows = (int)Pads::padded(a.R);
+      a.odd_rows = 0;
     } else {
       pads = Pads();
     }

@@ -50,3 +50,19 @@ def test_largest_extents_keep_their_sizes(host):
     assert status == 0 and [p["R"] for p in products] == [n] and need >= 2 * n
     m = 2 ** 31 - 1
     assert host("linear_backward", **{**lin, "N": m, "lddy": m, "ldz": m}) == (-2, 0, [], [])
+
+
+@pytest.mark.parametrize("entry", ["linear_forward", "glu_forward"])
+@pytest.mark.parametrize("M", [1, 16, 64])
+def test_padded_rows_take_the_kernel_of_aligned_rows(host, entry, M):
+    """X at an odd 2-byte offset and a wide aligned weight: X is copied into aligned rows, and the product loads those."""
+    N, K = 16384, 4096
+    odd, good = P + 2, P
+    weights = dict(W=good, ldw=K, Y=P, ldy=N, y_type=1) if entry == "linear_forward" else dict(Wg=good, ldwg=K, Wu=good, ldwu=K, H=P, ldh=N)
+    _, _, (aligned,), _ = host(entry, M=M, N=N, K=K, type=1, X=good, ldx=K, **weights)
+    status, _, (p,), launches = host(entry, M=M, N=N, K=K, type=1, X=odd, ldx=K, **weights)
+    assert status == 0 and launches == ["(igc_ffn::pad_kernel<0>)"]
+    assert p == aligned and p["odd"] == 0
+    # without a workspace nothing is padded
+    status, _, (p,), launches = host(entry, M=M, N=N, K=K, type=1, X=odd, ldx=K, workspace=0, **weights)
+    assert status == 0 and not launches and p["odd"] == 1
