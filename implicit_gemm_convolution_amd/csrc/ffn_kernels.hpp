@@ -235,7 +235,8 @@ __device__ __forceinline__ void act_one(float z, float& f, float& d) {
     const float w = __builtin_fmaf(z2, -2.0f * kGeluC * kGeluA * 1.44269504088896341f, -2.0f * kGeluC * 1.44269504088896341f);
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * w));
     f = z * s;
-    if constexpr (SLOPE) d = s + f * (1.0f - s) * (2.0f * kGeluC) * __builtin_fmaf(3.0f * kGeluA, z2, 1.0f);
+    // (s is 0 or 1 long before z2 could overflow: 0 times infinity)
+    if constexpr (SLOPE) d = s + f * (1.0f - s) * (2.0f * kGeluC) * __builtin_fmaf(3.0f * kGeluA, __builtin_fminf(z2, 1e30f), 1.0f);
   } else {
     const float s = sigmoid_f(z);
     if constexpr (ACT == ACT_SILU) {
