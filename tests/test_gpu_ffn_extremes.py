@@ -25,3 +25,17 @@ def test_slopes_of_extreme_sums(torch, igc, ws, act):  # noqa: F811
     dbg, dbu = torch.empty_like(db), torch.empty_like(db)
     igc.glu_backward(1, N, 8, dY, N, z, N, dY, N, dbias_g=dbg, dbias_u=dbu, act=_act_id(igc, act), workspace=ws)
     assert torch.equal(dbg, ref) and torch.equal(dbu, f)
+
+
+def test_tail_of_gelu_relative_to_its_size(torch, igc, ws):  # noqa: F811
+    """fp32 outputs down to gelu(-12.5) = -4.7e-35.  Relative to the value, in u = 2^-24: the exponent -z^2/2 log2(e) takes two
+    roundings and that of the constant (2.3 u, times z^2 / 2 in the exponential: 1.2 z^2 u); its exponential 2 u, the reciprocal
+    2 u, the fitted factor 7 u, x 3 u, four products and the store 5 u."""
+    z = -torch.linspace(0.5, 12.5, 4800, device="cuda")
+    N = z.numel()
+    one, zero = torch.ones(1, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(N, 8, dtype=torch.bfloat16, device="cuda")
+    Y = torch.empty(1, N, device="cuda")
+    igc.linear_forward(1, N, 8, one, 8, zero, 8, Y, N, y_type=igc.IGC_F32, bias=z, act=igc.IGC_ACT_GELU, workspace=ws)
+    ref = _f("gelu", z.double())[0]
+    bad = ~((Y[0].double() - ref).abs() <= (20 + 1.2 * z.double() ** 2) * U * ref.abs())
+    assert not bool(bad.any()), (int(bad.sum()), z[bad][:4], Y[0][bad][:4], ref[bad][:4])
