@@ -5,6 +5,7 @@
 // tensors, one Python call per property of each: 37).
 #include <Python.h>
 
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -155,6 +156,19 @@ struct Tensors {
   }
 };
 
+// The kernels take addresses of the current device only; with a Python error,
+// false for a tensor of another.
+bool on_device(const at::Tensor& t) {
+  if (!t.is_cuda()) {
+    PyErr_Format(PyExc_TypeError, "grad_clip takes tensors on the GPU, not on %s", t.device().str().c_str());
+    return false;
+  }
+  const c10::Device current = c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice();
+  if (t.device() == current) return true;
+  PyErr_Format(PyExc_ValueError, "a tensor on %s in a call on %s", t.device().str().c_str(), current.str().c_str());
+  return false;
+}
+
 // clip(entry, query, stream, ws, ws_bytes, grads, outs or None, max_norm, norm)
 // -> status, or with query (status, bytes).
 PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -201,6 +215,17 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return nullptr;
       }
       to[i] = o->data_ptr();
+    }
+    if (THPVariable_Check(args[8])) {
+      const at::Tensor& t = THPVariable_Unpack(args[8]);
+      if (t.scalar_type() != at::kFloat || t.numel() < 1)
+        return PyErr_Format(PyExc_TypeError, "norm must be a float32 tensor of one element");
+    }
+    if (!query) {
+      for (Py_ssize_t i = 0; i < grads.n; ++i)
+        if (!on_device(*grads(i)) || (out && !on_device(*outs(i)))) return nullptr;
+      for (PyObject* const o : {args[8], args[3]})
+        if (THPVariable_Check(o) && !on_device(THPVariable_Unpack(o))) return nullptr;
     }
     igc_grad_clip d;
     std::memset(&d, 0, sizeof(d));

@@ -175,3 +175,20 @@ def test_sizes_past_the_index_arithmetic(igc):
                 with pytest.raises(igc.IGCError, match=axis) as e:
                     query(**bad)
                 assert e.value.status == igc.IGC_EUNSUPPORTED
+
+
+def test_grad_clip_refuses_tensors_of_another_device_and_norms_of_another_type(igc):
+    """Nothing but addresses of the GPU reaches the kernels; the size query reads no tensor and takes any device's."""
+    import torch
+
+    a, norm = torch.zeros(4, 6), torch.zeros(1)
+    for bad in (torch.zeros(1, dtype=torch.float64), torch.zeros(1, dtype=torch.bfloat16), torch.zeros(0)):
+        with pytest.raises(TypeError, match="norm must be a float32"):
+            igc.grad_clip([a], 1.0, bad, workspace=P, ws_bytes=1 << 20, stream=0)
+    with pytest.raises(TypeError, match="on the GPU, not on cpu"):
+        igc.grad_clip([a], 1.0, P, workspace=P, ws_bytes=1 << 20, stream=0)
+    with pytest.raises(TypeError, match="on the GPU, not on cpu"):
+        igc.grad_clip([], 1.0, norm, workspace=P, ws_bytes=1 << 20, stream=0)
+    with pytest.raises(TypeError, match="on the GPU, not on cpu"):
+        igc.grad_clip([], 1.0, P, workspace=torch.zeros(1 << 16, dtype=torch.uint8), stream=0)
+    assert igc.grad_clip_workspace_size([a], 1.0, norm) > 0
