@@ -1,5 +1,6 @@
 """Build libigc.so (the HIP kernels and the C ABI) in-tree with hipcc for gfx950,
-and _marshal.so (the Python binding's marshalling, host code only) with g++.
+and, where torch is installed, _marshal.so (the Python binding's marshalling,
+host code only) with g++.
 
 The C ABI (csrc/igc.hip, csrc/ffn.hip) and the kernel instantiations
 (csrc/igc_launch.hip and csrc/ffn_launch.hip, compiled once per kernel kind
@@ -63,10 +64,13 @@ def _jobs() -> int:
     return max(1, min(n, 16, LAUNCH_UNITS + 1))
 
 
-def marshal_command(out: str) -> list:
-    """The command that compiles _marshal.so against the installed Python and torch."""
-    import torch
-    from torch.utils import cpp_extension
+def marshal_command(out: str) -> list | None:
+    """The command that compiles _marshal.so against the installed Python and torch; None without torch."""
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError:
+        return None
 
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -76,11 +80,12 @@ def marshal_command(out: str) -> list:
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Compile every source; libigc.so and _marshal.so go next to this file.  Returns libigc.so's path."""
+    """Compile every source; libigc.so and (where torch is installed) _marshal.so go next to this file.  Returns libigc.so's path."""
     tmpdir = tempfile.mkdtemp(prefix="igc_build_")
     try:
         marshal = os.path.join(tmpdir, "_marshal.so")
-        cmds = [marshal_command(marshal)]  # (among the longest: first)
+        extension = marshal_command(marshal)
+        cmds = [extension] if extension else []  # (among the longest: first)
         for src, defs, obj in _units():
             cmds.append([HIPCC, *HIP_FLAGS, *extra_flags, *defs, "-c", src, "-o", os.path.join(tmpdir, obj)])
 
@@ -96,8 +101,9 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         link = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
         run(link)
         os.replace(tmp, LIB_PATH)
-        shutil.copyfile(marshal, MARSHAL_PATH + ".tmp")
-        os.replace(MARSHAL_PATH + ".tmp", MARSHAL_PATH)
+        if extension:
+            shutil.copyfile(marshal, MARSHAL_PATH + ".tmp")
+            os.replace(MARSHAL_PATH + ".tmp", MARSHAL_PATH)
     finally:
         shutil.rmtree(tmpdir, ignore_errors=True)
     return LIB_PATH
