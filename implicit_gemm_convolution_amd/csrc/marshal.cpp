@@ -157,13 +157,13 @@ struct Tensors {
 };
 
 // The kernels take addresses of the current device only; with a Python error,
-// false for a tensor of another.
-bool on_device(const at::Tensor& t) {
+// false for a tensor of another.  (`current` is asked for once a call.)
+bool on_device(const at::Tensor& t, c10::Device& current) {
   if (!t.is_cuda()) {
     PyErr_Format(PyExc_TypeError, "grad_clip takes tensors on the GPU, not on %s", t.device().str().c_str());
     return false;
   }
-  const c10::Device current = c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice();
+  if (!current.is_cuda()) current = c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice();
   if (t.device() == current) return true;
   PyErr_Format(PyExc_ValueError, "a tensor on %s in a call on %s", t.device().str().c_str(), current.str().c_str());
   return false;
@@ -222,10 +222,11 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return PyErr_Format(PyExc_TypeError, "norm must be a float32 tensor of one element");
     }
     if (!query) {
+      c10::Device current(c10::DeviceType::CPU);
       for (Py_ssize_t i = 0; i < grads.n; ++i)
-        if (!on_device(*grads(i)) || (out && !on_device(*outs(i)))) return nullptr;
+        if (!on_device(*grads(i), current) || (out && !on_device(*outs(i), current))) return nullptr;
       for (PyObject* const o : {args[8], args[3]})
-        if (THPVariable_Check(o) && !on_device(THPVariable_Unpack(o))) return nullptr;
+        if (THPVariable_Check(o) && !on_device(THPVariable_Unpack(o), current)) return nullptr;
     }
     igc_grad_clip d;
     std::memset(&d, 0, sizeof(d));
