@@ -84,13 +84,19 @@ class Network:
     def grads(self):
         return [t for b in self.blocks for t in b.grads] + [self.dW, self.db]
 
+    def _forward_workspace(self, M):
+        """The most that one forward call of M rows asks for (fewer rows may ask for more: their reductions are split)."""
+        K, N, C, b = self.width, self.hidden, self.outputs, self.blocks[0]
+        return max(
+            igc.glu_forward_workspace_size(M, N, K, b.out, K, b.Wg, K, b.Wu, K, b.H, N, G=b.G, ldg=N, U=b.U, ldu=N, type=TYPE),
+            igc.linear_forward_workspace_size(M, K, N, b.H, N, b.W3, N, b.out, K, R=b.out, ldr=K, type=TYPE),
+            igc.linear_forward_workspace_size(M, C, K, b.out, K, self.W, K, self.y, C, type=TYPE, y_type=igc.IGC_F32))
+
     def _workspace(self):
         """The most that one call of a step asks for."""
         M, K, N, C, b = self.batch, self.width, self.hidden, self.outputs, self.blocks[0]
         return max(
-            igc.glu_forward_workspace_size(M, N, K, b.out, K, b.Wg, K, b.Wu, K, b.H, N, G=b.G, ldg=N, U=b.U, ldu=N, type=TYPE),
-            igc.linear_forward_workspace_size(M, K, N, b.H, N, b.W3, N, b.out, K, R=b.out, ldr=K, type=TYPE),
-            igc.linear_forward_workspace_size(M, C, K, b.out, K, self.W, K, self.y, C, type=TYPE, y_type=igc.IGC_F32),
+            self._forward_workspace(M),
             igc.linear_backward_workspace_size(M, C, K, self.dy, C, X=b.out, ldx=K, W=self.W, ldw=K, dX=self.dx, lddx=K, dW=self.dW,
                                                lddw=K, dbias=self.db, type=TYPE),
             igc.linear_backward_workspace_size(M, K, N, b.out, K, X=b.H, ldx=N, W=b.W3, ldw=N, dX=b.dH, lddx=N, dW=b.grads[2],
@@ -100,15 +106,15 @@ class Network:
                                             dbias_u=b.grads[4], type=TYPE),
             igc.grad_clip_workspace_size(self.grads(), 1.0, self.norm), 256)
 
-    def head(self, x, y):
+    def head(self, x, y, ws):
         K, C = self.width, self.outputs
-        igc.linear_forward(x.shape[0], C, K, x, K, self.W, K, y, C, y_type=igc.IGC_F32, bias=self.b, type=TYPE, workspace=self.ws)
+        igc.linear_forward(x.shape[0], C, K, x, K, self.W, K, y, C, y_type=igc.IGC_F32, bias=self.b, type=TYPE, workspace=ws)
         return y
 
     def forward(self, x):
         for b in self.blocks:
             x = b.forward(x, self.ws)
-        return self.head(x, self.y)
+        return self.head(x, self.y, self.ws)
 
     def step(self, x, target, rate, max_norm):
         """One step of gradient descent on the mean squared error."""
@@ -132,10 +138,13 @@ class Network:
     def serve(self, x):
         """The outputs of a few tokens (any number of rows up to the batch)."""
         M = x.shape[0]
+        need = self._forward_workspace(M)
+        # (not in the step's place: a captured step still writes there)
+        ws = self.ws if need <= self.ws.numel() else torch.empty(need, dtype=torch.uint8, device="cuda")
         H = torch.empty(M, self.hidden, dtype=KIND, device="cuda")
         for b in self.blocks:
-            x = b.forward(x, self.ws, keep=False, H=H, out=torch.empty(M, self.width, dtype=KIND, device="cuda"))
-        return self.head(x, torch.empty(M, self.outputs, device="cuda"))
+            x = b.forward(x, ws, keep=False, H=H, out=torch.empty(M, self.width, dtype=KIND, device="cuda"))
+        return self.head(x, torch.empty(M, self.outputs, device="cuda"), ws)
 
 
 def train(steps=60, blocks=2, width=512, hidden=1368, outputs=96, batch=384, rate=0.3, max_norm=0.5, graph=True, report=print):
