@@ -17,6 +17,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import sys
 
@@ -375,9 +376,17 @@ def _entry(name) -> int:
     return _entries[1][name]
 
 
+def _int32(v) -> int:
+    """A whole number that an int of the descriptor holds (ctypes would cut it to 32 bits)."""
+    v = operator.index(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise OverflowError("%d does not fit in 32 bits" % v)
+    return v
+
+
 def _describe(name, fields, workspace, ws_bytes):
     """The entry point's descriptor."""
-    values = [_addr(v) if kind == "p" else v for kind, v in zip(_FORMATS[name], fields)]
+    values = [_addr(v) if kind == "p" else _int32(v) for kind, v in zip(_FORMATS[name], fields)]
     return _DESCRIPTORS[name](*values, _addr(workspace), _ws_bytes(workspace, ws_bytes))
 
 

@@ -192,3 +192,23 @@ def test_grad_clip_refuses_tensors_of_another_device_and_norms_of_another_type(i
     with pytest.raises(TypeError, match="on the GPU, not on cpu"):
         igc.grad_clip([], 1.0, P, workspace=torch.zeros(1 << 16, dtype=torch.uint8), stream=0)
     assert igc.grad_clip_workspace_size([a], 1.0, norm) > 0
+
+
+def test_size_queries_take_the_numbers_that_the_calls_take(igc):
+    """Whole numbers of any type; one that an int does not hold is not cut to 32 bits."""
+    import numpy as np
+
+    good = dict(M=0, N=6, K=8, X=P, ldx=8, W=P, ldw=8, Y=P, ldy=6)
+    assert igc.linear_forward_workspace_size(**{**good, "N": np.int64(6), "ldx": np.int32(8)}) == 0
+    for bad in (dict(ldx=2 ** 32 + 8), dict(M=2 ** 32), dict(N=-2 ** 31 - 1)):
+        with pytest.raises(OverflowError):
+            igc.linear_forward_workspace_size(**{**good, **bad})
+    with pytest.raises(TypeError):
+        igc.linear_forward_workspace_size(**{**good, "M": 0.0})
+
+
+def test_without_torch_numbers_are_not_cut(igc, monkeypatch):
+    monkeypatch.setattr(igc.binding, "_native", False)
+    good = dict(M=0, N=6, K=8, X=P, ldx=8, W=P, ldw=8, Y=P, ldy=6, stream=0)
+    with pytest.raises(OverflowError):
+        igc.linear_forward(**{**good, "M": 2 ** 32})
