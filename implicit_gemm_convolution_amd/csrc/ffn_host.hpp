@@ -68,11 +68,12 @@ inline bool dma_operand(const void* p, long long ld, long long length) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0 && length > 0 && length % 8 == 0 && ld <= (1 << 21) - 8;
 }
 
-// What a launch of the aligned tiles takes, in us, fitted to 2700 timings on
-// MI355X (bf16; 55 outputs of 16 x 4096 to 8192 x 8192, reductions of 300 to
-// 30000, one to sixteen splits).  Over those products the plan with the
-// smallest estimate takes 1.1% longer than the fastest one in the mean and 19%
-// at most (gated block 0.3% and 19%).  Tiles chosen by how many fill the card,
+// What a launch of the aligned tiles takes, in us, fitted to timings on MI355X
+// (bf16; 52 outputs of 16 x 4096 to 8192 x 8192 in the four layouts, reductions
+// of 300 to 30000, one to sixteen splits; profiles/ has them).  Over 197 of
+// those products, 2001 timings, the plan with the smallest estimate takes 1.2%
+// longer than the fastest one in the mean and 18% at most (gated block 0.8%
+// and 10%).  Tiles chosen by how many fill the card,
 // split only below one per compute unit: 5%, and twice as long at
 // 640 x 2432 x 27392.
 //   k0, k1, k2  a K tile of 64 in an empty card; with one workgroup on every
