@@ -182,3 +182,42 @@ def test_gradients_of_zero(torch, igc, ws):  # noqa: F811
     igc.linear_backward(M, N, K, zero, N, Z=one, ldz=N, X=one, ldx=K, W=one, ldw=K, dX=dX, lddx=K, dW=dW, lddw=K, type=igc.IGC_F16,
                         act=igc.IGC_ACT_GELU, workspace=ws)
     assert int(dX.count_nonzero()) == 0 and int(dW.count_nonzero()) == 0
+
+
+def test_replays_with_gradients_of_changing_size(torch, igc):  # noqa: F811
+    """A captured backward pass finds D's scale anew on every replay."""
+    M, N, K = 200, 333, 264
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(10)
+    new = lambda r, c: torch.empty(r, c, dtype=torch.float16, device="cuda")  # noqa: E731
+    unit, Z, G = (torch.randn(M, N, generator=gen, device="cuda") for _ in range(3))
+    Z, G, dY = Z.half(), G.half(), new(M, N)
+    X, W, V = ((torch.randn(r, K, generator=gen, device="cuda") * 2.0 ** -6).half() for r in (M, N, N))
+    dX, dW, hX, hW, hV = new(M, K), new(N, K), new(M, K), new(N, K), new(N, K)
+    space = torch.full((32 << 20,), 255, dtype=torch.uint8, device="cuda")
+
+    def step():
+        igc.linear_backward(M, N, K, dY, N, Z=Z, ldz=N, X=X, ldx=K, W=W, ldw=K, dX=dX, lddx=K, dW=dW, lddw=K, type=igc.IGC_F16,
+                            act=igc.IGC_ACT_GELU, workspace=space)
+        igc.glu_backward(M, N, K, dY, N, G, N, Z, N, X=X, ldx=K, Wg=W, ldwg=K, Wu=V, ldwu=K, dX=hX, lddx=K, dWg=hW, lddwg=K, dWu=hV,
+                         lddwu=K, type=igc.IGC_F16, workspace=space)
+
+    outs = [dX, dW, hX, hW, hV]
+    dY.copy_(unit)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for std in (1.0, 2000.0, 1e-7, 1.0, 1e-2, 2000.0):
+        dY.copy_(unit * std)
+        for t in outs:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        step()
+        torch.cuda.synchronize()
+        for g, t in zip(got, outs):
+            assert bool(torch.isfinite(t).all()) and torch.equal(g, t), std
