@@ -316,7 +316,7 @@ def _act(name, z):
 
 def _plain_rows(x):
     """Rows in 8 bits (as whole fp32 numbers) and their scales.  127 x is exact, and of 16-bit values no quotient but a tie
-    lies within 2^-13 of its size of a tie: rounded once to fp32 it goes where the exact one goes."""
+    lies within 2^-19 of its size of a tie: rounded once to fp32 it goes where the exact one goes."""
     top = x.float().abs().amax(1, keepdim=True)
     return torch.round(127 * x.float() / top), top / 127
 
