@@ -51,6 +51,7 @@ EXPORTED = ("gemm_f16f32", "gemm_u8i8_zp", "conv2d_implicit_gemm", "conv2d_u8i8_
             "linear_forward", "linear_forward_workspace_size", "linear_backward", "linear_backward_workspace_size",
             "glu_forward", "glu_forward_workspace_size", "glu_backward", "glu_backward_workspace_size",
             "grad_clip", "grad_clip_workspace_size",
+            "layer_norm_forward", "layer_norm_backward", "layer_norm_backward_workspace_size", "dropout", "quantize_rows",
             "igc_status_string", "igc_last_error", "igc_device_check", "igc_set_tuning")
 
 
@@ -79,8 +80,8 @@ class Epilogue(ctypes.Structure):
 
 
 def _fields(text):
-    """Structure fields from "name:kind" words: i int, p pointer, f float, z size_t."""
-    kinds = {"i": ctypes.c_int, "p": ctypes.c_void_p, "f": ctypes.c_float, "z": ctypes.c_size_t}
+    """Structure fields from "name:kind" words: i int, p pointer, f float, d double, l uint64_t, z size_t."""
+    kinds = {"i": ctypes.c_int, "p": ctypes.c_void_p, "f": ctypes.c_float, "d": ctypes.c_double, "l": ctypes.c_uint64, "z": ctypes.c_size_t}
     return [(w.split(":")[0], kinds[w.split(":")[1]]) for w in text.split()]
 
 
@@ -113,11 +114,40 @@ class GradClip(ctypes.Structure):
     _fields_ = _fields("count:i grads:p outs:p sizes:p types:p max_norm:f norm:p workspace:p ws_bytes:z")
 
 
+class LayerNormForward(ctypes.Structure):
+    """igc_layer_norm_forward."""
+    _fields_ = _fields("M:i N:i type:i x_type:i eps:f X:p ldx:i gamma:p beta:p Y:p ldy:i mean:p rstd:p Q:p ldq:i scale:p")
+
+
+class LayerNormBackward(ctypes.Structure):
+    """igc_layer_norm_backward."""
+    _fields_ = _fields("M:i N:i type:i x_type:i dY:p lddy:i X:p ldx:i mean:p rstd:p gamma:p R:p ldr:i dX:p lddx:i dgamma:p dbeta:p "
+                       "workspace:p ws_bytes:z")
+
+
+class Dropout(ctypes.Structure):
+    """igc_dropout."""
+    _fields_ = _fields("M:i N:i type:i y_type:i p:d seed:l offset:l step:p X:p ldx:i R:p ldr:i Y:p ldy:i")
+
+
+class QuantizeRows(ctypes.Structure):
+    """igc_quantize_rows."""
+    _fields_ = _fields("M:i N:i type:i X:p ldx:i Q:p ldq:i scale:p")
+
+
 # The entry points that take a descriptor: its structure, and for _marshal
-# its fields before the workspace.
+# its fields before the workspace (which not every one has).
 _DESCRIPTORS = {"linear_forward": LinearForward, "linear_backward": LinearBackward, "glu_forward": GluForward,
-                "glu_backward": GluBackward, "grad_clip": GradClip}
-_FORMATS = {name: "".join("i" if kind is ctypes.c_int else "p" for _, kind in desc._fields_[:-2])
+                "glu_backward": GluBackward, "grad_clip": GradClip, "layer_norm_forward": LayerNormForward,
+                "layer_norm_backward": LayerNormBackward, "dropout": Dropout, "quantize_rows": QuantizeRows}
+_LETTERS = {ctypes.c_int: "i", ctypes.c_void_p: "p", ctypes.c_float: "f", ctypes.c_double: "d", ctypes.c_uint64: "l"}
+
+
+def _has_workspace(name):
+    return _DESCRIPTORS[name]._fields_[-1][0] == "ws_bytes"
+
+
+_FORMATS = {name: "".join(_LETTERS.get(kind, "p") for _, kind in (desc._fields_[:-2] if _has_workspace(name) else desc._fields_))
             for name, desc in _DESCRIPTORS.items()}
 
 _lib = None
@@ -163,8 +193,9 @@ def load() -> ctypes.CDLL:
     for name, desc in _DESCRIPTORS.items():
         getattr(L, name).argtypes = [ctypes.POINTER(desc), p]
         getattr(L, name).restype = i
-        getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(desc), pz]
-        getattr(L, name + "_workspace_size").restype = i
+        if _has_workspace(name):
+            getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(desc), pz]
+            getattr(L, name + "_workspace_size").restype = i
     L.igc_set_tuning.argtypes = [i, i]
     L.igc_set_tuning.restype = i
     L.igc_status_string.argtypes = [i]
@@ -372,7 +403,7 @@ def _entry(name) -> int:
     L = load()
     if _entries is None or _entries[0] is not L:
         _entries = L, {n + q: ctypes.cast(getattr(L, n + q), ctypes.c_void_p).value
-                       for n in _DESCRIPTORS for q in ("", "_workspace_size")}
+                       for n in _DESCRIPTORS for q in (("", "_workspace_size") if _has_workspace(n) else ("",))}
     return _entries[1][name]
 
 
@@ -384,10 +415,23 @@ def _int32(v) -> int:
     return v
 
 
+def _uint64(v) -> int:
+    """A whole number that a uint64_t of the descriptor holds."""
+    v = operator.index(v)
+    if not 0 <= v < 2 ** 64:
+        raise OverflowError("%d does not fit in an unsigned number of 64 bits" % v)
+    return v
+
+
+_CONVERT = {"p": _addr, "i": _int32, "f": float, "d": float, "l": _uint64}
+
+
 def _describe(name, fields, workspace, ws_bytes):
     """The entry point's descriptor."""
-    values = [_addr(v) if kind == "p" else _int32(v) for kind, v in zip(_FORMATS[name], fields)]
-    return _DESCRIPTORS[name](*values, _addr(workspace), _ws_bytes(workspace, ws_bytes))
+    values = [_CONVERT[kind](v) for kind, v in zip(_FORMATS[name], fields)]
+    if _has_workspace(name):
+        values += [_addr(workspace), _ws_bytes(workspace, ws_bytes)]
+    return _DESCRIPTORS[name](*values)
 
 
 def _call(name, check, stream, workspace, ws_bytes, *fields) -> int:
@@ -474,3 +518,38 @@ def grad_clip_workspace_size(grads, max_norm, norm, *, out=None) -> int:
     st, size = _clip("grad_clip_workspace_size", True, None, None, None, grads, out, max_norm, norm)
     _check(st, "grad_clip_workspace_size")
     return size
+
+
+# ---------------------------------------------------------------------------
+# What stands around the feed-forward products.
+# ---------------------------------------------------------------------------
+def layer_norm_forward(M, N, X, ldx, Y, ldy, *, gamma=None, beta=None, eps=1e-5, mean=None, rstd=None, Q=None, ldq=0, scale=None,
+                       type=IGC_BF16, x_type=None, stream=None, check=True) -> int:
+    """Y = (X - mean) rstd gamma + beta over each row, and the same in 8 bits into Q (x_type None: `type`)."""
+    return _call("layer_norm_forward", check, stream, None, None, M, N, type, type if x_type is None else x_type, eps, X, ldx, gamma, beta,
+                 Y, ldy, mean, rstd, Q, ldq, scale)
+
+
+def layer_norm_backward(M, N, dY, lddy, X, ldx, mean, rstd, *, gamma=None, R=None, ldr=0, dX=None, lddx=0, dgamma=None, dbeta=None,
+                        type=IGC_BF16, x_type=None, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """The gradients of layer_norm_forward, R added to dX (any subset)."""
+    return _call("layer_norm_backward", check, stream, workspace, ws_bytes, M, N, type, type if x_type is None else x_type, dY, lddy, X, ldx,
+                 mean, rstd, gamma, R, ldr, dX, lddx, dgamma, dbeta)
+
+
+def layer_norm_backward_workspace_size(M, N, dY, lddy, X, ldx, mean, rstd, *, gamma=None, R=None, ldr=0, dX=None, lddx=0, dgamma=None,
+                                       dbeta=None, type=IGC_BF16, x_type=None) -> int:
+    return _query("layer_norm_backward", M, N, type, type if x_type is None else x_type, dY, lddy, X, ldx, mean, rstd, gamma, R, ldr,
+                  dX, lddx, dgamma, dbeta)
+
+
+def dropout(M, N, X, ldx, Y, ldy, p, seed, offset=0, *, step=None, R=None, ldr=0, type=IGC_BF16, y_type=None, stream=None,
+            check=True) -> int:
+    """Y = X / (1 - p) where the generator keeps it, else 0, + R; the same call on dY without R gives dX."""
+    return _call("dropout", check, stream, None, None, M, N, type, type if y_type is None else y_type, p, seed, offset, step, X, ldx, R, ldr,
+                 Y, ldy)
+
+
+def quantize_rows(M, N, X, ldx, Q, ldq, scale, *, type=IGC_BF16, stream=None, check=True) -> int:
+    """Each row in 8 bits: scale = max|X| / 127, Q = round(127 X / max|X|)."""
+    return _call("quantize_rows", check, stream, None, None, M, N, type, X, ldx, Q, ldq, scale)

@@ -2,7 +2,7 @@
 and, where torch is installed, _marshal.so (the Python binding's marshalling,
 host code only) with g++.
 
-The C ABI (csrc/igc.hip, csrc/ffn.hip) and the kernel instantiations
+The C ABI (csrc/igc.hip, csrc/ffn.hip, csrc/rows.hip) and the kernel instantiations
 (csrc/igc_launch.hip and csrc/ffn_launch.hip, compiled once per kernel kind
 with -DIGC_LAUNCH_UNIT=<n> and -DIGC_FFN_UNIT=<n>) are separate objects
 compiled in parallel, then linked into one shared library.
@@ -27,9 +27,10 @@ LAUNCH_UNITS = 38  # the (kind, variant) pairs of IGC_LAUNCH_KINDS in igc_host.h
 FFN_SOURCE = os.path.join(CSRC, "ffn.hip")
 FFN_LAUNCH_SOURCE = os.path.join(CSRC, "ffn_launch.hip")
 FFN_LAUNCH_UNITS = 10  # the (type, layout) pairs of IGC_FFN_KINDS in ffn_host.hpp, and both types' joint backward launch
+ROWS_SOURCE = os.path.join(CSRC, "rows.hip")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
-SOURCES = [ABI_SOURCE, LAUNCH_SOURCE, FFN_SOURCE, FFN_LAUNCH_SOURCE]
+SOURCES = [ABI_SOURCE, LAUNCH_SOURCE, FFN_SOURCE, FFN_LAUNCH_SOURCE, ROWS_SOURCE]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 HIP_FLAGS = [
@@ -52,6 +53,7 @@ def _units():
     for n in range(LAUNCH_UNITS):
         yield LAUNCH_SOURCE, [f"-DIGC_LAUNCH_UNIT={n}"], f"igc_launch_{n}.o"
     yield FFN_SOURCE, [], "ffn.o"
+    yield ROWS_SOURCE, [], "rows.o"
     for n in range(FFN_LAUNCH_UNITS):
         yield FFN_LAUNCH_SOURCE, [f"-DIGC_FFN_UNIT={n}"], f"ffn_launch_{n}.o"
 

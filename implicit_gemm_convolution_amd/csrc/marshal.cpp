@@ -58,6 +58,19 @@ bool integer(PyObject* o, int* out) {
   return true;
 }
 
+bool real(PyObject* o, double* out) {
+  *out = PyFloat_AsDouble(o);
+  return !(*out == -1.0 && PyErr_Occurred());
+}
+
+bool unsigned64(PyObject* o, uint64_t* out) {
+  PyObject* const n = PyNumber_Index(o);
+  if (!n) return false;
+  *out = PyLong_AsUnsignedLongLong(n);  // (OverflowError for what does not fit)
+  Py_DECREF(n);
+  return !PyErr_Occurred();
+}
+
 // The workspace's address and, where the caller gives no size, its bytes.
 bool workspace(PyObject* ws, PyObject* bytes, void** p, size_t* size) {
   if (!address(ws, p)) return false;
@@ -91,8 +104,9 @@ int enter(void* entry, const void* descriptor, void* second) {
 }
 
 // call(entry, format, stream, ws, ws_bytes, fields...) -> status.  The
-// descriptor is laid out as the C compiler does: "i" an int, "p" an address;
-// the workspace and its size come last.
+// descriptor is laid out as the C compiler does: "i" an int, "f" a float, "d" a
+// double, "l" a uint64_t, "p" an address; the workspace and its size come last
+// (past the end of descriptors that have none).
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n < 5) return PyErr_Format(PyExc_TypeError, "call takes at least 5 arguments, not %zd", n);
@@ -111,11 +125,19 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (!integer(args[5 + i], &v)) return nullptr;
         std::memcpy(d + at, &v, 4);
         at += 4;
+      } else if (format[i] == 'f') {
+        double v;
+        if (!real(args[5 + i], &v)) return nullptr;
+        const float f = (float)v;
+        std::memcpy(d + at, &f, 4);
+        at += 4;
       } else {
+        double v;
+        uint64_t u;
         void* p;
-        if (!address(args[5 + i], &p)) return nullptr;
+        if (format[i] == 'd' ? !real(args[5 + i], &v) : format[i] == 'l' ? !unsigned64(args[5 + i], &u) : !address(args[5 + i], &p)) return nullptr;
         at = (at + 7) & ~size_t(7);
-        std::memcpy(d + at, &p, 8);
+        std::memcpy(d + at, format[i] == 'd' ? (void*)&v : format[i] == 'l' ? (void*)&u : (void*)&p, 8);
         at += 8;
       }
     }

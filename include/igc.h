@@ -537,6 +537,157 @@ typedef struct igc_grad_clip {
 int grad_clip(const igc_grad_clip* d, void* stream);
 int grad_clip_workspace_size(const igc_grad_clip* d, size_t* bytes);
 
+/* ------------------------------------------------------------------------
+ * What stands around the feed-forward products: layer norm in both
+ * directions, dropout, and the products in 8 bits with a scale for each token
+ * and each channel.
+ *
+ * The conventions of the feed-forward operators hold, but for these:
+ *  - Calls without a workspace in their descriptor need none.
+ *  - M and N (and K) go up to 2^31 - 4096; the K of the 8-bit products up to 131071
+ *    (128 * 128 * K has to fit in int32; IGC_EOVERFLOW beyond).
+ *  - Any leading dimension and any alignment that the element type allows. 16-byte
+ *    aligned rows with lengths that are multiples of 8 (of 16 in 8 bits) are the fast ones.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * layer_norm_forward -- for each of M rows of N elements
+ *   mean = sum x / N;  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps)
+ *   y = (x - mean) rstd gamma + beta
+ *
+ *   X            M x N of x_type: `type` or IGC_F32
+ *   gamma, beta  fp32 vectors of length N, or NULL (1, 0)
+ *   Y            M x N of `type` (IGC_F16 or IGC_BF16), or NULL
+ *   mean, rstd   fp32 vectors of length M for the backward pass, or NULL
+ *   Q, scale     int8 M x N and fp32 of length M: the rows of y, rounded to `type`,
+ *                in 8 bits as quantize_rows leaves them; or NULL
+ * The statistics are held in fp32 and the deviations taken from the row's own mean.
+ * A row with an infinity or NaN has NaN in all its outputs (zeros in Q).
+ * N == 0 leaves mean = 0 and rstd = 1 / sqrt(eps).
+ * Errors: IGC_EINVAL (NULL descriptor or X, no output, negative size, leading
+ * dimension below the row length, unknown type, eps negative or not finite,
+ * misaligned pointer, Q without scale), IGC_EUNSUPPORTED (too large),
+ * IGC_ENODEV, IGC_EHIP.
+ */
+typedef struct igc_layer_norm_forward {
+  int M, N;
+  int type, x_type;
+  float eps;
+  const void* X;
+  int ldx;
+  const float* gamma;
+  const float* beta;
+  void* Y;
+  int ldy;
+  float* mean;
+  float* rstd;
+  int8_t* Q;
+  int ldq;
+  float* scale;
+} igc_layer_norm_forward;
+int layer_norm_forward(const igc_layer_norm_forward* d, void* stream);
+
+/*
+ * layer_norm_backward -- with xh = (x - mean) rstd and g = dy gamma
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + r   (means over the row)
+ *   dgamma = sum over rows of dy xh;  dbeta = sum over rows of dy
+ *
+ *   dY           M x N of `type`
+ *   X            M x N of x_type, as in the forward pass
+ *   mean, rstd   what the forward pass left
+ *   gamma        or NULL (1)
+ *   R            M x N of x_type, added to dX: the gradient that reaches x past
+ *                the norm; or NULL
+ *   dX           M x N of x_type; dgamma, dbeta fp32 of length N
+ * Any non-empty subset of dX, dgamma and dbeta may be requested.  M == 0 sets
+ * dgamma and dbeta to zero.  The sums down the rows are added in an order that
+ * the sizes alone set.
+ * Errors: as layer_norm_forward, plus IGC_EINVAL when the workspace is missing
+ * or too small.
+ */
+typedef struct igc_layer_norm_backward {
+  int M, N;
+  int type, x_type;
+  const void* dY;
+  int lddy;
+  const void* X;
+  int ldx;
+  const float* mean;
+  const float* rstd;
+  const float* gamma;
+  const void* R;
+  int ldr;
+  void* dX;
+  int lddx;
+  float* dgamma;
+  float* dbeta;
+  void* workspace;
+  size_t ws_bytes;
+} igc_layer_norm_backward;
+int layer_norm_backward(const igc_layer_norm_backward* d, void* stream);
+int layer_norm_backward_workspace_size(const igc_layer_norm_backward* d, size_t* bytes);
+
+/*
+ * dropout -- y = (word < T ? 0 : x 2^32 / (2^32 - T)) + r with T = p 2^32 to the
+ * nearest whole number (ties to even).
+ *
+ * The word of element (m, n) is word n % 4 of Philox4x32-10 (Salmon, Moraes,
+ * Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with the key
+ * (low and high half of seed) and the counter (n / 4, m, low and high half of
+ * offset + *step), so no mask is stored: the backward pass is the same call on
+ * the gradient of y, with the same p, seed, offset and value of *step and
+ * without R.  Neither leading dimensions nor types change the mask.
+ *
+ *   X     M x N of `type`: IGC_F16, IGC_BF16 or IGC_F32
+ *   R     M x N of y_type, or NULL
+ *   Y     M x N of y_type: `type`, or IGC_F32, or any where `type` is IGC_F32.
+ *         Y may be X (where the types agree) or R itself: the same address and
+ *         leading dimension
+ *   step  device address of a 64-bit number that is added to offset when the
+ *         kernel runs, or NULL: a captured call draws a new mask at every replay
+ *         if the graph (or the program) changes the number
+ * p = 0 drops nothing, p = 1 everything.  A dropped x is replaced, not
+ * multiplied: infinities and NaN go with it.
+ * Errors: IGC_EINVAL (NULL descriptor or operand, negative size, leading dimension
+ * below the row length, unknown type, p outside [0, 1], misaligned pointer),
+ * IGC_EUNSUPPORTED (too large), IGC_ENODEV, IGC_EHIP.
+ */
+typedef struct igc_dropout {
+  int M, N;
+  int type, y_type;
+  double p;
+  uint64_t seed, offset;
+  const uint64_t* step;
+  const void* X;
+  int ldx;
+  const void* R;
+  int ldr;
+  void* Y;
+  int ldy;
+} igc_dropout;
+int dropout(const igc_dropout* d, void* stream);
+
+/*
+ * quantize_rows -- each row in 8 bits with a scale of its own:
+ *   scale = fl32(max|x| / 127);  q = round(127 x / max|x|), ties to even
+ * The quotient is rounded as if it were exact.  A row of zeros has the scale 0
+ * and zeros; a row with an infinity or NaN has NaN as its scale and zeros, so
+ * products of it are NaN.  N == 0 leaves the scale 0.
+ *
+ *   X  M x N of `type`: IGC_F16 or IGC_BF16;  Q  int8 M x N;  scale  fp32 of length M
+ * Errors: as dropout.
+ */
+typedef struct igc_quantize_rows {
+  int M, N;
+  int type;
+  const void* X;
+  int ldx;
+  int8_t* Q;
+  int ldq;
+  float* scale;
+} igc_quantize_rows;
+int quantize_rows(const igc_quantize_rows* d, void* stream);
+
 /* Diagnostics. */
 const char* igc_status_string(int status); /* static string for a status code              */
 const char* igc_last_error(void);          /* detail of this thread's last failure, or ""  */
