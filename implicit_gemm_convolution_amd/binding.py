@@ -52,6 +52,7 @@ EXPORTED = ("gemm_f16f32", "gemm_u8i8_zp", "conv2d_implicit_gemm", "conv2d_u8i8_
             "glu_forward", "glu_forward_workspace_size", "glu_backward", "glu_backward_workspace_size",
             "grad_clip", "grad_clip_workspace_size",
             "layer_norm_forward", "layer_norm_backward", "layer_norm_backward_workspace_size", "dropout", "quantize_rows",
+            "linear_i8", "linear_i8_workspace_size", "glu_i8", "glu_i8_workspace_size",
             "igc_status_string", "igc_last_error", "igc_device_check", "igc_set_tuning")
 
 
@@ -135,11 +136,23 @@ class QuantizeRows(ctypes.Structure):
     _fields_ = _fields("M:i N:i type:i X:p ldx:i Q:p ldq:i scale:p")
 
 
+class LinearI8(ctypes.Structure):
+    """igc_linear_i8."""
+    _fields_ = _fields("M:i N:i K:i act:i y_type:i X:p ldx:i x_scale:p W:p ldw:i w_scale:p bias:p R:p ldr:i Y:p ldy:i workspace:p ws_bytes:z")
+
+
+class GluI8(ctypes.Structure):
+    """igc_glu_i8."""
+    _fields_ = _fields("M:i N:i K:i type:i act:i X:p ldx:i x_scale:p Wg:p ldwg:i wg_scale:p Wu:p ldwu:i wu_scale:p bias_g:p bias_u:p "
+                       "H:p ldh:i workspace:p ws_bytes:z")
+
+
 # The entry points that take a descriptor: its structure, and for _marshal
 # its fields before the workspace (which not every one has).
 _DESCRIPTORS = {"linear_forward": LinearForward, "linear_backward": LinearBackward, "glu_forward": GluForward,
                 "glu_backward": GluBackward, "grad_clip": GradClip, "layer_norm_forward": LayerNormForward,
-                "layer_norm_backward": LayerNormBackward, "dropout": Dropout, "quantize_rows": QuantizeRows}
+                "layer_norm_backward": LayerNormBackward, "dropout": Dropout, "quantize_rows": QuantizeRows, "linear_i8": LinearI8,
+                "glu_i8": GluI8}
 _LETTERS = {ctypes.c_int: "i", ctypes.c_void_p: "p", ctypes.c_float: "f", ctypes.c_double: "d", ctypes.c_uint64: "l"}
 
 
@@ -553,3 +566,26 @@ def dropout(M, N, X, ldx, Y, ldy, p, seed, offset=0, *, step=None, R=None, ldr=0
 def quantize_rows(M, N, X, ldx, Q, ldq, scale, *, type=IGC_BF16, stream=None, check=True) -> int:
     """Each row in 8 bits: scale = max|X| / 127, Q = round(127 X / max|X|)."""
     return _call("quantize_rows", check, stream, None, None, M, N, type, X, ldx, Q, ldq, scale)
+
+
+def linear_i8(M, N, K, X, ldx, x_scale, W, ldw, w_scale, Y, ldy, *, y_type=IGC_BF16, act=IGC_ACT_NONE, bias=None, R=None, ldr=0,
+              stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """Y = act((X W^T) w_scale x_scale + bias) + R on rows in 8 bits."""
+    return _call("linear_i8", check, stream, workspace, ws_bytes, M, N, K, act, y_type, X, ldx, x_scale, W, ldw, w_scale, bias, R, ldr, Y, ldy)
+
+
+def linear_i8_workspace_size(M, N, K, X, ldx, x_scale, W, ldw, w_scale, Y, ldy, *, y_type=IGC_BF16, act=IGC_ACT_NONE, bias=None, R=None,
+                             ldr=0) -> int:
+    return _query("linear_i8", M, N, K, act, y_type, X, ldx, x_scale, W, ldw, w_scale, bias, R, ldr, Y, ldy)
+
+
+def glu_i8(M, N, K, X, ldx, x_scale, Wg, ldwg, wg_scale, Wu, ldwu, wu_scale, H, ldh, *, bias_g=None, bias_u=None, type=IGC_BF16,
+           act=IGC_ACT_SILU, stream=None, workspace=None, ws_bytes=None, check=True) -> int:
+    """G and U = (X W^T) w_scale x_scale + bias for each weight; H = act(G) U, on rows in 8 bits."""
+    return _call("glu_i8", check, stream, workspace, ws_bytes, M, N, K, type, act, X, ldx, x_scale, Wg, ldwg, wg_scale, Wu, ldwu, wu_scale,
+                 bias_g, bias_u, H, ldh)
+
+
+def glu_i8_workspace_size(M, N, K, X, ldx, x_scale, Wg, ldwg, wg_scale, Wu, ldwu, wu_scale, H, ldh, *, bias_g=None, bias_u=None,
+                          type=IGC_BF16, act=IGC_ACT_SILU) -> int:
+    return _query("glu_i8", M, N, K, type, act, X, ldx, x_scale, Wg, ldwg, wg_scale, Wu, ldwu, wu_scale, bias_g, bias_u, H, ldh)

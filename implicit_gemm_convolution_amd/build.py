@@ -2,9 +2,9 @@
 and, where torch is installed, _marshal.so (the Python binding's marshalling,
 host code only) with g++.
 
-The C ABI (csrc/igc.hip, csrc/ffn.hip, csrc/rows.hip) and the kernel instantiations
-(csrc/igc_launch.hip and csrc/ffn_launch.hip, compiled once per kernel kind
-with -DIGC_LAUNCH_UNIT=<n> and -DIGC_FFN_UNIT=<n>) are separate objects
+The C ABI (csrc/igc.hip, csrc/ffn.hip, csrc/rows.hip, csrc/i8.hip) and the kernel instantiations
+(csrc/igc_launch.hip, csrc/ffn_launch.hip and csrc/i8_launch.hip, compiled once
+per kernel kind with -DIGC_LAUNCH_UNIT=<n>, -DIGC_FFN_UNIT=<n> and -DIGC_I8_UNIT=<n>) are separate objects
 compiled in parallel, then linked into one shared library.
 """
 from __future__ import annotations
@@ -28,9 +28,12 @@ FFN_SOURCE = os.path.join(CSRC, "ffn.hip")
 FFN_LAUNCH_SOURCE = os.path.join(CSRC, "ffn_launch.hip")
 FFN_LAUNCH_UNITS = 10  # the (type, layout) pairs of IGC_FFN_KINDS in ffn_host.hpp, and both types' joint backward launch
 ROWS_SOURCE = os.path.join(CSRC, "rows.hip")
+I8_SOURCE = os.path.join(CSRC, "i8.hip")
+I8_LAUNCH_SOURCE = os.path.join(CSRC, "i8_launch.hip")
+I8_LAUNCH_UNITS = 4  # the (output type, layout) pairs of IGC_I8_KINDS in ffn_host.hpp
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
-SOURCES = [ABI_SOURCE, LAUNCH_SOURCE, FFN_SOURCE, FFN_LAUNCH_SOURCE, ROWS_SOURCE]
+SOURCES = [ABI_SOURCE, LAUNCH_SOURCE, FFN_SOURCE, FFN_LAUNCH_SOURCE, ROWS_SOURCE, I8_SOURCE, I8_LAUNCH_SOURCE]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 HIP_FLAGS = [
@@ -56,6 +59,9 @@ def _units():
     yield ROWS_SOURCE, [], "rows.o"
     for n in range(FFN_LAUNCH_UNITS):
         yield FFN_LAUNCH_SOURCE, [f"-DIGC_FFN_UNIT={n}"], f"ffn_launch_{n}.o"
+    yield I8_SOURCE, [], "i8.o"
+    for n in range(I8_LAUNCH_UNITS):
+        yield I8_LAUNCH_SOURCE, [f"-DIGC_I8_UNIT={n}"], f"i8_launch_{n}.o"
 
 
 def _jobs() -> int:
@@ -143,6 +149,11 @@ def assembly(out_dir: str, extra_flags=()) -> str:
 def ffn_assembly(out_dir: str, extra_flags=()) -> str:
     """The same for the kernels of the feed-forward products."""
     return _assembly(out_dir, "ffn-kernels-gfx950.s", FFN_LAUNCH_SOURCE, "IGC_FFN_UNIT", FFN_LAUNCH_UNITS, extra_flags)
+
+
+def i8_assembly(out_dir: str, extra_flags=()) -> str:
+    """The same for the kernels of the products in 8 bits."""
+    return _assembly(out_dir, "i8-kernels-gfx950.s", I8_LAUNCH_SOURCE, "IGC_I8_UNIT", I8_LAUNCH_UNITS, extra_flags)
 
 
 if __name__ == "__main__":

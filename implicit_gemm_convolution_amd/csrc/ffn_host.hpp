@@ -1,8 +1,8 @@
 // ffn_host.hpp -- host side of the feed-forward products: the launch plan
 // (tile, split, workspace bytes) and the launch on the caller's stream.
 // launch_product<BF, MODE> and launch_back<BF> are instantiated in
-// ffn_launch.hip, once per type and operand layout, so that they compile in parallel; ffn.hip plans and
-// calls it.
+// ffn_launch.hip and i8_launch.hip, once per type and operand layout, so that they compile in parallel; ffn.hip
+// and i8.hip plan and call them.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -225,6 +225,7 @@ inline Plan make_plan(int mode, long long M, long long N, long long R, int align
   return pl;
 }
 
+// (8 bits: a is an I8Args)
 template <bool BF, int MODE>
 int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t stream);
 
@@ -237,6 +238,13 @@ int launch_product(const igc_ffn::GemmArgs& a, const Plan& pl, hipStream_t strea
   X(5, true, igc_ffn::M_DX)      \
   X(6, false, igc_ffn::M_DW)     \
   X(7, true, igc_ffn::M_DW)
+
+// Products in 8 bits: the type of their outputs, the layout.
+#define IGC_I8_KINDS(X)          \
+  X(0, false, igc_ffn::M_I8)     \
+  X(1, true, igc_ffn::M_I8)      \
+  X(2, false, igc_ffn::M_I8_GLU) \
+  X(3, true, igc_ffn::M_I8_GLU)
 
 // Both backward products, planned on one tile size, and the column sums
 // (s.which_n 0: none).
@@ -251,6 +259,7 @@ extern template int launch_back<true>(const igc_ffn::GemmArgs&, const Plan&, con
 #define IGC_FFN_EXTERN(n, BF, MODE) \
   extern template int launch_product<BF, MODE>(const igc_ffn::GemmArgs&, const Plan&, hipStream_t);
 IGC_FFN_KINDS(IGC_FFN_EXTERN)
+IGC_I8_KINDS(IGC_FFN_EXTERN)
 #undef IGC_FFN_EXTERN
 
 // workgroups of the column sums

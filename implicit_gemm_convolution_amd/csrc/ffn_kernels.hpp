@@ -131,6 +131,27 @@ __device__ __forceinline__ uint4 load8_words(const uint8_t* p) {
                     __builtin_amdgcn_alignbit(v.w, v.z, bits), __builtin_amdgcn_alignbit(last, v.w, bits));
 }
 
+// The same for sixteen bytes from any address.
+__device__ __forceinline__ uint4 load16_words(const uint8_t* p) {
+  const uint32_t odd = (uint32_t)(uintptr_t)p & 3;
+  const uint8_t* const q = p - odd;
+  uint4 v;
+  uint32_t last;
+  __builtin_memcpy(&v, __builtin_assume_aligned(q, 4), 16);
+  __builtin_memcpy(&last, __builtin_assume_aligned(q + (odd ? 16 : 12), 4), 4);
+  const uint32_t bits = odd * 8;
+  return make_uint4(__builtin_amdgcn_alignbit(v.y, v.x, bits), __builtin_amdgcn_alignbit(v.z, v.y, bits),
+                    __builtin_amdgcn_alignbit(v.w, v.z, bits), __builtin_amdgcn_alignbit(last, v.w, bits));
+}
+// Fewer than sixteen bytes, zeros past them.
+__device__ __forceinline__ uint4 load16_tail(const uint8_t* p, int valid) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 15; ++e)
+    if (e < valid) w[e / 4] |= (uint32_t)p[e] << (8 * (e & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // V (4 or 8) 16-bit or fp32 elements as fp32 values, from and to any address;
 // those past `valid` are left alone.
 template <bool BF, int V>
@@ -279,7 +300,18 @@ __device__ __forceinline__ void act_n(int act, const float (&z)[N], float (&f)[N
 //   GLU   the same with two B operands, side by side    A ROW, B ROW
 //   DX    out[m][k] = sum_n D[m][n] W[n][k]             A ROW, B COL
 //   DW    out[n][k] = sum_m D[m][n] X[m][k]             A COL, B COL
-enum Mode : int { M_FWD = 0, M_GLU = 1, M_DX = 2, M_DW = 3 };
+//   I8, I8_GLU  FWD and GLU with operands in 8 bits, exact in int32, and a scale
+//               for each row and each column ahead of the bias
+// A tile's rows are 128 bytes of the reduction and a matrix instruction takes 16
+// of them a lane, whatever the type: the 8-bit products run through the same
+// kernels, 128 elements where 16-bit operands have 64.
+enum Mode : int { M_FWD = 0, M_GLU = 1, M_DX = 2, M_DW = 3, M_I8 = 4, M_I8_GLU = 5 };
+constexpr bool is_i8(int mode) { return mode == M_I8 || mode == M_I8_GLU; }
+constexpr bool is_fwd(int mode) { return mode == M_FWD || mode == M_I8; }
+constexpr bool is_glu(int mode) { return mode == M_GLU || mode == M_I8_GLU; }
+// four sums of a lane
+template <int MODE>
+using Sums = std::conditional_t<is_i8(MODE), igc::i32x4, f32x4>;
 
 struct GemmArgs {
   int M, N, R;  // output rows, output columns (of each product), reduction
@@ -310,9 +342,15 @@ struct GemmArgs {
   int tiles_m, tiles_n;
   int whole;    // tiles [0, whole) have a workgroup each
   int splits;   // workgroups that share the reduction of each tile after those
-  int odd_rows; // (few rows) rows start at odd multiples of 2 bytes
+  int odd_rows; // (few rows) rows start at odd multiples of 2 bytes (in 8 bits: at addresses that are no multiples of 4)
   float* part;  // their partial tiles
 };
+// 8 bits: the scales of A's rows, and of B's and B2's (the output's columns).
+struct I8Args : GemmArgs {
+  const float *xs, *ws, *ws2;
+};
+template <int MODE>
+using Args = std::conditional_t<is_i8(MODE), I8Args, GemmArgs>;
 
 template <bool BF>
 __device__ __forceinline__ void mfma16(f32x4& c, const uint4& a, const uint4& b) {
@@ -320,6 +358,11 @@ __device__ __forceinline__ void mfma16(f32x4& c, const uint4& a, const uint4& b)
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   else
     c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <bool BF>
+__device__ __forceinline__ void mfma16(igc::i32x4& c, const uint4& a, const uint4& b) {
+  c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(igc::i32x4, a), __builtin_bit_cast(igc::i32x4, b), c, 0, 0, 0);
 }
 
 // An operand's K tile in LDS: W rows (or columns) x 64 reduction elements.
@@ -531,20 +574,28 @@ __device__ __forceinline__ void tile_of(const GemmArgs& p, int b, int& tm, int& 
 // -> 100 us streamed).
 template <bool BF, int MODE, int V, int U, bool FULL, bool STREAM>
 struct Epilogue {
-  const GemmArgs& p;
+  const Args<MODE>& p;
   int col;       // this lane's first column
   int left;      // columns from there to the end
   float b1[V], b2[V];
+  float w1[V], w2[V];  // 8 bits: the columns' scales
   bool has_bias;
   float undo;
-  __device__ __forceinline__ Epilogue(const GemmArgs& args, int c) : p(args), col(c), left(args.N - c) {
+  __device__ __forceinline__ Epilogue(const Args<MODE>& args, int c) : p(args), col(c), left(args.N - c) {
     if constexpr (!BF && (MODE == M_DX || MODE == M_DW)) undo = p.undo ? *p.undo : 1.0f;
-    has_bias = (MODE == M_FWD && p.bias) || (MODE == M_GLU && (p.bias || p.bias2));
-    if constexpr (MODE == M_FWD || MODE == M_GLU) {
+    has_bias = (is_fwd(MODE) && p.bias) || (is_glu(MODE) && (p.bias || p.bias2));
+    if constexpr (is_fwd(MODE) || is_glu(MODE)) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         b1[e] = p.bias && e < have() ? p.bias[col + e] : 0.0f;
-        b2[e] = MODE == M_GLU && p.bias2 && e < have() ? p.bias2[col + e] : 0.0f;
+        b2[e] = is_glu(MODE) && p.bias2 && e < have() ? p.bias2[col + e] : 0.0f;
+      }
+    }
+    if constexpr (is_i8(MODE)) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        w1[e] = e < have() ? p.ws[col + e] : 0.0f;
+        w2[e] = MODE == M_I8_GLU && e < have() ? p.ws2[col + e] : 0.0f;
       }
     }
   }
@@ -597,7 +648,19 @@ struct Epilogue {
       }
     } else {
       float res[U * V], y[U * V], unused[U * V];
-      if (MODE == M_FWD && p.res) {
+      if constexpr (is_i8(MODE)) {  // the sums are whole numbers: one rounding, then one for each scale
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const int row = row0 + q * step;
+          const float xs = row < p.M ? p.xs[row] : 0.0f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            f[q * V + e] = (float)__builtin_bit_cast(int, f[q * V + e]) * w1[e] * xs;
+            if constexpr (MODE == M_I8_GLU) u[q * V + e] = (float)__builtin_bit_cast(int, u[q * V + e]) * w2[e] * xs;
+          }
+        }
+      }
+      if (is_fwd(MODE) && p.res) {
 #pragma unroll
         for (int q = 0; q < U; ++q) {
           const int row = row0 + q * step;
@@ -614,7 +677,7 @@ struct Epilogue {
       if (has_bias) {
 #pragma unroll
         for (int e = 0; e < U * V; ++e) f[e] += b1[e % V];
-        if constexpr (MODE == M_GLU) {
+        if constexpr (is_glu(MODE)) {
 #pragma unroll
           for (int e = 0; e < U * V; ++e) u[e] += b2[e % V];
         }
@@ -625,7 +688,7 @@ struct Epilogue {
           if (row0 + q * step < p.M) write<uint16_t>(p.Z, p.ldz, row0 + q * step, f, q);
       }
       act_n<false>(p.act, f, y, unused);
-      if constexpr (MODE == M_GLU) {
+      if constexpr (is_glu(MODE)) {
 #pragma unroll
         for (int q = 0; q < U; ++q)
           if (p.U && row0 + q * step < p.M) write<uint16_t>(p.U, p.ldu, row0 + q * step, u, q);
@@ -639,7 +702,7 @@ struct Epilogue {
       for (int q = 0; q < U; ++q) {
         const int row = row0 + q * step;
         if (row >= p.M) continue;
-        if (MODE == M_FWD && p.y_f32)
+        if (is_fwd(MODE) && p.y_f32)
           write<float>(p.Y, p.ldy, row, y, q);
         else
           write<uint16_t>(p.Y, p.ldy, row, y, q);
@@ -654,9 +717,9 @@ struct Epilogue {
 // (Joined in the same launch by the last workgroup to arrive, every arrival
 // writes its XCD's L2 back and every join drops it: 256 x 4096 x 4096 on
 // 64 x 64 tiles in two splits took 51 us so, against 23 unsplit.)
-template <int NQ>
-__device__ __forceinline__ f32x4* partial(const GemmArgs& p, int tile, int split, int thread) {
-  return reinterpret_cast<f32x4*>(p.part) + ((long long)(tile - p.whole) * p.splits + split) * NQ * 256 + thread;
+template <int NQ, class S>
+__device__ __forceinline__ S* partial(const GemmArgs& p, int tile, int split, int thread) {
+  return reinterpret_cast<S*>(p.part) + ((long long)(tile - p.whole) * p.splits + split) * NQ * 256 + thread;
 }
 // Workgroup b's tile and split.  (One split after the other, so that the
 // workgroups of an XCD keep neighbouring tiles of one split.)
@@ -679,8 +742,8 @@ __device__ __forceinline__ void split_of(const GemmArgs& p, int b, int& tile, in
 // (unrolled over the accumulators, its six activations overflow the
 // instruction cache).
 template <bool BF, int MODE, int FM, int FN, int REGION>
-__device__ __forceinline__ void write_out(const GemmArgs& p, const f32x4 (&acc)[FM][FN], uint8_t* lds, int row0, int col0) {
-  constexpr bool GLU = MODE == M_GLU;
+__device__ __forceinline__ void write_out(const Args<MODE>& p, const Sums<MODE> (&acc)[FM][FN], uint8_t* lds, int row0, int col0) {
+  constexpr bool GLU = is_glu(MODE);
   constexpr int TN = FN * 16, OUT = GLU ? TN / 2 : TN;  // staged columns, output columns
   constexpr int LPR = OUT / 8, RPP = 64 / LPR;          // lanes per row, rows per pass
   constexpr int FIT = REGION / (16 * TN * 4), GR = FIT >= FM ? FM : FM / 2;  // block rows staged at a time
@@ -795,7 +858,7 @@ __global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
     __syncthreads();
   }
   if (p.splits > 1) {
-    f32x4* const out = partial<FM * FN>(p, tile, split, threadIdx.x);
+    Sums<MODE>* const out = partial<FM * FN, Sums<MODE>>(p, tile, split, threadIdx.x);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -812,13 +875,14 @@ __global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
 // UN steps of 32 elements at once, so that a compute unit keeps over 100 KB
 // of weights in flight, which is what it takes to reach the memory's rate.
 // The waves' sums are added through LDS in wave order.  Any alignment.
-// ODD: rows may start at odd multiples of 2 bytes.
+// ODD: rows may start at odd multiples of 2 bytes (8 bits: at any).
 template <bool BF, int MODE, int MB, int NB, int NW, bool ODD>
-__global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) {
-  constexpr bool GLU = MODE == M_GLU;
+__device__ __forceinline__ void skinny_product(const Args<MODE>& p) {
+  constexpr bool GLU = is_glu(MODE);
   constexpr int PB = GLU ? NB / 2 : NB;  // column blocks
   constexpr int UN = MB == 1 ? 8 : 4;
-  __shared__ f32x4 red[NW][NB * MB][64];
+  constexpr int EB = is_i8(MODE) ? 1 : 2, CH = 16 / EB, SK = 4 * CH;  // bytes of an element, elements of a chunk and of a step
+  __shared__ Sums<MODE> red[NW][NB * MB][64];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * (PB * 16);
@@ -828,17 +892,17 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
   for (int j = 0; j < NB; ++j) {
     const bool second = GLU && j >= PB;
     const long long n = min(n0 + (second ? j - PB : j) * 16 + r, p.N - 1);
-    w[j] = (second ? p.B2 + n * p.ldb2 * 2 : p.B + n * p.ldb * 2) + g * 16;
+    w[j] = (second ? p.B2 + n * p.ldb2 * EB : p.B + n * p.ldb * EB) + g * 16;
   }
 #pragma unroll
-  for (int i = 0; i < MB; ++i) x[i] = p.A + (long long)min(i * 16 + r, p.M - 1) * p.lda * 2 + g * 16;
-  f32x4 acc[NB][MB];
+  for (int i = 0; i < MB; ++i) x[i] = p.A + (long long)min(i * 16 + r, p.M - 1) * p.lda * EB + g * 16;
+  Sums<MODE> acc[NB][MB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
 #pragma unroll
-    for (int i = 0; i < MB; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < MB; ++i) acc[j][i] = Sums<MODE>{0, 0, 0, 0};
 
-  const int steps = p.R / 32 + (p.R % 32 >= 8);  // (what is left of a chunk of 8 follows below)
+  const int steps = p.R / SK + (p.R % SK >= CH);  // (what is left of a chunk follows below)
   const int s1 = (int)((long long)steps * (wave + 1) / NW);
   int s = (int)((long long)steps * wave / NW);
   uint4 fw[UN][NB], fx[UN][MB];
@@ -849,12 +913,13 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
       for (int i = 0; i < MB; ++i) mfma16<BF>(acc[j][i], fw[u][j], fx[u][i]);
   };
   auto chunk = [](const uint8_t* q) {
-    if constexpr (ODD) return load8_words(q);
+    if constexpr (ODD && is_i8(MODE)) return load16_words(q);
+    else if constexpr (ODD) return load8_words(q);
     uint4 v;
     __builtin_memcpy(&v, q, 16);
     return v;
   };
-  for (; s + UN <= s1 && (s + UN) * 32 <= p.R; s += UN) {
+  for (; s + UN <= s1 && (s + UN) * SK <= p.R; s += UN) {
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
 #pragma unroll
@@ -868,7 +933,7 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
   if (s < s1) {  // the last batch: the steps that are left, the lanes whose chunk is whole
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const bool in = s + u < s1 && (s + u) * 32 + g * 8 + 8 <= p.R;
+      const bool in = s + u < s1 && (s + u) * SK + g * CH + CH <= p.R;
 #pragma unroll
       for (int j = 0; j < NB; ++j) fw[u][j] = in ? chunk(w[j] + (long long)(s + u) * 64) : make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -877,12 +942,16 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
 #pragma unroll
     for (int u = 0; u < UN; ++u) multiply(u);
   }
-  if ((p.R & 7) && wave == NW - 1) {  // the elements past the last whole chunk
-    const int k = p.R & ~7, left = g == 0 ? p.R & 7 : 0;
+  if ((p.R & (CH - 1)) && wave == NW - 1) {  // the elements past the last whole chunk
+    const int k = p.R & ~(CH - 1), left = g == 0 ? p.R & (CH - 1) : 0;
+    auto tail = [&](const uint8_t* q) {
+      if constexpr (is_i8(MODE)) return load16_tail(q, left);
+      else return load8(q, left);
+    };
 #pragma unroll
-    for (int j = 0; j < NB; ++j) fw[0][j] = load8(w[j] - g * 16 + (long long)k * 2, left);
+    for (int j = 0; j < NB; ++j) fw[0][j] = tail(w[j] - g * 16 + (long long)k * EB);
 #pragma unroll
-    for (int i = 0; i < MB; ++i) fx[0][i] = load8(x[i] - g * 16 + (long long)k * 2, left);
+    for (int i = 0; i < MB; ++i) fx[0][i] = tail(x[i] - g * 16 + (long long)k * EB);
     multiply(0);
   }
 #pragma unroll
@@ -893,16 +962,26 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
   // lane l of a block holds row l % 16, columns 4 (l / 16) .. +3
   for (int t = threadIdx.x; t < PB * MB * 64; t += 64 * NW) {
     const int b = t >> 6, l = t & 63;
-    f32x4 f4 = red[0][b][l], u4 = GLU ? red[0][PB * MB + b][l] : f4;
+    Sums<MODE> f4 = red[0][b][l], u4 = GLU ? red[0][PB * MB + b][l] : f4;
 #pragma unroll
     for (int q = 1; q < NW; ++q) {
       f4 += red[q][b][l];
       if constexpr (GLU) u4 += red[q][PB * MB + b][l];
     }
-    float f[4] = {f4[0], f4[1], f4[2], f4[3]}, u[4] = {u4[0], u4[1], u4[2], u4[3]};
+    float f[4], u[4];
+    __builtin_memcpy(f, &f4, 16);
+    __builtin_memcpy(u, &u4, 16);
     const Epilogue<BF, MODE, 4, 1, false, false> out(p, n0 + (b / MB) * 16 + 4 * (l >> 4));
     out((b % MB) * 16 + (l & 15), 0, f, u);
   }
+}
+template <bool BF, int MODE, int MB, int NB, int NW, bool ODD>
+__global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) {
+  skinny_product<BF, MODE, MB, NB, NW, ODD>(p);
+}
+template <bool BF, int MODE, int MB, int NB, int NW, bool ODD>
+__global__ void __launch_bounds__(64 * NW) i8_skinny_kernel(const I8Args p) {
+  skinny_product<BF, MODE, MB, NB, NW, ODD>(p);
 }
 
 // The product on aligned operands: both go from memory straight into LDS,
@@ -928,8 +1007,8 @@ __global__ void __launch_bounds__(64 * NW) gemm_skinny_kernel(const GemmArgs p) 
 constexpr int tile_lds(int bm, int bn, int depth) { return 128 * ((depth + 1) * bm + (depth == 2 ? 2 : depth + 1) * bn); }
 constexpr int tile_waves(int bm, int bn, int depth) { return 160 * 1024 / tile_lds(bm, bn, depth) > 1 ? 2 : 1; }  // per SIMD
 template <bool BF, int MODE, int BM, int BN, int DEPTH>
-__device__ __forceinline__ void tile_product(const GemmArgs& p, const int block, uint8_t* const smem) {
-  constexpr bool GLU = MODE == M_GLU, ACOL = MODE == M_DW, BCOL = MODE == M_DX || MODE == M_DW;
+__device__ __forceinline__ void tile_product(const Args<MODE>& p, const int block, uint8_t* const smem) {
+  constexpr bool GLU = is_glu(MODE), ACOL = MODE == M_DW, BCOL = MODE == M_DX || MODE == M_DW;
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   typedef LdsTile<BM, ACOL> TA;
   typedef LdsTile<BN, BCOL> TB;
@@ -947,7 +1026,10 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const int block,
   tile_of(p, tile, tm, tn);
   constexpr int ON = GLU ? BN / 2 : BN;
   const int m0 = tm * BM, n0 = tn * ON;
-  const int nk = max(1, (p.R + 63) / 64);
+  // (the loaders count in units of 2 bytes; rows in 8 bits are whole chunks of 16)
+  constexpr int UNIT = is_i8(MODE) ? 2 : 1;
+  const int R = p.R / UNIT;
+  const int nk = max(1, (R + 63) / 64);
   int k0 = 0, k1 = nk;
   if (shared) {
     k0 = (int)((long long)nk * split / p.splits);
@@ -955,14 +1037,14 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const int block,
   }
   LoadA la;
   LoadB lb;
-  la.init(p.A, p.lda, nullptr, 0, m0, p.M, p.R, p.R, p.R, k1);
-  lb.init(p.B, p.ldb, p.B2, p.ldb2, n0, p.N, p.R, p.r_split, p.b_rows, k1);
+  la.init(p.A, p.lda / UNIT, nullptr, 0, m0, p.M, R, R, R, k1);
+  lb.init(p.B, p.ldb / UNIT, p.B2, p.ldb2 / UNIT, n0, p.N, R, p.r_split, p.b_rows, k1);
 
-  f32x4 acc[FM][FN];
+  Sums<MODE> acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) acc[i][j] = Sums<MODE>{0, 0, 0, 0};
   auto blk_b = [&](int j) {
     if constexpr (GLU) return j < FN / 2 ? wn * (TN / 2) + j * 16 : BN / 2 + wn * (TN / 2) + (j - FN / 2) * 16;
     return wn * TN + j * 16;
@@ -1053,7 +1135,7 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const int block,
   wait_vmcnt_lgkm0<0>();
   lds_barrier();
   if (shared) {
-    f32x4* const out = partial<FM * FN>(p, tile, split, threadIdx.x);
+    Sums<MODE>* const out = partial<FM * FN, Sums<MODE>>(p, tile, split, threadIdx.x);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -1065,6 +1147,11 @@ __device__ __forceinline__ void tile_product(const GemmArgs& p, const int block,
 
 template <bool BF, int MODE, int BM, int BN, int DEPTH>
 __global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH)) gemm_tile_kernel(const GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_lds(BM, BN, DEPTH)];
+  tile_product<BF, MODE, BM, BN, DEPTH>(p, blockIdx.x, smem);
+}
+template <bool BF, int MODE, int BM, int BN, int DEPTH>
+__global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH)) i8_tile_kernel(const I8Args p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[tile_lds(BM, BN, DEPTH)];
   tile_product<BF, MODE, BM, BN, DEPTH>(p, blockIdx.x, smem);
 }
@@ -1121,24 +1208,32 @@ __global__ void __launch_bounds__(256, tile_waves(BM, BN, DEPTH))
 // 16 tiles of 256 x 256 in two splits 30 us).
 constexpr int join_waves(int bm) { return 4 * (bm / 2 / 16); }  // per tile
 template <bool BF, int MODE, int BM, int BN>
-__global__ void __launch_bounds__(64) gemm_join_kernel(const GemmArgs p) {
+__device__ __forceinline__ void join(const Args<MODE>& p) {
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
-  constexpr int ON = MODE == M_GLU ? BN / 2 : BN;
+  constexpr int ON = is_glu(MODE) ? BN / 2 : BN;
   __shared__ __attribute__((aligned(16))) uint8_t smem[16 * TN * 4];
   const int tile = p.whole + blockIdx.x / (4 * FM), rest = blockIdx.x % (4 * FM);
   const int wave = rest / FM, i = rest % FM, wm = wave >> 1, wn = wave & 1;
   int tm, tn;
   tile_of(p, tile, tm, tn);
-  f32x4 acc[1][FN];
+  Sums<MODE> acc[1][FN];
 #pragma unroll
-  for (int j = 0; j < FN; ++j) acc[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < FN; ++j) acc[0][j] = Sums<MODE>{0, 0, 0, 0};
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
-    const f32x4* const in = partial<FM * FN>(p, tile, s, wave * 64 + threadIdx.x) + (long long)i * FN * 256;
+    const Sums<MODE>* const in = partial<FM * FN, Sums<MODE>>(p, tile, s, wave * 64 + threadIdx.x) + (long long)i * FN * 256;
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[0][j] += in[j * 256];
   }
   write_out<BF, MODE, 1, FN, sizeof(smem)>(p, acc, smem, tm * BM + wm * TM + i * 16, tn * ON + wn * (ON / 2));
+}
+template <bool BF, int MODE, int BM, int BN>
+__global__ void __launch_bounds__(64) gemm_join_kernel(const GemmArgs p) {
+  join<BF, MODE, BM, BN>(p);
+}
+template <bool BF, int MODE, int BM, int BN>
+__global__ void __launch_bounds__(64) i8_join_kernel(const I8Args p) {
+  join<BF, MODE, BM, BN>(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -1200,6 +1295,34 @@ __device__ __forceinline__ void pad_rows(const PadArgs& p, int block) {
 template <int NONE = 0>
 __global__ void __launch_bounds__(256) pad_kernel(const PadArgs p) {
   pad_rows(p, blockIdx.x);
+}
+
+// The same for rows in 8 bits of any length (none: a chunk of zeros).
+template <int NONE = 0>
+__global__ void __launch_bounds__(256) pad_bytes_kernel(const PadArgs p) {
+  int op = 0;
+  while (op + 1 < p.count && (int)blockIdx.x >= p.first[op + 1]) ++op;
+  const uint8_t* const src = p.src[op];
+  const long long ld = p.ld[op];
+  const int cols = p.cols[op];
+  const uint32_t per = max((uint32_t)(cols + 15) / 16, 1u), end = p.chunks[op];
+  const uint32_t i0 = (uint32_t)(blockIdx.x - p.first[op]) * 1024 + threadIdx.x;
+  unsigned __int128 v[4];
+  int back[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t i = min(i0 + 256 * j, end - 1), row = i / per;
+    const int c = (int)(i - row * per) * 16;
+    const uint8_t* const q = src + row * ld + c;
+    back[j] = cols < 16 ? 0 : max(c + 16 - cols, 0);
+    const uint4 w = cols < 16 ? load16_tail(q, cols) : load16_words(q - back[j]);
+    __builtin_memcpy(&v[j], &w, 16);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] >>= 8 * back[j];
+    if (i0 + 256 * j < end) __builtin_memcpy(p.dst[op] + (long long)(i0 + 256 * j) * 16, &v[j], 16);
+  }
 }
 
 // Block b of the element-wise work: 512 columns (8 per lane) x `rows` rows; the

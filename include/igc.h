@@ -688,6 +688,72 @@ typedef struct igc_quantize_rows {
 } igc_quantize_rows;
 int quantize_rows(const igc_quantize_rows* d, void* stream);
 
+/*
+ * linear_i8 -- the linear operator on rows in 8 bits:
+ *   Z[m][n] = fl32(fl32(fl32(sum_k X[m][k] W[n][k]) w_scale[n]) x_scale[m]) + bias[n]
+ *   Y = act(Z) + R
+ * The sums are exact in int32.
+ *
+ *   X        int8 M x K with x_scale, fp32 of length M (quantize_rows and
+ *            layer_norm_forward leave them)
+ *   W        int8 N x K (one row per output column) with w_scale, fp32 of length N
+ *   bias     fp32 of length N, or NULL
+ *   R, Y     M x N of y_type: IGC_F16, IGC_BF16 or IGC_F32; R or NULL
+ * The workspace is required where its size is not 0: for reductions that are
+ * split, and for rows that are not 16-byte aligned or no multiple of 16 long,
+ * which are first copied into rows that are.
+ * Errors: as linear_forward, plus IGC_EINVAL (a scale is NULL, the workspace is
+ * missing) and IGC_EOVERFLOW (K > 131071).
+ */
+typedef struct igc_linear_i8 {
+  int M, N, K;
+  int act, y_type;
+  const int8_t* X;
+  int ldx;
+  const float* x_scale;
+  const int8_t* W;
+  int ldw;
+  const float* w_scale;
+  const float* bias;
+  const void* R;
+  int ldr;
+  void* Y;
+  int ldy;
+  void* workspace;
+  size_t ws_bytes;
+} igc_linear_i8;
+int linear_i8(const igc_linear_i8* d, void* stream);
+int linear_i8_workspace_size(const igc_linear_i8* d, size_t* bytes);
+
+/*
+ * glu_i8 -- the gated block on rows in 8 bits: G and U as Z of linear_i8, with
+ * Wg, wg_scale, bias_g and Wu, wu_scale, bias_u;  H = act(G) U.
+ *
+ *   H  M x N of `type`: IGC_F16 or IGC_BF16
+ * Errors: as linear_i8.
+ */
+typedef struct igc_glu_i8 {
+  int M, N, K;
+  int type, act;
+  const int8_t* X;
+  int ldx;
+  const float* x_scale;
+  const int8_t* Wg;
+  int ldwg;
+  const float* wg_scale;
+  const int8_t* Wu;
+  int ldwu;
+  const float* wu_scale;
+  const float* bias_g;
+  const float* bias_u;
+  void* H;
+  int ldh;
+  void* workspace;
+  size_t ws_bytes;
+} igc_glu_i8;
+int glu_i8(const igc_glu_i8* d, void* stream);
+int glu_i8_workspace_size(const igc_glu_i8* d, size_t* bytes);
+
 /* Diagnostics. */
 const char* igc_status_string(int status); /* static string for a status code              */
 const char* igc_last_error(void);          /* detail of this thread's last failure, or ""  */

@@ -1,4 +1,4 @@
-"""The row operators' entry points without a GPU: bad arguments are rejected
+"""The entry points of the row operators and of the products in 8 bits without a GPU: bad arguments are rejected
 with the documented status codes before any HIP call, and the binding's numbers
 arrive whole."""
 from __future__ import annotations
@@ -58,14 +58,43 @@ def test_quantize_rows_refuses(igc):  # noqa: F811
     assert igc.quantize_rows(**{**good, "M": 0, "X": None, "Q": None, "scale": None}, check=False) == igc.IGC_OK
 
 
+def test_linear_i8_refuses(igc):  # noqa: F811
+    good = dict(M=4, N=6, K=8, X=P, ldx=8, x_scale=P, W=P, ldw=8, w_scale=P, Y=P, ldy=6, bias=P, R=P, ldr=6)
+    bad = [dict(M=-1), dict(N=-1), dict(K=-1), dict(act=-1), dict(act=6), dict(y_type=3), dict(y_type=-1), dict(X=None), dict(W=None),
+           dict(Y=None), dict(x_scale=None), dict(w_scale=None), dict(ldx=7), dict(ldw=7), dict(ldy=5), dict(ldr=5), dict(Y=P + 1),
+           dict(y_type=igc.IGC_F32, Y=P + 2), dict(R=P + 1), dict(x_scale=P + 2), dict(w_scale=P + 1), dict(bias=P + 2)]
+    _rejects(igc, igc.linear_i8, good, bad)
+    for change in bad:
+        with pytest.raises(igc.IGCError) as e:
+            igc.linear_i8_workspace_size(**{**good, **change})
+        assert e.value.status == igc.IGC_EINVAL
+    long = {**good, "K": 131072, "ldx": 131072, "ldw": 131072}
+    assert igc.linear_i8(**long, check=False) == igc.IGC_EOVERFLOW and "131071" in igc.last_error()
+    assert igc.linear_i8(**{**good, "M": 0, "X": None, "x_scale": None, "Y": None}, check=False) == igc.IGC_OK
+    assert igc.linear_i8(**{**good, "N": 0, "W": None, "w_scale": None, "Y": None}, check=False) == igc.IGC_OK
+    assert igc.linear_i8_workspace_size(**{**good, "M": 0}) == 0
+
+
+def test_glu_i8_refuses(igc):  # noqa: F811
+    good = dict(M=4, N=6, K=8, X=P, ldx=8, x_scale=P, Wg=P, ldwg=8, wg_scale=P, Wu=P, ldwu=8, wu_scale=P, H=P, ldh=6, bias_g=P, bias_u=P)
+    bad = [dict(M=-1), dict(N=-1), dict(K=-1), dict(act=6), dict(type=igc.IGC_F32), dict(type=5), dict(X=None), dict(Wg=None), dict(Wu=None),
+           dict(H=None), dict(x_scale=None), dict(wg_scale=None), dict(wu_scale=None), dict(ldx=7), dict(ldwg=7), dict(ldwu=7), dict(ldh=5),
+           dict(H=P + 1), dict(x_scale=P + 2), dict(wg_scale=P + 2), dict(wu_scale=P + 1), dict(bias_g=P + 1), dict(bias_u=P + 2)]
+    _rejects(igc, igc.glu_i8, good, bad)
+    long = {**good, "K": 131072, "ldx": 131072, "ldwg": 131072, "ldwu": 131072}
+    assert igc.glu_i8(**long, check=False) == igc.IGC_EOVERFLOW
+    assert igc.glu_i8(**{**good, "M": 0, "X": None, "x_scale": None, "H": None}, check=False) == igc.IGC_OK
+    assert igc.glu_i8_workspace_size(**{**good, "N": 0}) == 0
+
+
 def test_null_descriptors_and_query_pointers(igc):  # noqa: F811
     L = igc.load()
-    for name in ("layer_norm_forward", "layer_norm_backward", "dropout", "quantize_rows"):
+    for name in ("layer_norm_forward", "layer_norm_backward", "dropout", "quantize_rows", "linear_i8", "glu_i8"):
         assert getattr(L, name)(None, None) == igc.IGC_EINVAL
     size = ctypes.c_size_t(0)
-    assert L.layer_norm_backward_workspace_size(None, ctypes.byref(size)) == igc.IGC_EINVAL
-    d = igc.binding.LayerNormBackward()
-    assert L.layer_norm_backward_workspace_size(ctypes.byref(d), None) == igc.IGC_EINVAL
+    for name, d in (("layer_norm_backward", igc.binding.LayerNormBackward()), ("linear_i8", igc.binding.LinearI8()), ("glu_i8", igc.binding.GluI8())):
+        assert getattr(L, name + "_workspace_size")(None, ctypes.byref(size)) == igc.IGC_EINVAL
+        assert getattr(L, name + "_workspace_size")(ctypes.byref(d), None) == igc.IGC_EINVAL
 
 
 def test_sizes_past_the_index_arithmetic(igc):  # noqa: F811
@@ -75,6 +104,8 @@ def test_sizes_past_the_index_arithmetic(igc):  # noqa: F811
         "layer_norm_backward": dict(M=4, N=6, dY=P, lddy=ld, X=P, ldx=ld, mean=P, rstd=P, dX=P, lddx=ld),
         "dropout": dict(M=4, N=6, X=P, ldx=ld, Y=P, ldy=ld, p=0.5, seed=0),
         "quantize_rows": dict(M=4, N=6, X=P, ldx=ld, Q=P, ldq=ld, scale=P),
+        "linear_i8": dict(M=4, N=6, K=8, X=P, ldx=ld, x_scale=P, W=P, ldw=ld, w_scale=P, Y=P, ldy=ld),
+        "glu_i8": dict(M=4, N=6, K=8, X=P, ldx=ld, x_scale=P, Wg=P, ldwg=ld, wg_scale=P, Wu=P, ldwu=ld, wu_scale=P, H=P, ldh=ld),
     }
     for name, good in calls.items():
         for axis in "MN":
