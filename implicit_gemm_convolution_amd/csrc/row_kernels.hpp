@@ -53,30 +53,62 @@ struct Raw<T_F32> {
   __device__ __forceinline__ void store(uint8_t* p, int valid) const { store_f32<8>(reinterpret_cast<float*>(p), valid, v); }
 };
 
-// A value of every thread of a row's T threads, combined in every one of
-// them: lanes of a wave first, then the waves through LDS.  Calls in a row take
-// slots in turn (two are enough: who writes a slot again has passed the
-// barrier of the other one, which everyone reaches after reading this one).
-template <int T, class V, class F>
-__device__ __forceinline__ V row_combine(V v, V* slot, F&& f) {
+// ---------------------------------------------------------------------------
+// Sums and maxima over the threads of a row.
+// ---------------------------------------------------------------------------
+// Every lane combined in every lane: within rows of 16 lanes by cross-lane
+// operands of the vector unit, the four rows through scalar registers (the way
+// through LDS, a shuffle a step, takes twelve trips of over 60 cycles each).
+// The order is fixed, and the same in every lane.
+template <class V, class F>
+__device__ __forceinline__ V wave_combine(V v, F&& f) {
+  static_assert(sizeof(V) == 4, "one register");
+  auto other = [](V x, auto ctrl) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v = f(v, other(v, std::integral_constant<int, 0xB1>()));   // quad_perm [1, 0, 3, 2]
+  v = f(v, other(v, std::integral_constant<int, 0x4E>()));   // quad_perm [2, 3, 0, 1]
+  v = f(v, other(v, std::integral_constant<int, 0x141>()));  // the other half of 8
+  v = f(v, other(v, std::integral_constant<int, 0x140>()));  // the other half of 16
+  auto lane = [&](int l) { return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+  return f(f(lane(0), lane(16)), f(lane(32), lane(48)));
+}
+
+// N values of every thread of a row's T threads, combined in every one of
+// them: the lanes of a wave, then the waves through LDS, with one barrier (of
+// the whole workgroup).  slot: W entries of the row.  Calls take slots in turn,
+// two at least: who writes a slot again has passed the barrier of the other
+// one, which everyone reaches after reading this one.
+template <int T, int N, class V, class F>
+__device__ __forceinline__ void row_combine(V (&v)[N], V (*slot)[N], F&& f) {
 #pragma unroll
-  for (int o = 32; o; o >>= 1) v = f(v, __shfl_xor(v, o));
+  for (int i = 0; i < N; ++i) v[i] = wave_combine(v[i], f);
   if constexpr (T > 64) {
-    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = slot[0];
+    const int t = threadIdx.x % T;
+    if ((t & 63) == 0) {
 #pragma unroll
-    for (int i = 1; i < T / 64; ++i) v = f(v, slot[i]);
+      for (int i = 0; i < N; ++i) slot[t >> 6][i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = slot[0][i];
+#pragma unroll
+      for (int w = 1; w < T / 64; ++w) v[i] = f(v[i], slot[w][i]);
+    }
   }
-  return v;
 }
 template <int T>
-__device__ __forceinline__ float row_sum(float v, float* slot) {
-  return row_combine<T>(v, slot, [](float a, float b) { return a + b; });
+__device__ __forceinline__ float row_sum(float v, float (*slot)[1]) {
+  float a[1] = {v};
+  row_combine<T, 1>(a, slot, [](float x, float y) { return x + y; });
+  return a[0];
 }
 template <int T>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* slot) {
-  return row_combine<T>(v, slot, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*slot)[1]) {
+  uint32_t a[1] = {v};
+  row_combine<T, 1>(a, slot, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+  return a[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -148,57 +180,125 @@ struct RowArgs {
   float* scale;  // or NULL: no rows in 8 bits
 };
 
-// A row by T threads: 64 take rows of a wave each, more share a workgroup's
-// row.  C: the row stays in registers, C chunks of 8 elements a thread; 0: it is
-// read again in every pass.  NORM: the norm of the rows (Y, Q or both);
-// otherwise Q alone.  X of type XT, Y and what is put into 8 bits of type OT.
+// A row by T threads (64: a wave has rows of its own), in registers: C chunks
+// of 8 elements a thread.  NORM: the norm of the rows (Y, Q or both); otherwise
+// Q alone.  X of type XT, Y and what is put into 8 bits of type OT.  A
+// workgroup walks over rows: gamma and beta stay in registers, and the next row
+// is on its way while this one is summed.
 template <bool NORM, int XT, int OT, int T, int C>
 __global__ void __launch_bounds__(T < 256 ? 256 : T) row_kernel(const RowArgs p) {
   constexpr int RG = T < 256 ? 256 / T : 1;  // rows of a workgroup
   constexpr int W = T / 64;
-  __shared__ float sums[2][W];
-  __shared__ uint32_t tops[2][W];
+  __shared__ float sums[2][W][1];
+  __shared__ uint32_t tops[2][W][1];
   const int t = threadIdx.x % T;
-  int turn = 0;
-  for (long long row = (long long)blockIdx.x * RG + threadIdx.x / T; row < p.M; row += (long long)gridDim.x * RG, turn ^= 1) {
+  auto col = [&](int j) { return (j * T + t) * 8; };
+  float gamma[C][8], beta[C][8];
+  Raw<XT> next[C];
+  auto load = [&](long long row) {
     const uint8_t* const x = p.X + row * p.ldx * Raw<XT>::EB;
-    Raw<XT> keep[C ? C : 1];
-    // f(chunk of 8, its first column, how many of its columns are in the row)
-    auto chunks = [&](bool first, auto&& f) {
-      if constexpr (C > 0) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          const int c = (j * T + t) * 8;
-          if (first && c < p.N) keep[j].load(x + (long long)c * Raw<XT>::EB, p.N - c);
-        }
+    for (int j = 0; j < C; ++j)
+      if (col(j) < p.N) next[j].load(x + (long long)col(j) * Raw<XT>::EB, p.N - col(j));
+  };
+  const long long step = (long long)gridDim.x * RG;
+  long long row = (long long)blockIdx.x * RG + threadIdx.x / T;
+  if (row < p.M) load(row);
+  if constexpr (NORM) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          const int c = (j * T + t) * 8;
-          if (c < p.N) {
-            float v[8];
-            keep[j].get(v);
-            f(v, c, min(p.N - c, 8));
-          }
-        }
+    for (int j = 0; j < C; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        gamma[j][e] = 1.0f;
+        beta[j][e] = 0.0f;
+      }
+      if (p.gamma && col(j) < p.N) load_f32<8>(p.gamma + col(j), p.N - col(j), gamma[j]);
+      if (p.beta && col(j) < p.N) load_f32<8>(p.beta + col(j), p.N - col(j), beta[j]);
+    }
+  }
+  for (int turn = 0; row < p.M; row += step, turn ^= 1) {
+    float v[C][8];
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (col(j) < p.N) {
+        next[j].get(v[j]);
       } else {
-        for (int c = t * 8; c < p.N; c += T * 8) {
-          float v[8];
-          keep[0].load(x + (long long)c * Raw<XT>::EB, p.N - c);
-          keep[0].get(v);
-          f(v, c, min(p.N - c, 8));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
+      }
+    if (row + step < p.M) load(row + step);
+    if constexpr (NORM) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[j][e];  // (zeros past the row)
+      const float mean = row_sum<T>(s, sums[0]) * p.inv_n;
+      s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[j][e] -= mean;
+          if (col(j) + e < p.N) s = __builtin_fmaf(v[j][e], v[j][e], s);
         }
+      const float rstd = 1.0f / __builtin_sqrtf(row_sum<T>(s, sums[1]) * p.inv_n + p.eps);
+      if (t == 0 && p.mean) p.mean[row] = mean;
+      if (t == 0 && p.rstd) p.rstd[row] = rstd;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = __builtin_fmaf(v[j][e] * rstd, gamma[j][e], beta[j][e]);
+        if (col(j) < p.N) {
+          Raw<OT> out;
+          out.set(v[j]);
+          if (p.Y) out.store(p.Y + (row * p.ldy + col(j)) * Raw<OT>::EB, p.N - col(j));
+          out.get(v[j]);
+        }
+      }
+    }
+    if (p.scale) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < C; ++j) top = max_bits(top, v[j], p.N - col(j));
+      const Quantizer q(row_max<T>(top, tops[turn]));
+      if (t == 0) p.scale[row] = q.scale;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (col(j) < p.N) q.store(p.Q + row * p.ldq + col(j), p.N - col(j), v[j]);
+    }
+  }
+}
+
+// Rows that registers do not hold: read again in every pass.
+template <bool NORM, int XT, int OT, int T>
+__global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
+  constexpr int W = T / 64;
+  __shared__ float sums[2][W][1];
+  __shared__ uint32_t tops[2][W][1];
+  int turn = 0;
+  for (long long row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
+    const uint8_t* const x = p.X + row * p.ldx * Raw<XT>::EB;
+    // f(chunk of 8, its first column, how many of its columns are in the row)
+    auto chunks = [&](auto&& f) {
+      for (int c = threadIdx.x * 8; c < p.N; c += T * 8) {
+        float v[8];
+        Raw<XT> raw;
+        raw.load(x + (long long)c * Raw<XT>::EB, p.N - c);
+        raw.get(v);
+        f(v, c, min(p.N - c, 8));
       }
     };
     float mean = 0.0f, rstd = 1.0f;
     if constexpr (NORM) {
       float s = 0.0f;
-      chunks(true, [&](const float(&v)[8], int, int n) {
+      chunks([&](const float(&v)[8], int, int) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v[e];  // (zeros past the row)
       });
       mean = row_sum<T>(s, sums[0]) * p.inv_n;
       s = 0.0f;
-      chunks(false, [&](const float(&v)[8], int, int n) {
+      chunks([&](const float(&v)[8], int, int n) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float d = e < n ? v[e] - mean : 0.0f;
@@ -206,43 +306,39 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) row_kernel(const RowArgs p)
         }
       });
       rstd = 1.0f / __builtin_sqrtf(row_sum<T>(s, sums[1]) * p.inv_n + p.eps);
-      if (t == 0 && p.mean) p.mean[row] = mean;
-      if (t == 0 && p.rstd) p.rstd[row] = rstd;
+      if (threadIdx.x == 0 && p.mean) p.mean[row] = mean;
+      if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
     }
-    auto normed = [&](float(&v)[8], int c, int n) {
+    auto normed = [&](float(&v)[8], int c, int n) {  // rounded to OT
       if constexpr (NORM) {
         float g[8], b[8];
         if (p.gamma) load_f32<8>(p.gamma + c, n, g);
         if (p.beta) load_f32<8>(p.beta + c, n, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          v[e] = (v[e] - mean) * rstd;
-          if (p.gamma) v[e] *= g[e];
-          if (p.beta) v[e] += b[e];
+          v[e] = __builtin_fmaf((v[e] - mean) * rstd, p.gamma ? g[e] : 1.0f, p.beta ? b[e] : 0.0f);
+          // (both passes round this fp32 value: an instruction that rounds the sum straight to fp16 may be chosen in one alone)
+          asm("" : "+v"(v[e]));
         }
       }
+      Raw<OT> out;
+      out.set(v);
+      out.get(v);
+      return out;
     };
     uint32_t top = 0;
     if (!NORM || p.Y || p.scale) {
-      chunks(!NORM, [&](float(&v)[8], int c, int n) {
-        normed(v, c, n);
-        Raw<OT> out;
-        out.set(v);
+      chunks([&](float(&v)[8], int c, int n) {
+        const Raw<OT> out = normed(v, c, n);
         if (p.Y) out.store(p.Y + (row * p.ldy + c) * Raw<OT>::EB, n);
-        if (p.scale) {
-          out.get(v);
-          top = max_bits(top, v, n);
-        }
+        if (p.scale) top = max_bits(top, v, n);
       });
     }
     if (p.scale) {
       const Quantizer q(row_max<T>(top, tops[turn]));
-      if (t == 0) p.scale[row] = q.scale;
-      chunks(false, [&](float(&v)[8], int c, int n) {
+      if (threadIdx.x == 0) p.scale[row] = q.scale;
+      chunks([&](float(&v)[8], int c, int n) {
         normed(v, c, n);
-        Raw<OT> out;
-        out.set(v);
-        out.get(v);
         q.store(p.Q + row * p.ldq + c, n, v);
       });
     }
@@ -267,15 +363,125 @@ struct NormBackArgs {
   int rows, groups, blocks;  // rows of a block; workgroups across the columns and down the rows
 };
 
+// Rows in registers: T threads a row, C chunks of 8 elements a thread, WG / T
+// rows at a time, one reduction of two sums a row, and the sums down the rows
+// in the registers of the threads that hold their columns.  Each input is read
+// once.  The next row is on its way while this one is summed.
+template <int XT, int OT, int T, int C, int WG>
+__global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p) {
+  constexpr int RG = WG / T, W = T / 64, COLS = T * C * 8;
+  __shared__ float slots[2][RG][W][2];
+  __shared__ float part[RG > 1 ? RG * COLS : 1];
+  const int t = threadIdx.x % T, rg = threadIdx.x / T;
+  auto col = [&](int j) { return (j * T + t) * 8; };
+  float gamma[C][8], sg[C][8], sb[C][8];
+  Raw<OT> dy[C];
+  Raw<XT> x[C], r[C];
+  auto load = [&](long long row) {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (col(j) < p.N) {
+        const int n = p.N - col(j);
+        dy[j].load(p.dY + (row * p.lddy + col(j)) * Raw<OT>::EB, n);
+        x[j].load(p.X + (row * p.ldx + col(j)) * Raw<XT>::EB, n);
+        if (p.R) r[j].load(p.R + (row * p.ldr + col(j)) * Raw<XT>::EB, n);
+      }
+  };
+  const long long step = (long long)gridDim.x * RG;
+  long long first = (long long)blockIdx.x * RG;
+  if (first + rg < p.M) load(first + rg);
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      gamma[j][e] = 1.0f;
+      sg[j][e] = sb[j][e] = 0.0f;
+    }
+    if (p.gamma && col(j) < p.N) load_f32<8>(p.gamma + col(j), p.N - col(j), gamma[j]);
+  }
+  for (int turn = 0; first < p.M; first += step, turn ^= 1) {  // (as often for every row of the workgroup: the barrier)
+    const long long row = first + rg;
+    const bool in = row < p.M;
+    const float mean = in ? p.mean[row] : 0.0f, rstd = in ? p.rstd[row] : 0.0f;
+    float d[C][8], v[C][8], a[C][8];
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (in && col(j) < p.N) {
+        dy[j].get(d[j]);
+        x[j].get(v[j]);
+        if (p.R) r[j].get(a[j]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[j][e] = v[j][e] = a[j][e] = 0.0f;
+      }
+    if (row + step < p.M) load(row + step);
+    float m[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[j][e] = (v[j][e] - mean) * rstd;
+        sg[j][e] = __builtin_fmaf(d[j][e], v[j][e], sg[j][e]);
+        sb[j][e] += d[j][e];
+        d[j][e] *= gamma[j][e];
+        if (col(j) + e < p.N) {
+          m[0] += d[j][e];
+          m[1] = __builtin_fmaf(d[j][e], v[j][e], m[1]);
+        }
+      }
+    if (!p.dX) continue;
+    row_combine<T, 2>(m, slots[turn][rg], [](float f, float g) { return f + g; });
+    m[0] *= p.inv_n;
+    m[1] *= p.inv_n;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (in && col(j) < p.N) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[j][e] = rstd * (__builtin_fmaf(-v[j][e], m[1], d[j][e]) - m[0]);
+          if (p.R) v[j][e] += a[j][e];
+        }
+        Raw<XT> out;
+        out.set(v[j]);
+        out.store(p.dX + (row * p.lddx + col(j)) * Raw<XT>::EB, p.N - col(j));
+      }
+  }
+  if (!p.sums) return;
+  float* const to = p.sums + (long long)blockIdx.x * 2 * p.width;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const auto& s = which ? sb : sg;
+    if constexpr (RG == 1) {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (col(j) < p.N) store_f32<8>(to + which * p.width + col(j), p.N - col(j), s[j]);
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < C; ++j) __builtin_memcpy(part + rg * COLS + col(j), s[j], 32);
+      __syncthreads();
+      for (int c = threadIdx.x; c < COLS && c < p.N; c += WG) {
+        float f = part[c];
+#pragma unroll
+        for (int i = 1; i < RG; ++i) f += part[i * COLS + c];
+        to[which * p.width + c] = f;
+      }
+    }
+  }
+}
+
+// Rows that registers do not hold: two launches, which read dY and X twice.
+
 // mean(g) and mean(g xh) of every row.
 template <int XT, int OT, int T>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) norm_back_stats_kernel(const NormBackArgs p) {
-  constexpr int RG = T < 256 ? 256 / T : 1, W = T / 64;
-  __shared__ float sums[2][W];
-  const int t = threadIdx.x % T;
-  for (long long row = (long long)blockIdx.x * RG + threadIdx.x / T; row < p.M; row += (long long)gridDim.x * RG) {
+__global__ void __launch_bounds__(T) norm_back_stats_kernel(const NormBackArgs p) {
+  constexpr int W = T / 64;
+  __shared__ float sums[2][W][2];
+  const int t = threadIdx.x;
+  int turn = 0;
+  for (long long row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float s = 0.0f, sx = 0.0f;
+    float m[2] = {0.0f, 0.0f};
     for (int c = t * 8; c < p.N; c += T * 8) {
       const int n = min(p.N - c, 8);
       Raw<OT> dy;
@@ -289,13 +495,12 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_back_stats_kernel(cons
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float ge = e < n ? (p.gamma ? d[e] * g[e] : d[e]) : 0.0f;
-        s += ge;
-        if (e < n) sx = __builtin_fmaf(ge, (v[e] - mean) * rstd, sx);
+        m[0] += ge;
+        if (e < n) m[1] = __builtin_fmaf(ge, (v[e] - mean) * rstd, m[1]);
       }
     }
-    s = row_sum<T>(s, sums[0]);
-    sx = row_sum<T>(sx, sums[1]);
-    if (t == 0) p.stats[row] = make_float2(s * p.inv_n, sx * p.inv_n);
+    row_combine<T, 2>(m, sums[turn], [](float f, float g) { return f + g; });
+    if (t == 0) p.stats[row] = make_float2(m[0] * p.inv_n, m[1] * p.inv_n);
   }
 }
 

@@ -39,21 +39,28 @@ void check_rows(Checker& c, int M, int N, int type) {
 
 // ---------------------------------------------------------------- rows
 // Threads to a row: those whose chunks hold it in registers, a wave for rows
-// of up to 2048 elements; longer rows than 32768 are read again in every pass.
+// of up to 2048 elements.  Few rows (no more than compute units) take as many
+// threads as they have chunks: latency.  Rows longer than 16384 are read again
+// in every pass.
 template <bool NORM, int XT, int OT>
 void launch_rows(const RowArgs& a, int cus, hipStream_t stream) {
-  auto run = [&](auto kernel, int threads, int rows) {
-    const long long groups = std::min(ceil_div(a.M, rows), 16LL * cus);
+  // places: workgroups that a compute unit takes at once
+  auto run = [&](auto kernel, int threads, int rows, int places) {
+    const long long groups = std::min(ceil_div(a.M, rows), (long long)places * cus);
     hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), 0, stream, a);
   };
   if (a.N <= 2048)
-    run(igc_rows::row_kernel<NORM, XT, OT, 64, 4>, 256, 4);
+    run(igc_rows::row_kernel<NORM, XT, OT, 64, 4>, 256, 4, 4);
+  else if (a.N <= 8192 && a.M <= cus)
+    run(igc_rows::row_kernel<NORM, XT, OT, 1024, 1>, 1024, 1, 1);
+  else if (a.N <= 4096)
+    run(igc_rows::row_kernel<NORM, XT, OT, 256, 2>, 256, 1, 6);
   else if (a.N <= 8192)
-    run(igc_rows::row_kernel<NORM, XT, OT, 256, 4>, 256, 1);
-  else if (a.N <= 32768)
-    run(igc_rows::row_kernel<NORM, XT, OT, 1024, 4>, 1024, 1);
+    run(igc_rows::row_kernel<NORM, XT, OT, 256, 4>, 256, 1, 4);
+  else if (a.N <= 16384)
+    run(igc_rows::row_kernel<NORM, XT, OT, 1024, 2>, 1024, 1, 1);
   else
-    run(igc_rows::row_kernel<NORM, XT, OT, 1024, 0>, 1024, 1);
+    run(igc_rows::long_row_kernel<NORM, XT, OT, 1024>, 1024, 1, 2);
 }
 
 int layer_norm_forward_impl(const igc_layer_norm_forward* d, hipStream_t stream) {
@@ -133,15 +140,44 @@ int quantize_rows_impl(const igc_quantize_rows* d, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------- backward
+// How a backward pass splits its rows: registers hold rows of up to 8192
+// elements (T threads a row, C chunks a thread, WG threads); longer ones go by
+// columns, after a launch for their means.
+struct BackPlan {
+  bool in_registers;
+  int rows, groups, blocks;  // rows at a time (a block, by columns); workgroups
+};
+BackPlan plan_back(long long M, int N, int cus) {
+  BackPlan b;
+  b.in_registers = N <= 8192;
+  if (b.in_registers) {
+    b.rows = N <= 1024 ? 8 : N <= 4096 ? 2 : 1;
+    b.groups = 1;
+    b.blocks = (int)std::min(ceil_div(M, b.rows), 2LL * cus);
+  } else {
+    // enough workgroups to fill the card, and few enough that their sums stay small beside the rows
+    b.groups = (int)ceil_div(N, 512);
+    b.rows = (int)std::max(16LL, ceil_div(M, std::max(1LL, 4LL * cus / b.groups)));
+    b.blocks = (int)ceil_div(M, b.rows);
+  }
+  return b;
+}
+
 template <int XT, int OT>
-int launch_back(const NormBackArgs& a, int cus, bool stats, hipStream_t stream) {
-  if (stats) {
-    if (a.N <= 2048)
-      hipLaunchKernelGGL((igc_rows::norm_back_stats_kernel<XT, OT, 64>), dim3((unsigned)std::min(ceil_div(a.M, 4), 16LL * cus)), dim3(256), 0,
-                         stream, a);
+int launch_back(const NormBackArgs& a, const BackPlan& pl, int cus, hipStream_t stream) {
+  auto run = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.blocks), dim3(threads), 0, stream, a); };
+  if (pl.in_registers) {
+    if (a.N <= 1024)
+      run(igc_rows::norm_back_rows_kernel<XT, OT, 64, 2, 512>, 512);
+    else if (a.N <= 4096)
+      run(igc_rows::norm_back_rows_kernel<XT, OT, 256, 2, 512>, 512);
     else
-      hipLaunchKernelGGL((igc_rows::norm_back_stats_kernel<XT, OT, 256>), dim3((unsigned)std::min<long long>(a.M, 16LL * cus)), dim3(256), 0,
-                         stream, a);
+      run(igc_rows::norm_back_rows_kernel<XT, OT, 512, 2, 512>, 512);
+    return launch_status();
+  }
+  if (a.dX) {
+    hipLaunchKernelGGL((igc_rows::norm_back_stats_kernel<XT, OT, 1024>), dim3((unsigned)std::min<long long>(a.M, 2LL * cus)), dim3(1024), 0,
+                       stream, a);
     if (int s = launch_status()) return s;
   }
   hipLaunchKernelGGL((igc_rows::norm_back_kernel<XT, OT>), dim3((unsigned)((long long)a.groups * a.blocks)), dim3(256), 0, stream, a);
@@ -173,18 +209,17 @@ int layer_norm_backward_impl(const igc_layer_norm_backward* d, size_t* query, hi
   int dev;
   if (int s = check_device(&dev)) return s;
   const int cus = device_cus(dev);
-  const bool want_x = d->dX && d->M > 0, sums = d->dgamma || d->dbeta;
-  const int width = (int)ceil_div(d->N, 64) * 64, groups = (int)ceil_div(d->N, 512);
-  // rows of a block: enough workgroups to fill the card, and few enough that their sums stay small beside the rows
-  const int rows = (int)std::max(16LL, ceil_div(d->M, std::max(1LL, 4LL * cus / groups)));
-  const int blocks = (int)ceil_div(d->M, rows);
-  const size_t stat_bytes = want_x ? round256((size_t)d->M * sizeof(float2)) : 0;
-  const size_t need = stat_bytes + (sums ? round256((size_t)blocks * 2 * width * sizeof(float)) : 0);
+  const bool sums = d->dgamma || d->dbeta;
+  const int width = (int)ceil_div(d->N, 64) * 64;
+  const BackPlan pl = plan_back(d->M, d->N, cus);
+  const size_t stat_bytes = d->dX && !pl.in_registers ? round256((size_t)d->M * sizeof(float2)) : 0;
+  const size_t need = stat_bytes + (sums ? round256((size_t)pl.blocks * 2 * width * sizeof(float)) : 0);
   if (query) {
     *query = need;
     return IGC_OK;
   }
-  if ((long long)groups * blocks > 0x7fffffLL) return fail(IGC_EUNSUPPORTED, "too many workgroups (%lld)", (long long)groups * blocks);
+  if ((long long)pl.groups * pl.blocks > 0x7fffffLL)
+    return fail(IGC_EUNSUPPORTED, "too many workgroups (%lld)", (long long)pl.groups * pl.blocks);
   if (int s = check_ws(d->workspace, d->ws_bytes, need, true)) return s;
   NormBackArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -205,21 +240,21 @@ int layer_norm_backward_impl(const igc_layer_norm_backward* d, size_t* query, hi
   a.stats = static_cast<float2*>(d->workspace);
   a.sums = sums ? reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + stat_bytes) : nullptr;
   a.width = width;
-  a.rows = rows;
-  a.groups = groups;
-  a.blocks = blocks;
+  a.rows = pl.rows;
+  a.groups = pl.groups;
+  a.blocks = pl.blocks;
   if (d->M > 0) {
     using namespace igc_ffn;
     const bool wide = d->x_type == IGC_F32;
     int s;
     if (d->type == IGC_BF16)
-      s = wide ? launch_back<T_F32, T_BF16>(a, cus, want_x, stream) : launch_back<T_BF16, T_BF16>(a, cus, want_x, stream);
+      s = wide ? launch_back<T_F32, T_BF16>(a, pl, cus, stream) : launch_back<T_BF16, T_BF16>(a, pl, cus, stream);
     else
-      s = wide ? launch_back<T_F32, T_F16>(a, cus, want_x, stream) : launch_back<T_F16, T_F16>(a, cus, want_x, stream);
+      s = wide ? launch_back<T_F32, T_F16>(a, pl, cus, stream) : launch_back<T_F16, T_F16>(a, pl, cus, stream);
     if (s) return s;
   }
   if (!sums) return IGC_OK;
-  const igc_ffn::ColsumArgs cs{a.sums, blocks, 2, width, d->N, d->dgamma, d->dbeta};
+  const igc_ffn::ColsumArgs cs{a.sums, pl.blocks, 2, width, d->N, d->dgamma, d->dbeta};
   hipLaunchKernelGGL((igc_ffn::colsum_kernel<0>), dim3((unsigned)igc_ffn_host::colsum_groups(cs)), dim3(256), 0, stream, cs);
   return launch_status();
 }
