@@ -55,11 +55,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs p) {
   long long row = first / (uint32_t)p.per;
   int chunk = (int)(first - (uint32_t)row * (uint32_t)p.per);
   while (row < p.M) {
-    const int c = chunk * 8, n = min(p.N - c, 8);
+    const int c = chunk * 8;
     Raw<XT> x;
     Raw<YT> r;
-    x.load(p.X + (row * p.ldx + c) * Raw<XT>::EB, n);
-    if (p.R) r.load(p.R + (row * p.ldr + c) * Raw<YT>::EB, n);
+    x.load(p.X + row * p.ldx * Raw<XT>::EB, c, p.N);
+    if (p.R) r.load(p.R + row * p.ldr * Raw<YT>::EB, c, p.N);
     float f[8];
     x.get(f);
     if (p.drops) {
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs p) {
       for (int e = 0; e < 8; ++e) f[e] += a[e];
     }
     r.set(f);
-    r.store(p.Y + (row * p.ldy + c) * Raw<YT>::EB, n);
+    r.store(p.Y + row * p.ldy * Raw<YT>::EB, c, p.N);
     row += p.step_row;
     chunk += p.step_chunk;
     if (chunk >= p.per) {

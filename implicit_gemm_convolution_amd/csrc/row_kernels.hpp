@@ -27,21 +27,47 @@ using igc_ffn::store8;
 using igc_ffn::store_f32;
 using igc_ffn::unpack8;
 
-// Eight elements of type T (igc_ffn::Type) as they lie in memory.
+// Eight elements of type T (igc_ffn::Type) as they lie in memory: those of a row
+// of n elements from column c, zeros past the row.  The chunk at a row's end is
+// loaded as the row's last eight elements and shifted (element by element, its
+// loads would wait for one another).
 template <int T>
 struct Raw {
   static constexpr int EB = 2;
   uint4 v;
-  __device__ __forceinline__ void load(const uint8_t* p, int valid) { v = load8(p, valid); }  // (zeros past `valid`)
+  __device__ __forceinline__ void load(const uint8_t* row, int c, int n) {
+    const uint8_t* const p = row + (long long)c * 2;
+    if (n - c >= 8 || c == 0) {
+      v = load8(p, n - c);
+    } else {
+      const int over = c + 8 - n;
+      unsigned __int128 w;
+      __builtin_memcpy(&w, p - over * 2, 16);
+      w >>= 16 * over;
+      __builtin_memcpy(&v, &w, 16);
+    }
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const { unpack8<T == T_BF16>(v, f); }
   __device__ __forceinline__ void set(const float (&f)[8]) { v = pack8<T == T_BF16>(f); }
-  __device__ __forceinline__ void store(uint8_t* p, int valid) const { store8(p, v, valid); }
+  __device__ __forceinline__ void store(uint8_t* row, int c, int n) const { store8(row + (long long)c * 2, v, n - c); }
 };
 template <>
 struct Raw<T_F32> {
   static constexpr int EB = 4;
   float v[8];
-  __device__ __forceinline__ void load(const uint8_t* p, int valid) { load_f32<8>(reinterpret_cast<const float*>(p), valid, v); }
+  __device__ __forceinline__ void load(const uint8_t* row, int c, int n) {
+    const float* const p = reinterpret_cast<const float*>(row) + c;
+    if (n - c >= 8 || c == 0) {
+      load_f32<8>(p, n - c, v);
+    } else {
+      const int over = c + 8 - n;
+      load_f32<8>(p - over, 8, v);
+#pragma unroll
+      for (int s = 4; s; s >>= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = !(over & s) ? v[e] : e + s < 8 ? v[(e + s) & 7] : 0.0f;
+    }
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = v[e];
@@ -50,17 +76,26 @@ struct Raw<T_F32> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = f[e];
   }
-  __device__ __forceinline__ void store(uint8_t* p, int valid) const { store_f32<8>(reinterpret_cast<float*>(p), valid, v); }
+  __device__ __forceinline__ void store(uint8_t* row, int c, int n) const {
+    store_f32<8>(reinterpret_cast<float*>(row) + c, n - c, v);
+  }
 };
+// Of a vector of n fp32 values.
+__device__ __forceinline__ void load_vector(const float* p, int c, int n, float (&f)[8]) {
+  Raw<T_F32> r;
+  r.load(reinterpret_cast<const uint8_t*>(p), c, n);
+  r.get(f);
+}
 
 // ---------------------------------------------------------------------------
 // Sums and maxima over the threads of a row.
 // ---------------------------------------------------------------------------
-// Every lane combined in every lane: within rows of 16 lanes by cross-lane
-// operands of the vector unit, the four rows through scalar registers (the way
-// through LDS, a shuffle a step, takes twelve trips of over 60 cycles each).
-// The order is fixed, and the same in every lane.
-template <class V, class F>
+// The lanes of a group of T (16, 32 or 64) combined in every one of them:
+// within rows of 16 lanes by cross-lane operands of the vector unit, the four
+// rows of a wave through scalar registers (the way through LDS, a shuffle a step,
+// takes twelve trips of over 60 cycles each).  The order is fixed, and the same
+// in every lane.
+template <int T, class V, class F>
 __device__ __forceinline__ V wave_combine(V v, F&& f) {
   static_assert(sizeof(V) == 4, "one register");
   auto other = [](V x, auto ctrl) {
@@ -70,8 +105,11 @@ __device__ __forceinline__ V wave_combine(V v, F&& f) {
   v = f(v, other(v, std::integral_constant<int, 0x4E>()));   // quad_perm [2, 3, 0, 1]
   v = f(v, other(v, std::integral_constant<int, 0x141>()));  // the other half of 8
   v = f(v, other(v, std::integral_constant<int, 0x140>()));  // the other half of 16
+  if constexpr (T == 16) return v;
   auto lane = [&](int l) { return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
-  return f(f(lane(0), lane(16)), f(lane(32), lane(48)));
+  const V low = f(lane(0), lane(16)), high = f(lane(32), lane(48));
+  if constexpr (T == 32) return (threadIdx.x & 32) ? high : low;
+  return f(low, high);
 }
 
 // N values of every thread of a row's T threads, combined in every one of
@@ -82,7 +120,7 @@ __device__ __forceinline__ V wave_combine(V v, F&& f) {
 template <int T, int N, class V, class F>
 __device__ __forceinline__ void row_combine(V (&v)[N], V (*slot)[N], F&& f) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_combine(v[i], f);
+  for (int i = 0; i < N; ++i) v[i] = wave_combine<(T < 64 ? T : 64)>(v[i], f);
   if constexpr (T > 64) {
     const int t = threadIdx.x % T;
     if ((t & 63) == 0) {
@@ -180,30 +218,31 @@ struct RowArgs {
   float* scale;  // or NULL: no rows in 8 bits
 };
 
-// A row by T threads (64: a wave has rows of its own), in registers: C chunks
-// of 8 elements a thread.  NORM: the norm of the rows (Y, Q or both); otherwise
-// Q alone.  X of type XT, Y and what is put into 8 bits of type OT.  A
-// workgroup walks over rows: gamma and beta stay in registers, and the next row
-// is on its way while this one is summed.
+// A row by T threads, in registers: C chunks of 8 elements a thread, 256 / T
+// rows of a workgroup at a time where T is less.  NORM: the norm of the rows (Y,
+// Q or both); otherwise Q alone.  X of type XT, Y and what is put into 8 bits of
+// type OT.  A workgroup walks over rows: gamma and beta stay in registers, and
+// the next row is on its way while this one is summed.
+template <int T>
+constexpr int row_threads = T < 256 ? 256 : T;
 template <bool NORM, int XT, int OT, int T, int C>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) row_kernel(const RowArgs p) {
-  constexpr int RG = T < 256 ? 256 / T : 1;  // rows of a workgroup
-  constexpr int W = T / 64;
-  __shared__ float sums[2][W][1];
-  __shared__ uint32_t tops[2][W][1];
-  const int t = threadIdx.x % T;
+__global__ void __launch_bounds__(row_threads<T>) row_kernel(const RowArgs p) {
+  constexpr int RG = row_threads<T> / T;  // rows of a workgroup
+  constexpr int W = T < 64 ? 1 : T / 64;
+  __shared__ float sums[2][RG][W][1];
+  __shared__ uint32_t tops[2][RG][W][1];
+  const int t = threadIdx.x % T, rg = threadIdx.x / T;
   auto col = [&](int j) { return (j * T + t) * 8; };
   float gamma[C][8], beta[C][8];
   Raw<XT> next[C];
   auto load = [&](long long row) {
-    const uint8_t* const x = p.X + row * p.ldx * Raw<XT>::EB;
 #pragma unroll
     for (int j = 0; j < C; ++j)
-      if (col(j) < p.N) next[j].load(x + (long long)col(j) * Raw<XT>::EB, p.N - col(j));
+      if (col(j) < p.N) next[j].load(p.X + row * p.ldx * Raw<XT>::EB, col(j), p.N);
   };
   const long long step = (long long)gridDim.x * RG;
-  long long row = (long long)blockIdx.x * RG + threadIdx.x / T;
-  if (row < p.M) load(row);
+  long long first = (long long)blockIdx.x * RG;
+  if (first + rg < p.M) load(first + rg);
   if constexpr (NORM) {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
@@ -212,15 +251,17 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) row_kernel(const RowArgs p)
         gamma[j][e] = 1.0f;
         beta[j][e] = 0.0f;
       }
-      if (p.gamma && col(j) < p.N) load_f32<8>(p.gamma + col(j), p.N - col(j), gamma[j]);
-      if (p.beta && col(j) < p.N) load_f32<8>(p.beta + col(j), p.N - col(j), beta[j]);
+      if (p.gamma && col(j) < p.N) load_vector(p.gamma, col(j), p.N, gamma[j]);
+      if (p.beta && col(j) < p.N) load_vector(p.beta, col(j), p.N, beta[j]);
     }
   }
-  for (int turn = 0; row < p.M; row += step, turn ^= 1) {
+  for (int turn = 0; first < p.M; first += step, turn ^= 1) {  // (as often for every row of the workgroup: the barriers)
+    const long long row = first + rg;
+    const bool in = row < p.M;
     float v[C][8];
 #pragma unroll
     for (int j = 0; j < C; ++j)
-      if (col(j) < p.N) {
+      if (in && col(j) < p.N) {
         next[j].get(v[j]);
       } else {
 #pragma unroll
@@ -233,7 +274,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) row_kernel(const RowArgs p)
       for (int j = 0; j < C; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v[j][e];  // (zeros past the row)
-      const float mean = row_sum<T>(s, sums[0]) * p.inv_n;
+      const float mean = row_sum<T>(s, sums[0][rg]) * p.inv_n;
       s = 0.0f;
 #pragma unroll
       for (int j = 0; j < C; ++j)
@@ -242,30 +283,28 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) row_kernel(const RowArgs p)
           v[j][e] -= mean;
           if (col(j) + e < p.N) s = __builtin_fmaf(v[j][e], v[j][e], s);
         }
-      const float rstd = 1.0f / __builtin_sqrtf(row_sum<T>(s, sums[1]) * p.inv_n + p.eps);
-      if (t == 0 && p.mean) p.mean[row] = mean;
-      if (t == 0 && p.rstd) p.rstd[row] = rstd;
+      const float rstd = 1.0f / __builtin_sqrtf(row_sum<T>(s, sums[1][rg]) * p.inv_n + p.eps);
+      if (in && t == 0 && p.mean) p.mean[row] = mean;
+      if (in && t == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] = __builtin_fmaf(v[j][e] * rstd, gamma[j][e], beta[j][e]);
-        if (col(j) < p.N) {
-          Raw<OT> out;
-          out.set(v[j]);
-          if (p.Y) out.store(p.Y + (row * p.ldy + col(j)) * Raw<OT>::EB, p.N - col(j));
-          out.get(v[j]);
-        }
+        Raw<OT> out;
+        out.set(v[j]);
+        if (p.Y && in && col(j) < p.N) out.store(p.Y + row * p.ldy * Raw<OT>::EB, col(j), p.N);
+        out.get(v[j]);
       }
     }
     if (p.scale) {
       uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < C; ++j) top = max_bits(top, v[j], p.N - col(j));
-      const Quantizer q(row_max<T>(top, tops[turn]));
-      if (t == 0) p.scale[row] = q.scale;
+      const Quantizer q(row_max<T>(top, tops[turn][rg]));
+      if (in && t == 0) p.scale[row] = q.scale;
 #pragma unroll
       for (int j = 0; j < C; ++j)
-        if (col(j) < p.N) q.store(p.Q + row * p.ldq + col(j), p.N - col(j), v[j]);
+        if (in && col(j) < p.N) q.store(p.Q + row * p.ldq + col(j), p.N - col(j), v[j]);
     }
   }
 }
@@ -284,7 +323,7 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
       for (int c = threadIdx.x * 8; c < p.N; c += T * 8) {
         float v[8];
         Raw<XT> raw;
-        raw.load(x + (long long)c * Raw<XT>::EB, p.N - c);
+        raw.load(x, c, p.N);
         raw.get(v);
         f(v, c, min(p.N - c, 8));
       }
@@ -312,8 +351,8 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
     auto normed = [&](float(&v)[8], int c, int n) {  // rounded to OT
       if constexpr (NORM) {
         float g[8], b[8];
-        if (p.gamma) load_f32<8>(p.gamma + c, n, g);
-        if (p.beta) load_f32<8>(p.beta + c, n, b);
+        if (p.gamma) load_vector(p.gamma, c, p.N, g);
+        if (p.beta) load_vector(p.beta, c, p.N, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           v[e] = __builtin_fmaf((v[e] - mean) * rstd, p.gamma ? g[e] : 1.0f, p.beta ? b[e] : 0.0f);
@@ -330,7 +369,7 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
     if (!NORM || p.Y || p.scale) {
       chunks([&](float(&v)[8], int c, int n) {
         const Raw<OT> out = normed(v, c, n);
-        if (p.Y) out.store(p.Y + (row * p.ldy + c) * Raw<OT>::EB, n);
+        if (p.Y) out.store(p.Y + row * p.ldy * Raw<OT>::EB, c, p.N);
         if (p.scale) top = max_bits(top, v, n);
       });
     }
@@ -369,7 +408,7 @@ struct NormBackArgs {
 // once.  The next row is on its way while this one is summed.
 template <int XT, int OT, int T, int C, int WG>
 __global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p) {
-  constexpr int RG = WG / T, W = T / 64, COLS = T * C * 8;
+  constexpr int RG = WG / T, W = T < 64 ? 1 : T / 64, COLS = T * C * 8;
   __shared__ float slots[2][RG][W][2];
   __shared__ float part[RG > 1 ? RG * COLS : 1];
   const int t = threadIdx.x % T, rg = threadIdx.x / T;
@@ -381,10 +420,9 @@ __global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p
 #pragma unroll
     for (int j = 0; j < C; ++j)
       if (col(j) < p.N) {
-        const int n = p.N - col(j);
-        dy[j].load(p.dY + (row * p.lddy + col(j)) * Raw<OT>::EB, n);
-        x[j].load(p.X + (row * p.ldx + col(j)) * Raw<XT>::EB, n);
-        if (p.R) r[j].load(p.R + (row * p.ldr + col(j)) * Raw<XT>::EB, n);
+        dy[j].load(p.dY + row * p.lddy * Raw<OT>::EB, col(j), p.N);
+        x[j].load(p.X + row * p.ldx * Raw<XT>::EB, col(j), p.N);
+        if (p.R) r[j].load(p.R + row * p.ldr * Raw<XT>::EB, col(j), p.N);
       }
   };
   const long long step = (long long)gridDim.x * RG;
@@ -397,7 +435,7 @@ __global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p
       gamma[j][e] = 1.0f;
       sg[j][e] = sb[j][e] = 0.0f;
     }
-    if (p.gamma && col(j) < p.N) load_f32<8>(p.gamma + col(j), p.N - col(j), gamma[j]);
+    if (p.gamma && col(j) < p.N) load_vector(p.gamma, col(j), p.N, gamma[j]);
   }
   for (int turn = 0; first < p.M; first += step, turn ^= 1) {  // (as often for every row of the workgroup: the barrier)
     const long long row = first + rg;
@@ -443,7 +481,7 @@ __global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p
         }
         Raw<XT> out;
         out.set(v[j]);
-        out.store(p.dX + (row * p.lddx + col(j)) * Raw<XT>::EB, p.N - col(j));
+        out.store(p.dX + row * p.lddx * Raw<XT>::EB, col(j), p.N);
       }
   }
   if (!p.sums) return;
@@ -486,12 +524,12 @@ __global__ void __launch_bounds__(T) norm_back_stats_kernel(const NormBackArgs p
       const int n = min(p.N - c, 8);
       Raw<OT> dy;
       Raw<XT> x;
-      dy.load(p.dY + (row * p.lddy + c) * Raw<OT>::EB, n);
-      x.load(p.X + (row * p.ldx + c) * Raw<XT>::EB, n);
+      dy.load(p.dY + row * p.lddy * Raw<OT>::EB, c, p.N);
+      x.load(p.X + row * p.ldx * Raw<XT>::EB, c, p.N);
       float d[8], v[8], g[8];
       dy.get(d);
       x.get(v);
-      if (p.gamma) load_f32<8>(p.gamma + c, n, g);
+      if (p.gamma) load_vector(p.gamma, c, p.N, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float ge = e < n ? (p.gamma ? d[e] * g[e] : d[e]) : 0.0f;
@@ -518,14 +556,14 @@ __global__ void __launch_bounds__(256) norm_back_kernel(const NormBackArgs p) {
   if (n > 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) gamma[e] = 1.0f;
-    if (p.gamma) load_f32<8>(p.gamma + c, n, gamma);
+    if (p.gamma) load_vector(p.gamma, c, p.N, gamma);
     const long long r0 = (long long)by * p.rows, r1 = min(p.M, r0 + p.rows);
     for (long long row = r0 + wave; row < r1; row += 4) {
       const float mean = p.mean[row], rstd = p.rstd[row];
       Raw<OT> dy;
       Raw<XT> x, r;
-      dy.load(p.dY + (row * p.lddy + c) * Raw<OT>::EB, n);
-      x.load(p.X + (row * p.ldx + c) * Raw<XT>::EB, n);
+      dy.load(p.dY + row * p.lddy * Raw<OT>::EB, c, p.N);
+      x.load(p.X + row * p.ldx * Raw<XT>::EB, c, p.N);
       float d[8], v[8], a[8];
       dy.get(d);
       x.get(v);
@@ -538,7 +576,7 @@ __global__ void __launch_bounds__(256) norm_back_kernel(const NormBackArgs p) {
       if (p.dX) {
         const float2 m = p.stats[row];
         if (p.R) {
-          r.load(p.R + (row * p.ldr + c) * Raw<XT>::EB, n);
+          r.load(p.R + row * p.ldr * Raw<XT>::EB, c, p.N);
           r.get(a);
         }
 #pragma unroll
@@ -547,7 +585,7 @@ __global__ void __launch_bounds__(256) norm_back_kernel(const NormBackArgs p) {
           if (p.R) v[e] += a[e];
         }
         x.set(v);
-        x.store(p.dX + (row * p.lddx + c) * Raw<XT>::EB, n);
+        x.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N);
       }
     }
   }

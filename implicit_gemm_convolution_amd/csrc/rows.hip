@@ -38,29 +38,24 @@ void check_rows(Checker& c, int M, int N, int type) {
 }
 
 // ---------------------------------------------------------------- rows
-// Threads to a row: those whose chunks hold it in registers, a wave for rows
-// of up to 2048 elements.  Few rows (no more than compute units) take as many
-// threads as they have chunks: latency.  Rows longer than 16384 are read again
-// in every pass.
+// Threads to a row: as many as it has chunks, up to 1024 with two chunks each
+// (8192 x 4096 bf16: TODO).  Longer rows are read again in every pass.
 template <bool NORM, int XT, int OT>
 void launch_rows(const RowArgs& a, int cus, hipStream_t stream) {
-  // places: workgroups that a compute unit takes at once
-  auto run = [&](auto kernel, int threads, int rows, int places) {
-    const long long groups = std::min(ceil_div(a.M, rows), (long long)places * cus);
+  auto run = [&](auto kernel, int threads, int rows) {
+    const long long groups = std::min(ceil_div(a.M, rows), 2048LL / threads * cus);
     hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), 0, stream, a);
   };
-  if (a.N <= 2048)
-    run(igc_rows::row_kernel<NORM, XT, OT, 64, 4>, 256, 4, 4);
-  else if (a.N <= 8192 && a.M <= cus)
-    run(igc_rows::row_kernel<NORM, XT, OT, 1024, 1>, 1024, 1, 1);
-  else if (a.N <= 4096)
-    run(igc_rows::row_kernel<NORM, XT, OT, 256, 2>, 256, 1, 6);
-  else if (a.N <= 8192)
-    run(igc_rows::row_kernel<NORM, XT, OT, 256, 4>, 256, 1, 4);
-  else if (a.N <= 16384)
-    run(igc_rows::row_kernel<NORM, XT, OT, 1024, 2>, 1024, 1, 1);
-  else
-    run(igc_rows::long_row_kernel<NORM, XT, OT, 1024>, 1024, 1, 2);
+  using igc_rows::row_kernel;
+  if (a.N <= 128) run(row_kernel<NORM, XT, OT, 16, 1>, 256, 16);
+  else if (a.N <= 256) run(row_kernel<NORM, XT, OT, 32, 1>, 256, 8);
+  else if (a.N <= 512) run(row_kernel<NORM, XT, OT, 64, 1>, 256, 4);
+  else if (a.N <= 1024) run(row_kernel<NORM, XT, OT, 128, 1>, 256, 2);
+  else if (a.N <= 2048) run(row_kernel<NORM, XT, OT, 256, 1>, 256, 1);
+  else if (a.N <= 4096) run(row_kernel<NORM, XT, OT, 512, 1>, 512, 1);
+  else if (a.N <= 8192) run(row_kernel<NORM, XT, OT, 1024, 1>, 1024, 1);
+  else if (a.N <= 16384) run(row_kernel<NORM, XT, OT, 1024, 2>, 1024, 1);
+  else run(igc_rows::long_row_kernel<NORM, XT, OT, 1024>, 1024, 1);
 }
 
 int layer_norm_forward_impl(const igc_layer_norm_forward* d, hipStream_t stream) {
@@ -151,9 +146,11 @@ BackPlan plan_back(long long M, int N, int cus) {
   BackPlan b;
   b.in_registers = N <= 8192;
   if (b.in_registers) {
-    b.rows = N <= 1024 ? 8 : N <= 4096 ? 2 : 1;
+    int threads = 16;  // to a row
+    while (threads * 8 < N) threads *= 2;
+    b.rows = 1024 / threads;
     b.groups = 1;
-    b.blocks = (int)std::min(ceil_div(M, b.rows), 2LL * cus);
+    b.blocks = (int)std::min(ceil_div(M, b.rows), (long long)cus);
   } else {
     // enough workgroups to fill the card, and few enough that their sums stay small beside the rows
     b.groups = (int)ceil_div(N, 512);
@@ -167,12 +164,14 @@ template <int XT, int OT>
 int launch_back(const NormBackArgs& a, const BackPlan& pl, int cus, hipStream_t stream) {
   auto run = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.blocks), dim3(threads), 0, stream, a); };
   if (pl.in_registers) {
-    if (a.N <= 1024)
-      run(igc_rows::norm_back_rows_kernel<XT, OT, 64, 2, 512>, 512);
-    else if (a.N <= 4096)
-      run(igc_rows::norm_back_rows_kernel<XT, OT, 256, 2, 512>, 512);
-    else
-      run(igc_rows::norm_back_rows_kernel<XT, OT, 512, 2, 512>, 512);
+    using igc_rows::norm_back_rows_kernel;
+    if (a.N <= 128) run(norm_back_rows_kernel<XT, OT, 16, 1, 1024>, 1024);
+    else if (a.N <= 256) run(norm_back_rows_kernel<XT, OT, 32, 1, 1024>, 1024);
+    else if (a.N <= 512) run(norm_back_rows_kernel<XT, OT, 64, 1, 1024>, 1024);
+    else if (a.N <= 1024) run(norm_back_rows_kernel<XT, OT, 128, 1, 1024>, 1024);
+    else if (a.N <= 2048) run(norm_back_rows_kernel<XT, OT, 256, 1, 1024>, 1024);
+    else if (a.N <= 4096) run(norm_back_rows_kernel<XT, OT, 512, 1, 1024>, 1024);
+    else run(norm_back_rows_kernel<XT, OT, 1024, 1, 1024>, 1024);
     return launch_status();
   }
   if (a.dX) {
