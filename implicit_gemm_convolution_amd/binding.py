@@ -394,6 +394,7 @@ def conv2d_u8i8_zp(Nb, H, W, C, Kout, R, S, stride_h, stride_w, pad_h, pad_w, x,
 # ---------------------------------------------------------------------------
 _native = None   # the _marshal module; False without torch
 _entries = None  # (the library, addresses of its entry points)
+_bound = {}      # _marshal's calls of them
 
 
 def _marshal():
@@ -450,7 +451,10 @@ def _describe(name, fields, workspace, ws_bytes):
 def _call(name, check, stream, workspace, ws_bytes, *fields) -> int:
     native = _native if _native is not None else _marshal()
     if native:
-        st = native.call(_entry(name), _FORMATS[name], _stream(stream), workspace, ws_bytes, *fields)
+        f = _bound.get(name)
+        if f is None:
+            f = _bound[name] = native.bind(_entry(name), _FORMATS[name])
+        st = f(_stream(stream), workspace, ws_bytes, *fields)
     else:
         st = getattr(load(), name)(_describe(name, fields, workspace, ws_bytes), _stream(stream))
     return _check(st, name) if check else st

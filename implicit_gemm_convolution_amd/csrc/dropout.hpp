@@ -41,6 +41,7 @@ struct DropArgs {
   int drops;           // T > 0
   uint32_t last;       // T - 1: the largest word that drops its element
   float scale;
+  int stream;  // Y is written past the caches
   uint32_t seed0, seed1;
   uint64_t offset;
   const uint64_t* step;  // added to offset, or NULL
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs p) {
       for (int e = 0; e < 8; ++e) f[e] += a[e];
     }
     r.set(f);
-    r.store(p.Y + row * p.ldy * Raw<YT>::EB, c, p.N);
+    r.store(p.Y + row * p.ldy * Raw<YT>::EB, c, p.N, p.stream);
     row += p.step_row;
     chunk += p.step_chunk;
     if (chunk >= p.per) {

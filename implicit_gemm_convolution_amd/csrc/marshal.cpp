@@ -45,6 +45,14 @@ bool address(PyObject* o, void** out) {
 }
 
 bool integer(PyObject* o, int* out) {
+  if (PyLong_CheckExact(o)) {  // (the usual kind, without a reference of its own)
+    int over;
+    const long v = PyLong_AsLongAndOverflow(o, &over);
+    if (!over && v >= INT_MIN && v <= INT_MAX) {
+      *out = (int)v;
+      return true;
+    }
+  }
   PyObject* const n = PyNumber_Index(o);
   if (!n) return false;
   const long v = PyLong_AsLong(n);
@@ -103,51 +111,92 @@ int enter(void* entry, const void* descriptor, void* second) {
   return status;
 }
 
-// call(entry, format, stream, ws, ws_bytes, fields...) -> status.  The
-// descriptor is laid out as the C compiler does: "i" an int, "f" a float, "d" a
-// double, "l" a uint64_t, "p" an address; the workspace and its size come last
-// (past the end of descriptors that have none).
-PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
+// An entry point and the format of its descriptor, which is laid out as the C
+// compiler does: "i" an int, "f" a float, "d" a double, "l" a uint64_t, "p" an
+// address; the workspace and its size come last (past the end of descriptors
+// that have none).
+struct Bound {
+  void* entry;
+  size_t fields;
+  char format[64];
+};
+constexpr size_t DESCRIPTOR = 512;
+
+// What bind() returns: (stream, ws, ws_bytes, fields...) -> status.
+PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (n < 5) return PyErr_Format(PyExc_TypeError, "call takes at least 5 arguments, not %zd", n);
-    void *entry, *stream;
-    if (!address(args[0], &entry) || !address(args[2], &stream)) return nullptr;
-    Py_ssize_t fields;
-    const char* const format = PyUnicode_AsUTF8AndSize(args[1], &fields);
-    if (!format) return nullptr;
-    alignas(8) unsigned char d[512] = {};
-    if (!entry || fields != n - 5 || fields * 8 + 16 > (Py_ssize_t)sizeof(d))
-      return PyErr_Format(PyExc_TypeError, "%zd fields for the format %s", n - 5, format);
+    const Bound* const b = static_cast<const Bound*>(PyCapsule_GetPointer(self, nullptr));
+    if (!b) return nullptr;
+    if (n != (Py_ssize_t)b->fields + 3) return PyErr_Format(PyExc_TypeError, "%zd fields for the format %s", n - 3, b->format);
+    void* stream;
+    if (!address(args[0], &stream)) return nullptr;
+    alignas(8) unsigned char d[DESCRIPTOR] = {};
     size_t at = 0;
-    for (Py_ssize_t i = 0; i < fields; ++i) {
-      if (format[i] == 'i') {
+    for (size_t i = 0; i < b->fields; ++i) {
+      PyObject* const o = args[3 + i];
+      const char kind = b->format[i];
+      if (kind == 'i') {
         int v;
-        if (!integer(args[5 + i], &v)) return nullptr;
+        if (!integer(o, &v)) return nullptr;
         std::memcpy(d + at, &v, 4);
         at += 4;
-      } else if (format[i] == 'f') {
+      } else if (kind == 'f') {
         double v;
-        if (!real(args[5 + i], &v)) return nullptr;
+        if (!real(o, &v)) return nullptr;
         const float f = (float)v;
         std::memcpy(d + at, &f, 4);
         at += 4;
       } else {
+        at = (at + 7) & ~size_t(7);
         double v;
         uint64_t u;
         void* p;
-        if (format[i] == 'd' ? !real(args[5 + i], &v) : format[i] == 'l' ? !unsigned64(args[5 + i], &u) : !address(args[5 + i], &p)) return nullptr;
-        at = (at + 7) & ~size_t(7);
-        std::memcpy(d + at, format[i] == 'd' ? (void*)&v : format[i] == 'l' ? (void*)&u : (void*)&p, 8);
+        if (kind == 'd') {
+          if (!real(o, &v)) return nullptr;
+          std::memcpy(d + at, &v, 8);
+        } else if (kind == 'l') {
+          if (!unsigned64(o, &u)) return nullptr;
+          std::memcpy(d + at, &u, 8);
+        } else {
+          if (!address(o, &p)) return nullptr;
+          std::memcpy(d + at, &p, 8);
+        }
         at += 8;
       }
     }
     void* ws;
     size_t size;
-    if (!workspace(args[3], args[4], &ws, &size)) return nullptr;
+    if (!workspace(args[1], args[2], &ws, &size)) return nullptr;
     at = (at + 7) & ~size_t(7);
     std::memcpy(d + at, &ws, 8);
     std::memcpy(d + at + 8, &size, 8);
-    return PyLong_FromLong(enter(entry, d, stream));
+    return PyLong_FromLong(enter(b->entry, d, stream));
+  });
+}
+
+void release(PyObject* capsule) { delete static_cast<Bound*>(PyCapsule_GetPointer(capsule, nullptr)); }
+
+// bind(entry, format): the call of one entry point.
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    static PyMethodDef def = {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL, nullptr};
+    if (n != 2) return PyErr_Format(PyExc_TypeError, "bind takes 2 arguments, not %zd", n);
+    void* entry;
+    Py_ssize_t fields;
+    const char* const format = PyUnicode_AsUTF8AndSize(args[1], &fields);
+    if (!format || !address(args[0], &entry)) return nullptr;
+    if (!entry || fields >= (Py_ssize_t)sizeof(Bound::format) || fields * 8 + 16 > (Py_ssize_t)DESCRIPTOR)
+      return PyErr_Format(PyExc_TypeError, "no entry point, or too long a format: %s", format);
+    Bound* const b = new Bound{entry, (size_t)fields, {}};
+    std::memcpy(b->format, format, fields);
+    PyObject* const capsule = PyCapsule_New(b, nullptr, release);
+    if (!capsule) {
+      delete b;
+      return nullptr;
+    }
+    PyObject* const f = PyCFunction_New(&def, capsule);
+    Py_DECREF(capsule);
+    return f;
   });
 }
 
@@ -269,7 +318,7 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 PyMethodDef methods[] = {
-    {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL, nullptr},
+    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {"clip", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(clip)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -31,6 +31,10 @@ using igc_ffn::unpack8;
 // of n elements from column c, zeros past the row.  The chunk at a row's end is
 // loaded as the row's last eight elements and shifted (element by element, its
 // loads would wait for one another).
+// STREAM (chunks of whole, aligned rows alone): written past the caches.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 template <int T>
 struct Raw {
   static constexpr int EB = 2;
@@ -49,7 +53,26 @@ struct Raw {
   }
   __device__ __forceinline__ void get(float (&f)[8]) const { unpack8<T == T_BF16>(v, f); }
   __device__ __forceinline__ void set(const float (&f)[8]) { v = pack8<T == T_BF16>(f); }
-  __device__ __forceinline__ void store(uint8_t* row, int c, int n) const { store8(row + (long long)c * 2, v, n - c); }
+  __device__ __forceinline__ void clear_from(int n) {  // zeros from element n (1 to 7) on
+    unsigned __int128 w;
+    __builtin_memcpy(&w, &v, 16);
+    w = w << 16 * (8 - n) >> 16 * (8 - n);
+    __builtin_memcpy(&v, &w, 16);
+  }
+  // The bits of the largest |value|: they order as the values do, infinities
+  // and NaN on top.
+  __device__ __forceinline__ uint32_t top() const {
+    auto abs = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7fff7fffu); };
+    const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(abs(v.x), abs(v.y)), __builtin_elementwise_max(abs(v.z), abs(v.w)));
+    return max((uint32_t)m[0], (uint32_t)m[1]);
+  }
+  __device__ __forceinline__ void store(uint8_t* row, int c, int n, bool stream) const {
+    uint8_t* const p = row + (long long)c * 2;
+    if (stream)
+      __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
+    else
+      store8(p, v, n - c);
+  }
 };
 template <>
 struct Raw<T_F32> {
@@ -76,8 +99,16 @@ struct Raw<T_F32> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = f[e];
   }
-  __device__ __forceinline__ void store(uint8_t* row, int c, int n) const {
-    store_f32<8>(reinterpret_cast<float*>(row) + c, n - c, v);
+  __device__ __forceinline__ void store(uint8_t* row, int c, int n, bool stream) const {
+    float* const p = reinterpret_cast<float*>(row) + c;
+    if (stream) {
+      u32x4 w[2];
+      __builtin_memcpy(w, v, 32);
+      __builtin_nontemporal_store(w[0], reinterpret_cast<u32x4*>(p));
+      __builtin_nontemporal_store(w[1], reinterpret_cast<u32x4*>(p) + 1);
+    } else {
+      store_f32<8>(p, n - c, v);
+    }
   }
 };
 // Of a vector of n fp32 values.
@@ -90,7 +121,7 @@ __device__ __forceinline__ void load_vector(const float* p, int c, int n, float 
 // ---------------------------------------------------------------------------
 // Sums and maxima over the threads of a row.
 // ---------------------------------------------------------------------------
-// The lanes of a group of T (16, 32 or 64) combined in every one of them:
+// The lanes of a group of T (2 to 64) combined in every one of them:
 // within rows of 16 lanes by cross-lane operands of the vector unit, the four
 // rows of a wave through scalar registers (the way through LDS, a shuffle a step,
 // takes twelve trips of over 60 cycles each).  The order is fixed, and the same
@@ -101,11 +132,11 @@ __device__ __forceinline__ V wave_combine(V v, F&& f) {
   auto other = [](V x, auto ctrl) {
     return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
   };
-  v = f(v, other(v, std::integral_constant<int, 0xB1>()));   // quad_perm [1, 0, 3, 2]
-  v = f(v, other(v, std::integral_constant<int, 0x4E>()));   // quad_perm [2, 3, 0, 1]
-  v = f(v, other(v, std::integral_constant<int, 0x141>()));  // the other half of 8
-  v = f(v, other(v, std::integral_constant<int, 0x140>()));  // the other half of 16
-  if constexpr (T == 16) return v;
+  v = f(v, other(v, std::integral_constant<int, 0xB1>()));                          // quad_perm [1, 0, 3, 2]
+  if constexpr (T >= 4) v = f(v, other(v, std::integral_constant<int, 0x4E>()));    // quad_perm [2, 3, 0, 1]
+  if constexpr (T >= 8) v = f(v, other(v, std::integral_constant<int, 0x141>()));   // the other half of 8
+  if constexpr (T >= 16) v = f(v, other(v, std::integral_constant<int, 0x140>()));  // the other half of 16
+  if constexpr (T <= 16) return v;
   auto lane = [&](int l) { return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
   const V low = f(lane(0), lane(16)), high = f(lane(32), lane(48));
   if constexpr (T == 32) return (threadIdx.x & 32) ? high : low;
@@ -113,8 +144,8 @@ __device__ __forceinline__ V wave_combine(V v, F&& f) {
 }
 
 // N values of every thread of a row's T threads, combined in every one of
-// them: the lanes of a wave, then the waves through LDS, with one barrier (of
-// the whole workgroup).  slot: W entries of the row.  Calls take slots in turn,
+// them: the lanes of a wave, then the waves through LDS, a lane for each, with
+// one barrier (of the whole workgroup).  slot: W entries of the row.  Calls take slots in turn,
 // two at least: who writes a slot again has passed the barrier of the other
 // one, which everyone reaches after reading this one.
 template <int T, int N, class V, class F>
@@ -129,11 +160,7 @@ __device__ __forceinline__ void row_combine(V (&v)[N], V (*slot)[N], F&& f) {
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = slot[0][i];
-#pragma unroll
-      for (int w = 1; w < T / 64; ++w) v[i] = f(v[i], slot[w][i]);
-    }
+    for (int i = 0; i < N; ++i) v[i] = wave_combine<T / 64>(slot[t % (T / 64)][i], f);
   }
 }
 template <int T>
@@ -158,32 +185,41 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*slot)[1]) {
 // reciprocal and the product are off by 2^-23 together, and rounding to 20
 // significant bits moves the result by 2^-20 at most: it takes quotients that
 // are ties back to them (a tie has 8 significant bits) and the others across
-// none.  Seven operations an element, where a division takes about as many
-// again.  `by` is 127 times a power of two and `inv` the reciprocal of m times
+// none.  Adding 1.5 2^23 then rounds to a whole number, ties to even, and leaves
+// it in the lowest byte.  Five operations an element, and three for four to pack
+// them.  `by` is 127 times a power of two and `inv` the reciprocal of m times
 // the same power, which keeps both products of any m within fp32.
 struct Quantizer {
   float by, inv, scale;
-  // m: the bits of the largest |x|, which order as the values do, infinities and NaN on top.
-  // Rows that hold one of those get NaN as their scale and zeros, which carries the NaN into what is made of them.
-  __device__ __forceinline__ explicit Quantizer(uint32_t m) {
-    const float top = __builtin_bit_cast(float, m);
-    const bool finite = m < 0x7f800000u, some = m != 0;
+  // m: the bits of the largest |x| of a row of type T.  Rows with an infinity or NaN
+  // get NaN as their scale and zeros, which carries the NaN into what is made of them.
+  template <int T>
+  __device__ __forceinline__ static Quantizer of(uint32_t m) {
+    const float top = T == T_BF16 ? __builtin_bit_cast(float, m << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+    const bool finite = m < (T == T_BF16 ? 0x7f80u : 0x7c00u), some = m != 0;
     const float k = top >= 0x1p100f ? 0x1p-64f : top < 0x1p-64f ? 0x1p64f : 1.0f;
-    by = finite && some ? 127.0f * k : 0.0f;
-    inv = finite && some ? 1.0f / (top * k) : 0.0f;
-    scale = finite ? top / 127.0f : __builtin_nanf("");
+    Quantizer q;
+    q.by = 127.0f * k;
+    q.inv = finite && some ? 1.0f / (top * k) : 0.0f;
+    q.scale = finite ? top / 127.0f : __builtin_nanf("");
+    return q;
   }
-  __device__ __forceinline__ int operator()(float x) const {
+  __device__ __forceinline__ uint32_t operator()(float x) const {  // in the lowest byte
     const float t = (x * by) * inv;
     const uint32_t u = (__builtin_bit_cast(uint32_t, t) + 8u) & ~15u;
-    return (int)__builtin_rintf(__builtin_bit_cast(float, u));
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u) + 12582912.0f);
   }
-  __device__ __forceinline__ void store(int8_t* p, int valid, const float (&f)[8]) const {
-    uint32_t w[2] = {0, 0};
+  __device__ __forceinline__ void store(int8_t* p, int valid, const float (&f)[8], bool stream) const {
+    uint32_t w[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e / 4] |= ((uint32_t)(*this)(f[e]) & 255u) << (8 * (e & 3));
-    if (inv == 0.0f) w[0] = w[1] = 0;  // (infinities and NaN times zero)
-    if (valid >= 8) {
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a = __builtin_amdgcn_perm((*this)(f[i * 4 + 1]), (*this)(f[i * 4]), 0x0c0c0400u);
+      const uint32_t b = __builtin_amdgcn_perm((*this)(f[i * 4 + 3]), (*this)(f[i * 4 + 2]), 0x0c0c0400u);
+      w[i] = inv == 0.0f ? 0u : a | b << 16;  // (infinities and NaN times zero)
+    }
+    if (stream) {
+      __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p));
+    } else if (valid >= 8) {
       __builtin_memcpy(p, w, 8);
     } else {
 #pragma unroll
@@ -192,13 +228,6 @@ struct Quantizer {
     }
   }
 };
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
-__device__ __forceinline__ uint32_t max_bits(uint32_t m, const float (&f)[8], int valid) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < valid) m = max(m, abs_bits(f[e]));
-  return m;
-}
 
 // ---------------------------------------------------------------------------
 // Forward: the norm, and rows in 8 bits.
@@ -216,7 +245,57 @@ struct RowArgs {
   int8_t* Q;
   long long ldq;
   float* scale;  // or NULL: no rows in 8 bits
+  int stream_y, stream_q;  // written past the caches
 };
+
+// Mean and variance of a row in its threads' registers, with one barrier: every
+// wave takes the mean of its own elements and their squared distances from it,
+// and the waves' parts join as M2 = sum of M2_w + n_w (mean_w - mean)^2: no
+// difference of large squares anywhere.  (A barrier for the mean and one for the
+// distances from it: 8192 x 4096 bf16 TODO us.)
+template <int T, int C>
+__device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, float inv_n, float2* parts, float& mean, float& var) {
+  constexpr int WT = T < 64 ? T : 64;
+  auto add = [](float a, float b) { return a + b; };
+  auto of_wave = [&](int w) {  // elements that wave w holds
+    int k = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) k += min(max(n - (j * T + w * 64) * 8, 0), WT * 8);
+    return (float)k;
+  };
+  constexpr int W = T / 64;
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += v[j][e];  // (zeros past the row)
+  s = wave_combine<WT>(s, add);
+  const float m = T <= 64 ? s * inv_n : s / fmaxf(of_wave(t >> 6), 1.0f);
+  float d2 = 0.0f;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int c = (j * T + t) * 8;
+    const float mc = c < n ? m : 0.0f;  // (chunks past the row are zeros, and their distances)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float d = v[j][e] - mc;
+      if ((n & 7) && c + e >= n) d = 0.0f;
+      d2 = __builtin_fmaf(d, d, d2);
+    }
+  }
+  d2 = wave_combine<WT>(d2, add);
+  if constexpr (T <= 64) {
+    mean = m;
+    var = d2 * inv_n;
+  } else {
+    if ((t & 63) == 0) parts[t >> 6] = make_float2(m, d2);
+    __syncthreads();
+    const float2 w = parts[t % W];  // (a lane for each wave's part)
+    const float k = of_wave(t % W);
+    mean = wave_combine<W>(w.x * k, add) * inv_n;
+    var = wave_combine<W>(__builtin_fmaf((w.x - mean) * (w.x - mean), k, w.y), add) * inv_n;
+  }
+}
 
 // A row by T threads, in registers: C chunks of 8 elements a thread, 256 / T
 // rows of a workgroup at a time where T is less.  NORM: the norm of the rows (Y,
@@ -226,10 +305,10 @@ struct RowArgs {
 template <int T>
 constexpr int row_threads = T < 256 ? 256 : T;
 template <bool NORM, int XT, int OT, int T, int C>
-__global__ void __launch_bounds__(row_threads<T>) row_kernel(const RowArgs p) {
+__global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : XT == T_F32 && T < 1024 ? 7 : 8) row_kernel(const RowArgs p) {
   constexpr int RG = row_threads<T> / T;  // rows of a workgroup
   constexpr int W = T < 64 ? 1 : T / 64;
-  __shared__ float sums[2][RG][W][1];
+  __shared__ float2 parts[2][RG][W];
   __shared__ uint32_t tops[2][RG][W][1];
   const int t = threadIdx.x % T, rg = threadIdx.x / T;
   auto col = [&](int j) { return (j * T + t) * 8; };
@@ -258,53 +337,50 @@ __global__ void __launch_bounds__(row_threads<T>) row_kernel(const RowArgs p) {
   for (int turn = 0; first < p.M; first += step, turn ^= 1) {  // (as often for every row of the workgroup: the barriers)
     const long long row = first + rg;
     const bool in = row < p.M;
-    float v[C][8];
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (in && col(j) < p.N) {
-        next[j].get(v[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
-      }
-    if (row + step < p.M) load(row + step);
+    Raw<OT> out[C];
     if constexpr (NORM) {
-      float s = 0.0f;
+      float v[C][8];
 #pragma unroll
       for (int j = 0; j < C; ++j)
+        if (in && col(j) < p.N) {
+          next[j].get(v[j]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[j][e];  // (zeros past the row)
-      const float mean = row_sum<T>(s, sums[0][rg]) * p.inv_n;
-      s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[j][e] -= mean;
-          if (col(j) + e < p.N) s = __builtin_fmaf(v[j][e], v[j][e], s);
+          for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
         }
-      const float rstd = 1.0f / __builtin_sqrtf(row_sum<T>(s, sums[1][rg]) * p.inv_n + p.eps);
+      if (row + step < p.M) load(row + step);
+      float mean, var;
+      row_stats<T, C>(v, t, p.N, p.inv_n, parts[turn][rg], mean, var);
+      const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
       if (in && t == 0 && p.mean) p.mean[row] = mean;
       if (in && t == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = __builtin_fmaf(v[j][e] * rstd, gamma[j][e], beta[j][e]);
-        Raw<OT> out;
-        out.set(v[j]);
-        if (p.Y && in && col(j) < p.N) out.store(p.Y + row * p.ldy * Raw<OT>::EB, col(j), p.N);
-        out.get(v[j]);
+        for (int e = 0; e < 8; ++e) v[j][e] = __builtin_fmaf((v[j][e] - mean) * rstd, gamma[j][e], beta[j][e]);
+        out[j].set(v[j]);
+        if (p.Y && in && col(j) < p.N) out[j].store(p.Y + row * p.ldy * Raw<OT>::EB, col(j), p.N, p.stream_y);
+        if ((p.N & 7) && col(j) < p.N && p.N - col(j) < 8) out[j].clear_from(p.N - col(j));
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < C; ++j) out[j] = next[j];
+      if (row + step < p.M) load(row + step);
     }
     if (p.scale) {
       uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < C; ++j) top = max_bits(top, v[j], p.N - col(j));
-      const Quantizer q(row_max<T>(top, tops[turn][rg]));
+      for (int j = 0; j < C; ++j)
+        if (in && col(j) < p.N) top = max(top, out[j].top());
+      const Quantizer q = Quantizer::of<OT>(row_max<T>(top, tops[turn][rg]));
       if (in && t == 0) p.scale[row] = q.scale;
 #pragma unroll
       for (int j = 0; j < C; ++j)
-        if (in && col(j) < p.N) q.store(p.Q + row * p.ldq + col(j), p.N - col(j), v[j]);
+        if (in && col(j) < p.N) {
+          float v[8];
+          out[j].get(v);
+          q.store(p.Q + row * p.ldq + col(j), p.N - col(j), v, p.stream_q);
+        }
     }
   }
 }
@@ -368,17 +444,18 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
     uint32_t top = 0;
     if (!NORM || p.Y || p.scale) {
       chunks([&](float(&v)[8], int c, int n) {
-        const Raw<OT> out = normed(v, c, n);
-        if (p.Y) out.store(p.Y + row * p.ldy * Raw<OT>::EB, c, p.N);
-        if (p.scale) top = max_bits(top, v, n);
+        Raw<OT> out = normed(v, c, n);
+        if (p.Y) out.store(p.Y + row * p.ldy * Raw<OT>::EB, c, p.N, p.stream_y);
+        if (n < 8) out.clear_from(n);
+        top = max(top, out.top());
       });
     }
     if (p.scale) {
-      const Quantizer q(row_max<T>(top, tops[turn]));
+      const Quantizer q = Quantizer::of<OT>(row_max<T>(top, tops[turn]));
       if (threadIdx.x == 0) p.scale[row] = q.scale;
       chunks([&](float(&v)[8], int c, int n) {
         normed(v, c, n);
-        q.store(p.Q + row * p.ldq + c, n, v);
+        q.store(p.Q + row * p.ldq + c, n, v, p.stream_q);
       });
     }
   }
@@ -400,6 +477,7 @@ struct NormBackArgs {
   float* sums;    // or NULL: dgamma and dbeta of each row block, [blocks][2][width]
   int width;      // N rounded up to a multiple of 64
   int rows, groups, blocks;  // rows of a block; workgroups across the columns and down the rows
+  int stream;                // dX is written past the caches
 };
 
 // Rows in registers: T threads a row, C chunks of 8 elements a thread, WG / T
@@ -481,7 +559,7 @@ __global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p
         }
         Raw<XT> out;
         out.set(v[j]);
-        out.store(p.dX + row * p.lddx * Raw<XT>::EB, col(j), p.N);
+        out.store(p.dX + row * p.lddx * Raw<XT>::EB, col(j), p.N, p.stream);
       }
   }
   if (!p.sums) return;
@@ -585,7 +663,7 @@ __global__ void __launch_bounds__(256) norm_back_kernel(const NormBackArgs p) {
           if (p.R) v[e] += a[e];
         }
         x.set(v);
-        x.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N);
+        x.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N, p.stream);
       }
     }
   }
