@@ -32,8 +32,8 @@ inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // products: half as many output columns).
 // P_TILE_*: aligned operands, straight into LDS (P_TILE_32: 64 x 32); P_ANY_*: any operand,
 // through registers; P_SKINNY_*: few rows, any operand, 16 or 32 weight rows
-// per workgroup.
-enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_TILE_32, P_ANY_128, P_ANY_64, P_SKINNY_16, P_SKINNY_32 };
+// per workgroup; P_BYTES: 8 bits, any operand, through registers.
+enum Variant { P_TILE_256, P_TILE_128, P_TILE_64, P_TILE_32, P_ANY_128, P_ANY_64, P_SKINNY_16, P_SKINNY_32, P_BYTES };
 
 struct Plan {
   int variant = P_ANY_64;

@@ -868,6 +868,183 @@ __global__ void __launch_bounds__(256, 2) gemm_any_kernel(const GemmArgs p) {
   write_out<BF, MODE, FM, FN, sizeof(smem) / 4>(p, acc, smem + wave * (sizeof(smem) / 4), m0 + wm * TM, n0 + wn * (ON / 2));
 }
 
+// An operand's K tiles of 128 bytes from rows of any alignment, through
+// registers: eight lanes take a row, each the four aligned words that its chunk of
+// 16 bytes begins in.  The word in which a chunk ends is the next lane's first,
+// or the first of the row's next tile, so nothing is loaded for it (a load of
+// that word a chunk cost as much as the chunk's own: 0.42 us a K tile).  Rows
+// past the end repeat the last one (their sums are not stored).
+template <int W, bool TWO>
+struct ByteOperand {
+  static constexpr int NC = W * 8 / 256;  // chunks of a thread
+  const uint8_t* base[NC];  // the aligned word that the chunk of the next tile begins in
+  uint32_t bits[NC];        // where it begins there
+  uint32_t end[NC];         // the word after the last whole tile
+  __device__ __forceinline__ const uint8_t* row(int j, const uint8_t* p, long long ld, const uint8_t* p2, long long ld2, int o0, int extent) const {
+    int o = (int)(threadIdx.x + 256 * j) >> 3;
+    const bool second = TWO && o >= W / 2;
+    if (second) o -= W / 2;
+    o = min(o0 + o, extent - 1);
+    return (second ? p2 : p) + (long long)o * (second ? ld2 : ld);
+  }
+  __device__ __forceinline__ void init(const uint8_t* p, long long ld, const uint8_t* p2, long long ld2, int o0, int extent, int nk) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const uint8_t* const q = row(j, p, ld, p2, ld2, o0, extent);
+      const uint32_t odd = (uint32_t)(uintptr_t)q & 3;
+      base[j] = q - odd + (threadIdx.x & 7) * 16;
+      bits[j] = odd * 8;
+      if (nk) __builtin_memcpy(&end[j], __builtin_assume_aligned(q - odd + (long long)nk * 128 - (odd ? 0 : 4), 4), 4);
+    }
+  }
+  // `step`: how far the tile after this one is
+  __device__ __forceinline__ void load(uint4 (&q)[NC], int step) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      __builtin_memcpy(&q[j], __builtin_assume_aligned(base[j], 4), 16);
+      base[j] += step;
+    }
+  }
+  // A tile into LDS, given the next one (or, where there is none, `end`).
+  __device__ __forceinline__ void store(uint8_t* st, const uint4 (&q)[NC], const uint4 (&after)[NC], bool some, uint32_t mask) const {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int idx = threadIdx.x + 256 * j;
+      const uint4& v = q[j];
+      const uint32_t lane = __builtin_amdgcn_mov_dpp(v.x, 0x101, 0xf, 0xf, true);                            // of the next lane
+      const uint32_t tile = __builtin_amdgcn_mov_dpp(some ? after[j].x : end[j], 0x117, 0xf, 0xf, true);     // of the lane 7 before
+      const uint32_t last = (threadIdx.x & 7) == 7 ? tile : lane;
+      lds_write16(st, swz(idx >> 3, idx & 7),
+                  make_uint4(__builtin_amdgcn_alignbit(v.y, v.x, bits[j]) & mask, __builtin_amdgcn_alignbit(v.z, v.y, bits[j]) & mask,
+                             __builtin_amdgcn_alignbit(v.w, v.z, bits[j]) & mask, __builtin_amdgcn_alignbit(last, v.w, bits[j]) & mask));
+    }
+  }
+  // The bytes past the last whole tile, from `from` to the rows' end at `end`, zeros after them.
+  __device__ __forceinline__ void tail(uint4 (&q)[NC], const uint8_t* p, long long ld, const uint8_t* p2, long long ld2, int o0, int extent,
+                                       int from, int end) const {
+    const int k = from + (threadIdx.x & 7) * 16, over = k + 16 - end;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const uint8_t* const r = row(j, p, ld, p2, ld2, o0, extent);
+      if (over <= 0) {
+        q[j] = load16_words(r + k);
+      } else if (over >= 16) {
+        q[j] = make_uint4(0, 0, 0, 0);
+      } else if (end >= 16) {  // (the row's last 16 bytes, shifted)
+        const uint4 w = load16_words(r + end - 16);
+        unsigned __int128 x;
+        __builtin_memcpy(&x, &w, 16);
+        x >>= 8 * over;
+        __builtin_memcpy(&q[j], &x, 16);
+      } else {
+        q[j] = load16_tail(r + k, 16 - over);
+      }
+    }
+  }
+  __device__ __forceinline__ void store_tail(uint8_t* st, const uint4 (&q)[NC]) const {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int idx = threadIdx.x + 256 * j;
+      lds_write16(st, swz(idx >> 3, idx & 7), q[j]);
+    }
+  }
+};
+
+// The 8-bit product on rows of any alignment and length, without a copy of them
+// first: 64 x 64 sums (the gated block: of each product) a workgroup, K tiles
+// through registers, DEPTH of them on their way, into two LDS stages.  What is
+// left of the reduction past the last whole tile comes first, so the loop has
+// whole tiles alone; it turns a multiple of DEPTH times without a branch, which
+// keeps the compiler's waits at the oldest loads, and the turns past the last
+// tile multiply by zeros.
+template <bool BF, int MODE, int DEPTH>
+__global__ void __launch_bounds__(256) i8_any_kernel(const I8Args p) {
+  constexpr bool GLU = is_glu(MODE);
+  constexpr int BM = 64, BN = GLU ? 128 : 64, TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
+  typedef LdsTile<BM, false> TA;
+  typedef LdsTile<BN, false> TB;
+  typedef ByteOperand<BM, false> LoadA;
+  typedef ByteOperand<BN, GLU> LoadB;
+  constexpr int STAGE = TA::BYTES + TB::BYTES;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
+  const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
+  int tm, tn;
+  tile_of(p, blockIdx.x, tm, tn);
+  constexpr int ON = GLU ? BN / 2 : BN;  // output columns of a tile
+  const int m0 = tm * BM, n0 = tn * ON;
+  const int nk = p.R / 128, rest = p.R - nk * 128;
+  igc::i32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = igc::i32x4{0, 0, 0, 0};
+  auto blk_b = [&](int j) {
+    if constexpr (GLU) return j < FN / 2 ? wn * (TN / 2) + j * 16 : BN / 2 + wn * (TN / 2) + (j - FN / 2) * 16;
+    return wn * TN + j * 16;
+  };
+  auto multiply = [&](const uint8_t* st) {
+    uint4 fa[2][FM], fb[2][FN];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[ks][i] = TA::frag(st, wm * TM + i * 16, ks);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[ks][j] = TB::frag(st + TA::BYTES, blk_b(j), ks);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) mfma16<BF>(acc[i][j], fb[ks][j], fa[ks][i]);
+  };
+  LoadA la;
+  LoadB lb;
+  la.init(p.A, p.lda, nullptr, 0, m0, p.M, nk);
+  lb.init(p.B, p.ldb, p.B2, p.ldb2, n0, p.N, nk);
+  uint4 ta[LoadA::NC], tb[LoadB::NC];
+  if (rest) {
+    la.tail(ta, p.A, p.lda, nullptr, 0, m0, p.M, nk * 128, p.R);
+    lb.tail(tb, p.B, p.ldb, p.B2, p.ldb2, n0, p.N, nk * 128, p.R);
+  }
+  uint4 qa[DEPTH][LoadA::NC], qb[DEPTH][LoadB::NC];
+  if (nk) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {  // (tiles past the last one are the last one again)
+      la.load(qa[d], d + 1 < nk ? 128 : 0);
+      lb.load(qb[d], d + 1 < nk ? 128 : 0);
+    }
+  }
+  if (rest) {
+    la.store_tail(smem + STAGE, ta);
+    lb.store_tail(smem + STAGE + TA::BYTES, tb);
+    __syncthreads();
+    multiply(smem + STAGE);
+  }
+  if (nk) {
+    la.store(smem, qa[0], qa[1], nk > 1, ~0u);
+    lb.store(smem + TA::BYTES, qb[0], qb[1], nk > 1, ~0u);
+    __syncthreads();
+    static_assert(DEPTH % 2 == 0 && DEPTH > 2, "stages, and a tile after the next");
+    for (int k0 = 0; k0 < nk; k0 += DEPTH) {
+      static_for<DEPTH>([&](auto U) {
+        constexpr int u = decltype(U)::value, next = (u + 1) % DEPTH, after = (u + 2) % DEPTH;
+        const int kt = k0 + u;
+        const int step = kt + DEPTH + 1 < nk ? 128 : 0;
+        la.load(qa[u], step);
+        lb.load(qb[u], step);
+        multiply(smem + (u & 1) * STAGE);
+        uint8_t* const to = smem + (next & 1) * STAGE;
+        la.store(to, qa[next], qa[after], kt + 2 < nk, kt + 1 < nk ? ~0u : 0u);
+        lb.store(to + TA::BYTES, qb[next], qb[after], kt + 2 < nk, ~0u);
+        __syncthreads();
+      });
+    }
+  }
+  __syncthreads();
+  write_out<BF, MODE, FM, FN, 2 * STAGE / 4>(p, acc, smem + wave * (2 * STAGE / 4), m0 + wm * TM, n0 + wn * (ON / 2));
+}
+
 // The forward products of few rows (M <= 16 MB): bound by streaming the
 // weights once.  A workgroup takes NB blocks of 16 weight rows (the gated
 // block: half of them from each weight) and its waves split the reduction;

@@ -58,6 +58,20 @@ struct Pads {
   float us() const { return 4.0f + (float)moved / 5.7e6f; }
 };
 
+// The plan of the kernel that takes rows of any alignment as they lie: a chain
+// of K tiles of 128, or so much for each of its workgroups where they fill the
+// card, and their outputs.  us, as they lie | copied first or few rows streamed:
+// 131 x 5003 x 2049 11.0 | 18.0, 64 x 5003 x 2049 10.7 | 13.2, 300 x 16001 x 2049
+// 33.9 | 35.6, 1000 x 16001 x 2049 94.7 | 52.9, 8 x 1001 x 2049 9.8 | 6.2; the gated block
+// 131 x 5003 x 2049 16.4 | 21.6, 600 x 5003 x 2049 55.6 | 32.8.
+Plan bytes_plan(bool glu, long long M, long long N, long long K, int cus) {
+  Plan pl = tile_plan(glu ? igc_ffn::M_GLU : igc_ffn::M_FWD, P_TILE_64, M, N);
+  pl.variant = P_BYTES;
+  const float count = (float)pl.tiles_m * (float)pl.tiles_n * 256.0f / (float)cus, tiles = (float)ceil_div(K, 128);
+  pl.us = glu ? 6.0f + tiles * std::max(0.52f, 2.7e-3f * count) + 0.014f * count : 4.5f + tiles * std::max(0.35f, 1.3e-3f * count) + 0.005f * count;
+  return pl;
+}
+
 template <int MODE>
 int product_i8(I8Args& a, int type, void* ws, size_t ws_bytes, size_t* query, hipStream_t stream) {
   if (a.M == 0 || a.N == 0) {
@@ -78,27 +92,25 @@ int product_i8(I8Args& a, int type, void* ws, size_t ws_bytes, size_t* query, hi
   if (align == 16) {
     pl = make_plan(AS, a.M, a.N, units, 16, cus, true);
   } else {
-    // Rows of another alignment or length: few of them stream from where they
-    // lie; otherwise they are copied into rows of whole chunks first.
+    // Rows of another alignment or length: taken from where they lie, or copied
+    // into rows of whole chunks first.
     if (a_al != 16) ia = pads.add(a.A, a.lda, a.M, a.R);
     if (b_al != 16) ib = pads.add(a.B, a.ldb, a.N, a.R);
     if (b2_al != 16) ib2 = pads.add(a.B2, a.ldb2, a.N, a.R);
     pl = make_plan(AS, a.M, a.N, whole / 2, 16, cus, true);
-    bool copy = pads.possible;
+    pl.us = pads.possible ? pl.us + pads.us() : 1e30f;
+    bool copy = true;
+    auto take = [&](const Plan& q) {
+      if (q.us >= pl.us) return;
+      pl = q;
+      copy = false;
+    };
     if (a.M <= 64) {
       const int skinny_align = align < 4 ? 2 : 4;
-      Plan few = skinny_plan(AS, P_SKINNY_32, a.M, a.N, units, skinny_align, cus);
-      if (!GLU) {
-        const Plan q = skinny_plan(AS, P_SKINNY_16, a.M, a.N, units, skinny_align, cus);
-        if (q.us < few.us) few = q;
-      }
-      if (!copy || few.us <= pads.us() + pl.us) {
-        pl = few;
-        copy = false;
-      }
-    } else if (!copy) {
-      return fail(IGC_EUNSUPPORTED, "rows that are not 16-byte aligned or no multiple of 16 long: too many of them to copy");
+      take(skinny_plan(AS, P_SKINNY_32, a.M, a.N, units, skinny_align, cus));
+      if (!GLU) take(skinny_plan(AS, P_SKINNY_16, a.M, a.N, units, skinny_align, cus));
     }
+    take(bytes_plan(GLU, a.M, a.N, a.R, cus));
     if (!copy) {
       pads = Pads();
       ia = ib = ib2 = -1;

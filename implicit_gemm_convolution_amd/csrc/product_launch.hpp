@@ -82,7 +82,12 @@ int launch_product(const igc_ffn::GemmArgs& args, const Plan& pl, hipStream_t st
       return launch_status();
     default: break;
   }
-  if constexpr (!igc_ffn::is_i8(MODE)) {
+  if constexpr (igc_ffn::is_i8(MODE)) {
+    if (pl.variant == P_BYTES) {
+      hipLaunchKernelGGL((igc_ffn::i8_any_kernel<BF, MODE, 4>), g, dim3(256), 0, stream, a);
+      return launch_status();
+    }
+  } else {
     if (pl.variant == P_ANY_128) {
       launch_any<BF, MODE, 128, 128>(a, pl, g, stream);
       return launch_status();
