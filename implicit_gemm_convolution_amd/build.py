@@ -156,6 +156,11 @@ def i8_assembly(out_dir: str, extra_flags=()) -> str:
     return _assembly(out_dir, "i8-kernels-gfx950.s", I8_LAUNCH_SOURCE, "IGC_I8_UNIT", I8_LAUNCH_UNITS, extra_flags)
 
 
+def rows_assembly(out_dir: str, extra_flags=()) -> str:
+    """The same for the row operators."""
+    return _assembly(out_dir, "rows-kernels-gfx950.s", ROWS_SOURCE, "IGC_ROWS_UNIT", 1, extra_flags)
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
     sys.exit(0)

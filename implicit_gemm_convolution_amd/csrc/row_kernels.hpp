@@ -251,8 +251,8 @@ struct RowArgs {
 // Mean and variance of a row in its threads' registers, with one barrier: every
 // wave takes the mean of its own elements and their squared distances from it,
 // and the waves' parts join as M2 = sum of M2_w + n_w (mean_w - mean)^2: no
-// difference of large squares anywhere.  (A barrier for the mean and one for the
-// distances from it: 8192 x 4096 bf16 TODO us.)
+// difference of large squares anywhere.  (With a barrier for the mean and one for
+// the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
 template <int T, int C>
 __device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, float inv_n, float2* parts, float& mean, float& var) {
   constexpr int WT = T < 64 ? T : 64;
@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
     const uint8_t* const x = p.X + row * p.ldx * Raw<XT>::EB;
     // f(chunk of 8, its first column, how many of its columns are in the row)
     auto chunks = [&](auto&& f) {
-      for (int c = threadIdx.x * 8; c < p.N; c += T * 8) {
+      for (uint32_t u = threadIdx.x * 8; u < (uint32_t)p.N; u += T * 8) {  // (steps past 2^31 at most once)
+        const int c = (int)u;
         float v[8];
         Raw<XT> raw;
         raw.load(x, c, p.N);
@@ -598,8 +599,8 @@ __global__ void __launch_bounds__(T) norm_back_stats_kernel(const NormBackArgs p
   for (long long row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
     const float mean = p.mean[row], rstd = p.rstd[row];
     float m[2] = {0.0f, 0.0f};
-    for (int c = t * 8; c < p.N; c += T * 8) {
-      const int n = min(p.N - c, 8);
+    for (uint32_t u = t * 8; u < (uint32_t)p.N; u += T * 8) {
+      const int c = (int)u, n = min(p.N - c, 8);
       Raw<OT> dy;
       Raw<XT> x;
       dy.load(p.dY + row * p.lddy * Raw<OT>::EB, c, p.N);

@@ -47,23 +47,25 @@ void check_rows(Checker& c, int M, int N, int type) {
 
 // ---------------------------------------------------------------- rows
 // Threads to a row: as many as it has chunks, up to 1024 with two chunks each
-// (8192 x 4096 bf16: TODO).  Longer rows are read again in every pass.
+// (more rows at once in a compute unit's registers than with more chunks a
+// thread: 8192 x 4096 bf16 32.6 us with 512 threads, 36.0 with 256 and two chunks;
+// 8192 x 1024 10.4, and 14.6 by a wave with two).  Longer rows are read again in
+// every pass (2000 x 20000 54 us: 2.9 TB/s).
 template <bool NORM, int XT, int OT>
 void launch_rows(const RowArgs& a, int cus, hipStream_t stream) {
-  auto run = [&](auto kernel, int threads, int rows) {
-    const long long groups = std::min(ceil_div(a.M, rows), 2048LL / threads * cus);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), 0, stream, a);
-  };
-  using igc_rows::row_kernel;
-  if (a.N <= 128) run(row_kernel<NORM, XT, OT, 16, 1>, 256, 16);
-  else if (a.N <= 256) run(row_kernel<NORM, XT, OT, 32, 1>, 256, 8);
-  else if (a.N <= 512) run(row_kernel<NORM, XT, OT, 64, 1>, 256, 4);
-  else if (a.N <= 1024) run(row_kernel<NORM, XT, OT, 128, 1>, 256, 2);
-  else if (a.N <= 2048) run(row_kernel<NORM, XT, OT, 256, 1>, 256, 1);
-  else if (a.N <= 4096) run(row_kernel<NORM, XT, OT, 512, 1>, 512, 1);
-  else if (a.N <= 8192) run(row_kernel<NORM, XT, OT, 1024, 1>, 1024, 1);
-  else if (a.N <= 16384) run(row_kernel<NORM, XT, OT, 1024, 2>, 1024, 1);
-  else run(igc_rows::long_row_kernel<NORM, XT, OT, 1024>, 1024, 1);
+  auto groups = [&](int threads, int rows) { return dim3((unsigned)std::min(ceil_div(a.M, rows), 2048LL / threads * cus)); };
+#define IGC_ROWS(threads, rows, ...) \
+  hipLaunchKernelGGL((igc_rows::__VA_ARGS__), groups(threads, rows), dim3(threads), 0, stream, a)
+  if (a.N <= 128) IGC_ROWS(256, 16, row_kernel<NORM, XT, OT, 16, 1>);
+  else if (a.N <= 256) IGC_ROWS(256, 8, row_kernel<NORM, XT, OT, 32, 1>);
+  else if (a.N <= 512) IGC_ROWS(256, 4, row_kernel<NORM, XT, OT, 64, 1>);
+  else if (a.N <= 1024) IGC_ROWS(256, 2, row_kernel<NORM, XT, OT, 128, 1>);
+  else if (a.N <= 2048) IGC_ROWS(256, 1, row_kernel<NORM, XT, OT, 256, 1>);
+  else if (a.N <= 4096) IGC_ROWS(512, 1, row_kernel<NORM, XT, OT, 512, 1>);
+  else if (a.N <= 8192) IGC_ROWS(1024, 1, row_kernel<NORM, XT, OT, 1024, 1>);
+  else if (a.N <= 16384) IGC_ROWS(1024, 1, row_kernel<NORM, XT, OT, 1024, 2>);
+  else IGC_ROWS(1024, 1, long_row_kernel<NORM, XT, OT, 1024>);
+#undef IGC_ROWS
 }
 
 int layer_norm_forward_impl(const igc_layer_norm_forward* d, hipStream_t stream) {
@@ -174,16 +176,17 @@ BackPlan plan_back(long long M, int N, int cus) {
 
 template <int XT, int OT>
 int launch_back(const NormBackArgs& a, const BackPlan& pl, int cus, hipStream_t stream) {
-  auto run = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.blocks), dim3(threads), 0, stream, a); };
   if (pl.in_registers) {
-    using igc_rows::norm_back_rows_kernel;
-    if (a.N <= 128) run(norm_back_rows_kernel<XT, OT, 16, 1, 1024>, 1024);
-    else if (a.N <= 256) run(norm_back_rows_kernel<XT, OT, 32, 1, 1024>, 1024);
-    else if (a.N <= 512) run(norm_back_rows_kernel<XT, OT, 64, 1, 1024>, 1024);
-    else if (a.N <= 1024) run(norm_back_rows_kernel<XT, OT, 128, 1, 1024>, 1024);
-    else if (a.N <= 2048) run(norm_back_rows_kernel<XT, OT, 256, 1, 1024>, 1024);
-    else if (a.N <= 4096) run(norm_back_rows_kernel<XT, OT, 512, 1, 1024>, 1024);
-    else run(norm_back_rows_kernel<XT, OT, 1024, 1, 1024>, 1024);
+    const dim3 g((unsigned)a.blocks);
+#define IGC_BACK(T) hipLaunchKernelGGL((igc_rows::norm_back_rows_kernel<XT, OT, T, 1, 1024>), g, dim3(1024), 0, stream, a)
+    if (a.N <= 128) IGC_BACK(16);
+    else if (a.N <= 256) IGC_BACK(32);
+    else if (a.N <= 512) IGC_BACK(64);
+    else if (a.N <= 1024) IGC_BACK(128);
+    else if (a.N <= 2048) IGC_BACK(256);
+    else if (a.N <= 4096) IGC_BACK(512);
+    else IGC_BACK(1024);
+#undef IGC_BACK
     return launch_status();
   }
   if (a.dX) {
