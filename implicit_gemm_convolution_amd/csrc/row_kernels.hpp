@@ -182,27 +182,38 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*slot)[1]) {
 // q = round(127 x / m) with ties to even, exact for x and m (the largest |x|)
 // of a 16-bit type: with significands a and c below 2^11 the quotient is a tie
 // or at least 1 / 254 a > 2^-19 of its own size off every tie.  127 x is exact, the
-// reciprocal and the product are off by 2^-23 together, and rounding to 20
-// significant bits moves the result by 2^-20 at most: it takes quotients that
-// are ties back to them (a tie has 8 significant bits) and the others across
-// none.  Adding 1.5 2^23 then rounds to a whole number, ties to even, and leaves
+// reciprocal (an ulp) and the product (half of one) are off by 1.5 2^-23
+// together, and rounding to 20 significant bits moves the result by 2^-20 at
+// most: it takes quotients that are ties back to them (a tie has 8 significant
+// bits) and the others across none.  Adding 1.5 2^23 then rounds to a whole number, ties to even, and leaves
 // it in the lowest byte.  Five operations an element, and three for four to pack
 // them.  `by` is 127 times a power of two and `inv` the reciprocal of m times
 // the same power, which keeps both products of any m within fp32.
 struct Quantizer {
-  float by, inv, scale;
+  float by, inv;
   // m: the bits of the largest |x| of a row of type T.  Rows with an infinity or NaN
   // get NaN as their scale and zeros, which carries the NaN into what is made of them.
   template <int T>
   __device__ __forceinline__ static Quantizer of(uint32_t m) {
-    const float top = T == T_BF16 ? __builtin_bit_cast(float, m << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)m);
-    const bool finite = m < (T == T_BF16 ? 0x7f80u : 0x7c00u), some = m != 0;
+    const float top = value<T>(m);
+    const bool finite = m < limit<T>(), some = m != 0;
     const float k = top >= 0x1p100f ? 0x1p-64f : top < 0x1p-64f ? 0x1p64f : 1.0f;
     Quantizer q;
     q.by = 127.0f * k;
-    q.inv = finite && some ? 1.0f / (top * k) : 0.0f;
-    q.scale = finite ? top / 127.0f : __builtin_nanf("");
+    q.inv = finite && some ? __builtin_amdgcn_rcpf(top * k) : 0.0f;
     return q;
+  }
+  template <int T>
+  __device__ __forceinline__ static float scale(uint32_t m) {
+    return m < limit<T>() ? value<T>(m) / 127.0f : __builtin_nanf("");
+  }
+  template <int T>
+  __device__ __forceinline__ static float value(uint32_t m) {
+    return T == T_BF16 ? __builtin_bit_cast(float, m << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+  }
+  template <int T>
+  __device__ __forceinline__ static constexpr uint32_t limit() {
+    return T == T_BF16 ? 0x7f80u : 0x7c00u;
   }
   __device__ __forceinline__ uint32_t operator()(float x) const {  // in the lowest byte
     const float t = (x * by) * inv;
@@ -248,29 +259,50 @@ struct RowArgs {
   int stream_y, stream_q;  // written past the caches
 };
 
+// 1 / sqrt(v), off by 2^-23 of its size at most (the square root and the division
+// in full, 27 instructions in every thread for 2, where v may be too small for
+// the instruction).
+__device__ __forceinline__ float rsqrt_of(float v) {
+  return v < 0x1p-100f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
+}
+
 // Mean and variance of a row in its threads' registers, with one barrier: every
 // wave takes the mean of its own elements and their squared distances from it,
 // and the waves' parts join as M2 = sum of M2_w + n_w (mean_w - mean)^2: no
 // difference of large squares anywhere.  (With a barrier for the mean and one for
 // the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
-template <int T, int C>
-__device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, float inv_n, float2* parts, float& mean, float& var) {
-  constexpr int WT = T < 64 ? T : 64;
-  auto add = [](float a, float b) { return a + b; };
-  auto of_wave = [&](int w) {  // elements that wave w holds
-    int k = 0;
+// What does not change from row to row: one over the number of elements that this
+// thread's wave holds, and how many the wave holds whose part this lane takes.
+struct WaveShare {
+  float inv_own = 0.0f, lane = 0.0f;
+  template <int T, int C>
+  __device__ __forceinline__ static WaveShare of(int t, int n) {
+    WaveShare r;
+    auto held = [&](int w) {
+      int k = 0;
 #pragma unroll
-    for (int j = 0; j < C; ++j) k += min(max(n - (j * T + w * 64) * 8, 0), WT * 8);
-    return (float)k;
-  };
-  constexpr int W = T / 64;
+      for (int j = 0; j < C; ++j) k += min(max(n - (j * T + w * 64) * 8, 0), 512);
+      return (float)k;
+    };
+    if constexpr (T > 64) {
+      r.inv_own = 1.0f / fmaxf(held(t >> 6), 1.0f);
+      r.lane = held(t % (T / 64));
+    }
+    return r;
+  }
+};
+template <int T, int C>
+__device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, float inv_n, const WaveShare& w, float2* parts, float& mean,
+                                          float& var) {
+  constexpr int WT = T < 64 ? T : 64, W = T / 64;
+  auto add = [](float a, float b) { return a + b; };
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < C; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += v[j][e];  // (zeros past the row)
   s = wave_combine<WT>(s, add);
-  const float m = T <= 64 ? s * inv_n : s / fmaxf(of_wave(t >> 6), 1.0f);
+  const float m = s * (T <= 64 ? inv_n : w.inv_own);
   float d2 = 0.0f;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
@@ -290,10 +322,9 @@ __device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, 
   } else {
     if ((t & 63) == 0) parts[t >> 6] = make_float2(m, d2);
     __syncthreads();
-    const float2 w = parts[t % W];  // (a lane for each wave's part)
-    const float k = of_wave(t % W);
-    mean = wave_combine<W>(w.x * k, add) * inv_n;
-    var = wave_combine<W>(__builtin_fmaf((w.x - mean) * (w.x - mean), k, w.y), add) * inv_n;
+    const float2 a = parts[t % W];  // (a lane for each wave's part)
+    mean = wave_combine<W>(a.x * w.lane, add) * inv_n;
+    var = wave_combine<W>(__builtin_fmaf((a.x - mean) * (a.x - mean), w.lane, a.y), add) * inv_n;
   }
 }
 
@@ -305,13 +336,14 @@ __device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, 
 template <int T>
 constexpr int row_threads = T < 256 ? 256 : T;
 template <bool NORM, int XT, int OT, int T, int C>
-__global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : XT == T_F32 && T < 1024 ? 7 : 8) row_kernel(const RowArgs p) {
+__global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : T == 128 || (XT == T_F32 && T < 1024) ? 7 : 8) row_kernel(const RowArgs p) {
   constexpr int RG = row_threads<T> / T;  // rows of a workgroup
   constexpr int W = T < 64 ? 1 : T / 64;
   __shared__ float2 parts[2][RG][W];
   __shared__ uint32_t tops[2][RG][W][1];
   const int t = threadIdx.x % T, rg = threadIdx.x / T;
   auto col = [&](int j) { return (j * T + t) * 8; };
+  const WaveShare share = WaveShare::of<T, C>(t, p.N);
   float gamma[C][8], beta[C][8];
   Raw<XT> next[C];
   auto load = [&](long long row) {
@@ -350,8 +382,8 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : XT == T_F32 && T <
         }
       if (row + step < p.M) load(row + step);
       float mean, var;
-      row_stats<T, C>(v, t, p.N, p.inv_n, parts[turn][rg], mean, var);
-      const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
+      row_stats<T, C>(v, t, p.N, p.inv_n, share, parts[turn][rg], mean, var);
+      const float rstd = rsqrt_of(var + p.eps);
       if (in && t == 0 && p.mean) p.mean[row] = mean;
       if (in && t == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
@@ -372,8 +404,9 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : XT == T_F32 && T <
 #pragma unroll
       for (int j = 0; j < C; ++j)
         if (in && col(j) < p.N) top = max(top, out[j].top());
-      const Quantizer q = Quantizer::of<OT>(row_max<T>(top, tops[turn][rg]));
-      if (in && t == 0) p.scale[row] = q.scale;
+      top = row_max<T>(top, tops[turn][rg]);
+      const Quantizer q = Quantizer::of<OT>(top);
+      if (in && t == 0) p.scale[row] = Quantizer::scale<OT>(top);
 #pragma unroll
       for (int j = 0; j < C; ++j)
         if (in && col(j) < p.N) {
@@ -421,7 +454,7 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
           s = __builtin_fmaf(d, d, s);
         }
       });
-      rstd = 1.0f / __builtin_sqrtf(row_sum<T>(s, sums[1]) * p.inv_n + p.eps);
+      rstd = rsqrt_of(row_sum<T>(s, sums[1]) * p.inv_n + p.eps);
       if (threadIdx.x == 0 && p.mean) p.mean[row] = mean;
       if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
     }
@@ -452,8 +485,9 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
       });
     }
     if (p.scale) {
-      const Quantizer q = Quantizer::of<OT>(row_max<T>(top, tops[turn]));
-      if (threadIdx.x == 0) p.scale[row] = q.scale;
+      top = row_max<T>(top, tops[turn]);
+      const Quantizer q = Quantizer::of<OT>(top);
+      if (threadIdx.x == 0) p.scale[row] = Quantizer::scale<OT>(top);
       chunks([&](float(&v)[8], int c, int n) {
         normed(v, c, n);
         q.store(p.Q + row * p.ldq + c, n, v, p.stream_q);

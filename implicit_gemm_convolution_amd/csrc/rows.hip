@@ -47,7 +47,7 @@ void check_rows(Checker& c, int M, int N, int type) {
 
 // ---------------------------------------------------------------- rows
 // Threads to a row: as many as it has chunks, up to 1024 with two chunks each
-// (more rows at once in a compute unit's registers than with more chunks a
+// (so more rows at once in a compute unit's registers than with more chunks a
 // thread: 8192 x 4096 bf16 32.6 us with 512 threads, 36.0 with 256 and two chunks;
 // 8192 x 1024 10.4, and 14.6 by a wave with two).  Longer rows are read again in
 // every pass (2000 x 20000 54 us: 2.9 TB/s).
@@ -56,6 +56,17 @@ void launch_rows(const RowArgs& a, int cus, hipStream_t stream) {
   auto groups = [&](int threads, int rows) { return dim3((unsigned)std::min(ceil_div(a.M, rows), 2048LL / threads * cus)); };
 #define IGC_ROWS(threads, rows, ...) \
   hipLaunchKernelGGL((igc_rows::__VA_ARGS__), groups(threads, rows), dim3(threads), 0, stream, a)
+  if constexpr (NORM) {
+    // Many rows of fp32, or to 8 bits, are bound by instructions, and what a row
+    // takes of them in every thread is shared by two chunks (us, one chunk and
+    // two: 8192 x 4096 fp32 to bf16 41.8 and 37.6, 8192 x 8192 to 8 bits 61 and 55; 8192 x 4096
+    // bf16 to bf16 22.5 and 22.7, 1000 x 5001 fp32 to fp16 10.6 and 12.4).
+    if (a.N > 2048 && a.N <= 8192 && a.M >= 8LL * cus && (a.scale || XT == igc_ffn::T_F32)) {
+      if (a.N <= 4096) IGC_ROWS(256, 1, row_kernel<NORM, XT, OT, 256, 2>);
+      else IGC_ROWS(512, 1, row_kernel<NORM, XT, OT, 512, 2>);
+      return;
+    }
+  }
   if (a.N <= 128) IGC_ROWS(256, 16, row_kernel<NORM, XT, OT, 16, 1>);
   else if (a.N <= 256) IGC_ROWS(256, 8, row_kernel<NORM, XT, OT, 32, 1>);
   else if (a.N <= 512) IGC_ROWS(256, 4, row_kernel<NORM, XT, OT, 64, 1>);

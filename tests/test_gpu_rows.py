@@ -120,6 +120,32 @@ def test_layer_norm_forward(torch, igc, size, kind, x_kind):  # noqa: F811
     assert torch.equal(Y.t, kept) and torch.equal(Q.t, q) and torch.equal(scale[:M], s)
 
 
+@pytest.mark.parametrize("kind,x_kind", TYPES, ids=str)
+@pytest.mark.parametrize("N", [2049, 2500, 4096, 4100, 5001, 8192])
+def test_layer_norm_forward_of_many_rows(torch, igc, N, kind, x_kind):  # noqa: F811
+    """Rows enough that a workgroup takes several, with the kernels that only many rows take."""
+    M = 2100
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(N)
+    X = Mat(torch, M, N, x_kind, values=_stream(torch, gen, M, N))
+    gamma, beta = 1 + 0.3 * torch.randn(N, generator=gen, device="cuda"), torch.randn(N, generator=gen, device="cuda")
+    Y, Q, R = Mat(torch, M, N, kind), Bytes(torch, M, N), Bytes(torch, M, N)
+    mean, rstd, s, t = (torch.empty(M, device="cuda") for _ in range(4))
+    kw = dict(gamma=gamma, beta=beta, eps=EPS, type=_type(igc, kind), x_type=_type(igc, x_kind))
+    igc.layer_norm_forward(M, N, X.ptr, N, Y.ptr, N, mean=mean, rstd=rstd, Q=Q.ptr, ldq=N, scale=s, **kw)
+    y, m, r, ey, em, er = _norm_reference(X.double(), gamma.double(), beta.double())
+    _check("Y", Y.t, y, ey + _store(kind, y.abs() + ey))
+    _check("mean", mean, m, em + U * m.abs())
+    _check("rstd", rstd, r, er)
+    q, scale = _exact_rows(Y.double())
+    assert torch.equal(Q.t.double(), q) and torch.equal(s, scale) and Q.others_untouched() and Y.others_untouched()
+    igc.layer_norm_forward(M, N, X.ptr, N, None, N, Q=R.ptr, ldq=N, scale=t, **kw)
+    assert torch.equal(R.t, Q.t) and torch.equal(s, t)
+    mean.fill_(float("nan"))
+    igc.layer_norm_forward(M, N, X.ptr, N, None, N, mean=mean, **kw)  # the means alone
+    _check("mean", mean, m, em + U * m.abs())
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("size", SIZES, ids=str)
 def test_quantize_rows(torch, igc, size, kind):  # noqa: F811
