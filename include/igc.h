@@ -52,7 +52,7 @@ extern "C" {
 #define IGC_OK 0
 #define IGC_EINVAL (-1)       /* null pointer, negative size, ld too small, zero point out of range */
 #define IGC_EUNSUPPORTED (-2) /* a shape / stride combination no kernel variant handles             */
-#define IGC_EOVERFLOW (-3)    /* u8 x i8 with K > 33025: the int32 result could overflow              */
+#define IGC_EOVERFLOW (-3)    /* K > 33025 (u8 x i8) or > 131071 (i8 x i8): int32 sums could overflow  */
 #define IGC_EHIP (-4)         /* HIP runtime or launch error; detail in igc_last_error()              */
 #define IGC_ENODEV (-5)       /* the current HIP device is not a gfx950 GPU, or there is no device    */
 
