@@ -145,9 +145,9 @@ __device__ __forceinline__ V wave_combine(V v, F&& f) {
 
 // N values of every thread of a row's T threads, combined in every one of
 // them: the lanes of a wave, then the waves through LDS, a lane for each, with
-// one barrier (of the whole workgroup).  slot: W entries of the row.  Calls take slots in turn,
-// two at least: who writes a slot again has passed the barrier of the other
-// one, which everyone reaches after reading this one.
+// one barrier (of the whole workgroup).  slot: W entries of the row.  Calls take
+// slots in turn, two at least: who writes a slot again has passed the barrier of
+// the other one, which everyone reaches after reading this one.
 template <int T, int N, class V, class F>
 __device__ __forceinline__ void row_combine(V (&v)[N], V (*slot)[N], F&& f) {
 #pragma unroll
@@ -185,10 +185,12 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*slot)[1]) {
 // reciprocal (an ulp) and the product (half of one) are off by 1.5 2^-23
 // together, and rounding to 20 significant bits moves the result by 2^-20 at
 // most: it takes quotients that are ties back to them (a tie has 8 significant
-// bits) and the others across none.  Adding 1.5 2^23 then rounds to a whole number, ties to even, and leaves
-// it in the lowest byte.  Five operations an element, and three for four to pack
-// them.  `by` is 127 times a power of two and `inv` the reciprocal of m times
-// the same power, which keeps both products of any m within fp32.
+// bits) and the others across none.  Adding 1.5 2^23 then rounds to a whole
+// number, ties to even, and leaves it in the lowest byte.  Five operations an
+// element, and three for four to pack them (8192 x 4096 bf16 17.0 us, 5.9 TB/s;
+// 21.9 with a conversion and shifts).  `by` is 127 times a power of two and `inv`
+// the reciprocal of m times the same power, which keeps both products of any m
+// within fp32.
 struct Quantizer {
   float by, inv;
   // m: the bits of the largest |x| of a row of type T.  Rows with an infinity or NaN
@@ -266,11 +268,6 @@ __device__ __forceinline__ float rsqrt_of(float v) {
   return v < 0x1p-100f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
 }
 
-// Mean and variance of a row in its threads' registers, with one barrier: every
-// wave takes the mean of its own elements and their squared distances from it,
-// and the waves' parts join as M2 = sum of M2_w + n_w (mean_w - mean)^2: no
-// difference of large squares anywhere.  (With a barrier for the mean and one for
-// the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
 // What does not change from row to row: one over the number of elements that this
 // thread's wave holds, and how many the wave holds whose part this lane takes.
 struct WaveShare {
@@ -291,6 +288,11 @@ struct WaveShare {
     return r;
   }
 };
+// Mean and variance of a row in its threads' registers, with one barrier: every
+// wave takes the mean of its own elements and their squared distances from it,
+// and the waves' parts join as M2 = sum of M2_w + n_w (mean_w - mean)^2: no
+// difference of large squares anywhere.  (With a barrier for the mean and one for
+// the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
 template <int T, int C>
 __device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, float inv_n, const WaveShare& w, float2* parts, float& mean,
                                           float& var) {
@@ -515,87 +517,82 @@ struct NormBackArgs {
   int stream;                // dX is written past the caches
 };
 
-// Rows in registers: T threads a row, C chunks of 8 elements a thread, WG / T
+// Rows in registers: T threads a row, a chunk of 8 elements a thread, 1024 / T
 // rows at a time, one reduction of two sums a row, and the sums down the rows
 // in the registers of the threads that hold their columns.  Each input is read
-// once.  The next row is on its way while this one is summed.
-template <int XT, int OT, int T, int C, int WG>
-__global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p) {
-  constexpr int RG = WG / T, W = T < 64 ? 1 : T / 64, COLS = T * C * 8;
+// once.  The next row is on its way while this one is summed.  (8192 x 4096 bf16
+// with a residual 43 us, 6.2 TB/s, and 4.5 for the second launch; two launches that read dY
+// and X twice 75.)
+template <int XT, int OT, int T>
+__global__ void __launch_bounds__(1024) norm_back_rows_kernel(const NormBackArgs p) {
+  constexpr int RG = 1024 / T, W = T < 64 ? 1 : T / 64, COLS = T * 8;
   __shared__ float slots[2][RG][W][2];
   __shared__ float part[RG > 1 ? RG * COLS : 1];
   const int t = threadIdx.x % T, rg = threadIdx.x / T;
-  auto col = [&](int j) { return (j * T + t) * 8; };
-  float gamma[C][8], sg[C][8], sb[C][8];
-  Raw<OT> dy[C];
-  Raw<XT> x[C], r[C];
+  const int c = t * 8;
+  const bool have = c < p.N;
+  float gamma[8], sg[8], sb[8];
+  Raw<OT> dy;
+  Raw<XT> x, r;
+  float next_mean = 0.0f, next_rstd = 0.0f;
   auto load = [&](long long row) {
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (col(j) < p.N) {
-        dy[j].load(p.dY + row * p.lddy * Raw<OT>::EB, col(j), p.N);
-        x[j].load(p.X + row * p.ldx * Raw<XT>::EB, col(j), p.N);
-        if (p.R) r[j].load(p.R + row * p.ldr * Raw<XT>::EB, col(j), p.N);
-      }
+    next_mean = p.mean[row];
+    next_rstd = p.rstd[row];
+    if (have) {
+      dy.load(p.dY + row * p.lddy * Raw<OT>::EB, c, p.N);
+      x.load(p.X + row * p.ldx * Raw<XT>::EB, c, p.N);
+      if (p.R) r.load(p.R + row * p.ldr * Raw<XT>::EB, c, p.N);
+    }
   };
   const long long step = (long long)gridDim.x * RG;
   long long first = (long long)blockIdx.x * RG;
   if (first + rg < p.M) load(first + rg);
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      gamma[j][e] = 1.0f;
-      sg[j][e] = sb[j][e] = 0.0f;
-    }
-    if (p.gamma && col(j) < p.N) load_vector(p.gamma, col(j), p.N, gamma[j]);
+  for (int e = 0; e < 8; ++e) {
+    gamma[e] = 1.0f;
+    sg[e] = sb[e] = 0.0f;
   }
+  if (p.gamma && have) load_vector(p.gamma, c, p.N, gamma);
   for (int turn = 0; first < p.M; first += step, turn ^= 1) {  // (as often for every row of the workgroup: the barrier)
     const long long row = first + rg;
     const bool in = row < p.M;
-    const float mean = in ? p.mean[row] : 0.0f, rstd = in ? p.rstd[row] : 0.0f;
-    float d[C][8], v[C][8], a[C][8];
+    const float mean = in ? next_mean : 0.0f, rstd = in ? next_rstd : 0.0f;
+    float d[8], v[8], a[8];
+    if (in && have) {
+      dy.get(d);
+      x.get(v);
+      if (p.R) r.get(a);
+    } else {
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (in && col(j) < p.N) {
-        dy[j].get(d[j]);
-        x[j].get(v[j]);
-        if (p.R) r[j].get(a[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[j][e] = v[j][e] = a[j][e] = 0.0f;
-      }
+      for (int e = 0; e < 8; ++e) d[e] = v[e] = a[e] = 0.0f;
+    }
     if (row + step < p.M) load(row + step);
     float m[2] = {0.0f, 0.0f};
+    const float from = have ? mean : 0.0f;  // (what lies past the row is 0, and 0 from there)
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[j][e] = (v[j][e] - mean) * rstd;
-        sg[j][e] = __builtin_fmaf(d[j][e], v[j][e], sg[j][e]);
-        sb[j][e] += d[j][e];
-        d[j][e] *= gamma[j][e];
-        if (col(j) + e < p.N) {
-          m[0] += d[j][e];
-          m[1] = __builtin_fmaf(d[j][e], v[j][e], m[1]);
-        }
-      }
+    for (int e = 0; e < 8; ++e) {
+      v[e] = (v[e] - from) * rstd;
+      if ((p.N & 7) && c + e >= p.N) v[e] = 0.0f;
+      sg[e] = __builtin_fmaf(d[e], v[e], sg[e]);
+      sb[e] += d[e];
+      d[e] *= gamma[e];
+      m[0] += d[e];
+      m[1] = __builtin_fmaf(d[e], v[e], m[1]);
+    }
     if (!p.dX) continue;
     row_combine<T, 2>(m, slots[turn][rg], [](float f, float g) { return f + g; });
     m[0] *= p.inv_n;
     m[1] *= p.inv_n;
+    if (in && have) {
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (in && col(j) < p.N) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[j][e] = rstd * (__builtin_fmaf(-v[j][e], m[1], d[j][e]) - m[0]);
-          if (p.R) v[j][e] += a[j][e];
-        }
-        Raw<XT> out;
-        out.set(v[j]);
-        out.store(p.dX + row * p.lddx * Raw<XT>::EB, col(j), p.N, p.stream);
+      for (int e = 0; e < 8; ++e) {
+        v[e] = rstd * (__builtin_fmaf(-v[e], m[1], d[e]) - m[0]);
+        if (p.R) v[e] += a[e];
       }
+      Raw<XT> out;
+      out.set(v);
+      out.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N, p.stream);
+    }
   }
   if (!p.sums) return;
   float* const to = p.sums + (long long)blockIdx.x * 2 * p.width;
@@ -603,19 +600,16 @@ __global__ void __launch_bounds__(WG) norm_back_rows_kernel(const NormBackArgs p
   for (int which = 0; which < 2; ++which) {
     const auto& s = which ? sb : sg;
     if constexpr (RG == 1) {
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-        if (col(j) < p.N) store_f32<8>(to + which * p.width + col(j), p.N - col(j), s[j]);
+      if (have) store_f32<8>(to + which * p.width + c, p.N - c, s);
     } else {
       __syncthreads();
-#pragma unroll
-      for (int j = 0; j < C; ++j) __builtin_memcpy(part + rg * COLS + col(j), s[j], 32);
+      __builtin_memcpy(part + rg * COLS + c, s, 32);
       __syncthreads();
-      for (int c = threadIdx.x; c < COLS && c < p.N; c += WG) {
-        float f = part[c];
+      for (int i = threadIdx.x; i < COLS && i < p.N; i += 1024) {
+        float f = part[i];
 #pragma unroll
-        for (int i = 1; i < RG; ++i) f += part[i * COLS + c];
-        to[which * p.width + c] = f;
+        for (int g = 1; g < RG; ++g) f += part[g * COLS + i];
+        to[which * p.width + i] = f;
       }
     }
   }

@@ -189,7 +189,7 @@ template <int XT, int OT>
 int launch_back(const NormBackArgs& a, const BackPlan& pl, int cus, hipStream_t stream) {
   if (pl.in_registers) {
     const dim3 g((unsigned)a.blocks);
-#define IGC_BACK(T) hipLaunchKernelGGL((igc_rows::norm_back_rows_kernel<XT, OT, T, 1, 1024>), g, dim3(1024), 0, stream, a)
+#define IGC_BACK(T) hipLaunchKernelGGL((igc_rows::norm_back_rows_kernel<XT, OT, T>), g, dim3(1024), 0, stream, a)
     if (a.N <= 128) IGC_BACK(16);
     else if (a.N <= 256) IGC_BACK(32);
     else if (a.N <= 512) IGC_BACK(64);

@@ -562,7 +562,7 @@ int grad_clip_workspace_size(const igc_grad_clip* d, size_t* bytes);
  *   Q, scale     int8 M x N and fp32 of length M: the rows of y, rounded to `type`,
  *                in 8 bits as quantize_rows leaves them; or NULL
  * The statistics are held in fp32 and the deviations taken from the row's own mean.
- * A row with an infinity or NaN has NaN in all its outputs (zeros in Q).
+ * A row with an infinity or NaN has NaN in Y, zeros in Q and NaN as its scale.
  * N == 0 leaves mean = 0 and rstd = 1 / sqrt(eps).
  * Errors: IGC_EINVAL (NULL descriptor or X, no output, negative size, leading
  * dimension below the row length, unknown type, eps negative or not finite,

@@ -338,6 +338,29 @@ def test_layer_norm_gradient_against_differences(torch, igc, ws):  # noqa: F811
             assert abs(float(got.view(-1)[i]) - diff) <= 2e-6 + 40 * U * (abs(diff) + float(dY.abs().max()) * N), (which, i)
 
 
+@pytest.mark.parametrize("N", [7, 9, 60, 500, 1001, 3000, 8001, 9001, 20001])
+def test_norm_of_rows_of_one_huge_value(torch, igc, ws, N):  # noqa: F811
+    """Deviations of nothing, far from zero: what lies past the row in the last chunk must not come in."""
+    M = 3
+    X = torch.tensor([2.0 ** 100, -(2.0 ** 110), 2.0 ** 126], device="cuda")[:, None].repeat(1, N)
+    X[2] = torch.where(torch.arange(N, device="cuda") % 2 == 0, X[2], -X[2])  # mean 0 or a few, deviations that overflow
+    Y, mean, rstd = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    kw = dict(type=igc.IGC_BF16, x_type=igc.IGC_F32)
+    igc.layer_norm_forward(M, N, X, N, Y, N, mean=mean, rstd=rstd, **kw)
+    # whole powers of two: the means are off by their sums' roundings at most
+    assert float((mean[:2].double() - X[:2, 0].double()).abs().max() / 2.0 ** 110) <= _depth(N) * U
+    assert float(rstd[2]) == 0.0 and not bool(Y[2].any())  # (the variance is past fp32: as the formula has it there)
+    mean[:2] = X[:2, 0]
+    rstd[:2] = 316.0
+    dY = torch.randn(M, N, device="cuda").bfloat16()
+    dX, dg, db = torch.empty_like(X), torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    igc.layer_norm_backward(2, N, dY, N, X, N, mean, rstd, dX=dX, lddx=N, dgamma=dg, dbeta=db, workspace=ws, **kw)
+    d = dY[:2].double()
+    want = 316.0 * (d - d.mean(1, keepdim=True))
+    assert float((dX[:2].double() - want).abs().max()) <= 316.0 * (_depth(N) + 4) * U * float(d.abs().max()) * 2
+    assert not bool(dg.any())
+
+
 def test_rows_past_32_bit_offsets(torch, igc, ws):  # noqa: F811
     """Rows that begin more than 2^32 bytes, and 2^31 elements, into their matrices."""
     M, N, ld = 3, 520, 2 ** 30 + 64
