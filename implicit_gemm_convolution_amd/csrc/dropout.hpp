@@ -41,7 +41,6 @@ struct DropArgs {
   int drops;           // T > 0
   uint32_t last;       // T - 1: the largest word that drops its element
   float scale;
-  int stream;  // Y is written past the caches
   uint32_t seed0, seed1;
   uint64_t offset;
   const uint64_t* step;  // added to offset, or NULL
@@ -62,6 +61,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs p) {
     x.load(p.X + row * p.ldx * Raw<XT>::EB, c, p.N);
     if (p.R) r.load(p.R + row * p.ldr * Raw<YT>::EB, c, p.N);
     float f[8];
+    x.settle(c, p.N);
     x.get(f);
     if (p.drops) {
       uint32_t w[8];
@@ -72,12 +72,13 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs p) {
     }
     if (p.R) {
       float a[8];
+      r.settle(c, p.N);
       r.get(a);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] += a[e];
     }
     r.set(f);
-    r.store(p.Y + row * p.ldy * Raw<YT>::EB, c, p.N, p.stream);
+    r.store(p.Y + row * p.ldy * Raw<YT>::EB, c, p.N);
     row += p.step_row;
     chunk += p.step_chunk;
     if (chunk >= p.per) {

@@ -29,27 +29,35 @@ using igc_ffn::unpack8;
 
 // Eight elements of type T (igc_ffn::Type) as they lie in memory: those of a row
 // of n elements from column c, zeros past the row.  The chunk at a row's end is
-// loaded as the row's last eight elements and shifted (element by element, its
-// loads would wait for one another).
-// STREAM (chunks of whole, aligned rows alone): written past the caches.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// loaded as the row's last eight elements (element by element, its loads would
+// wait for one another) and shifted into place by settle(), where it is used: at
+// the load the shift would wait for the data, and the workgroup's other waves for
+// that one at the next barrier (backward of 8192 x 4095 bf16 73 us, so 54; rows in 8
+// bits of 8192 x 4097 25, so 22).
+// Whole chunks are written past the caches, wherever they lie (us, in the caches
+// and past them: norm of 8192 x 4096 bf16 32.7 and 26.7, of 1000 x 4096 9.1 and 7.8, and
+// in its form of now, 8192 x 4095 35 and 26.6, 2048 x 20001 63 and 52; rows in 8 bits of
+// 8192 x 4097 33 and 25; the backward pass of 8192 x 4095 75 and 73; dropout of 8192 x
+// 8191 from -3 to +3%).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 template <int T>
 struct Raw {
   static constexpr int EB = 2;
   uint4 v;
   __device__ __forceinline__ void load(const uint8_t* row, int c, int n) {
-    const uint8_t* const p = row + (long long)c * 2;
-    if (n - c >= 8 || c == 0) {
-      v = load8(p, n - c);
-    } else {
-      const int over = c + 8 - n;
-      unsigned __int128 w;
-      __builtin_memcpy(&w, p - over * 2, 16);
-      w >>= 16 * over;
-      __builtin_memcpy(&v, &w, 16);
-    }
+    if (n >= 8)
+      v = load8(row + (long long)min(c, n - 8) * 2, 8);
+    else
+      v = load8(row, n);
+  }
+  __device__ __forceinline__ void settle(int c, int n) {
+    if (n - c >= 8 || c == 0) return;
+    unsigned __int128 w;
+    __builtin_memcpy(&w, &v, 16);
+    w >>= 16 * (c + 8 - n);
+    __builtin_memcpy(&v, &w, 16);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const { unpack8<T == T_BF16>(v, f); }
   __device__ __forceinline__ void set(const float (&f)[8]) { v = pack8<T == T_BF16>(f); }
@@ -66,9 +74,9 @@ struct Raw {
     const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(abs(v.x), abs(v.y)), __builtin_elementwise_max(abs(v.z), abs(v.w)));
     return max((uint32_t)m[0], (uint32_t)m[1]);
   }
-  __device__ __forceinline__ void store(uint8_t* row, int c, int n, bool stream) const {
+  __device__ __forceinline__ void store(uint8_t* row, int c, int n) const {
     uint8_t* const p = row + (long long)c * 2;
-    if (stream)
+    if (n - c >= 8)
       __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
     else
       store8(p, v, n - c);
@@ -79,17 +87,19 @@ struct Raw<T_F32> {
   static constexpr int EB = 4;
   float v[8];
   __device__ __forceinline__ void load(const uint8_t* row, int c, int n) {
-    const float* const p = reinterpret_cast<const float*>(row) + c;
-    if (n - c >= 8 || c == 0) {
-      load_f32<8>(p, n - c, v);
-    } else {
-      const int over = c + 8 - n;
-      load_f32<8>(p - over, 8, v);
+    const float* const p = reinterpret_cast<const float*>(row);
+    if (n >= 8)
+      load_f32<8>(p + min(c, n - 8), 8, v);
+    else
+      load_f32<8>(p, n, v);
+  }
+  __device__ __forceinline__ void settle(int c, int n) {
+    if (n - c >= 8 || c == 0) return;
+    const int over = c + 8 - n;
 #pragma unroll
-      for (int s = 4; s; s >>= 1)
+    for (int s = 4; s; s >>= 1)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = !(over & s) ? v[e] : e + s < 8 ? v[(e + s) & 7] : 0.0f;
-    }
+      for (int e = 0; e < 8; ++e) v[e] = !(over & s) ? v[e] : e + s < 8 ? v[(e + s) & 7] : 0.0f;
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
@@ -99,9 +109,9 @@ struct Raw<T_F32> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = f[e];
   }
-  __device__ __forceinline__ void store(uint8_t* row, int c, int n, bool stream) const {
+  __device__ __forceinline__ void store(uint8_t* row, int c, int n) const {
     float* const p = reinterpret_cast<float*>(row) + c;
-    if (stream) {
+    if (n - c >= 8) {
       u32x4 w[2];
       __builtin_memcpy(w, v, 32);
       __builtin_nontemporal_store(w[0], reinterpret_cast<u32x4*>(p));
@@ -115,6 +125,7 @@ struct Raw<T_F32> {
 __device__ __forceinline__ void load_vector(const float* p, int c, int n, float (&f)[8]) {
   Raw<T_F32> r;
   r.load(reinterpret_cast<const uint8_t*>(p), c, n);
+  r.settle(c, n);
   r.get(f);
 }
 
@@ -222,7 +233,7 @@ struct Quantizer {
     const uint32_t u = (__builtin_bit_cast(uint32_t, t) + 8u) & ~15u;
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u) + 12582912.0f);
   }
-  __device__ __forceinline__ void store(int8_t* p, int valid, const float (&f)[8], bool stream) const {
+  __device__ __forceinline__ void store(int8_t* p, int valid, const float (&f)[8]) const {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -230,10 +241,8 @@ struct Quantizer {
       const uint32_t b = __builtin_amdgcn_perm((*this)(f[i * 4 + 3]), (*this)(f[i * 4 + 2]), 0x0c0c0400u);
       w[i] = inv == 0.0f ? 0u : a | b << 16;  // (infinities and NaN times zero)
     }
-    if (stream) {
+    if (valid >= 8) {
       __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p));
-    } else if (valid >= 8) {
-      __builtin_memcpy(p, w, 8);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -258,7 +267,6 @@ struct RowArgs {
   int8_t* Q;
   long long ldq;
   float* scale;  // or NULL: no rows in 8 bits
-  int stream_y, stream_q;  // written past the caches
 };
 
 // 1 / sqrt(v), off by 2^-23 of its size at most (the square root and the division
@@ -294,7 +302,7 @@ struct WaveShare {
 // difference of large squares anywhere.  (With a barrier for the mean and one for
 // the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
 template <int T, int C>
-__device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, float inv_n, const WaveShare& w, float2* parts, float& mean,
+__device__ __forceinline__ void row_stats(float (&v)[C][8], int t, int n, float inv_n, const WaveShare& w, float2* parts, float& mean,
                                           float& var) {
   constexpr int WT = T < 64 ? T : 64, W = T / 64;
   auto add = [](float a, float b) { return a + b; };
@@ -310,10 +318,13 @@ __device__ __forceinline__ void row_stats(const float (&v)[C][8], int t, int n, 
   for (int j = 0; j < C; ++j) {
     const int c = (j * T + t) * 8;
     const float mc = c < n ? m : 0.0f;  // (chunks past the row are zeros, and their distances)
+    if ((n & 7) && c < n && c + 8 > n) {  // the row's last chunk: no distance from the mean past the row
+#pragma unroll
+      for (int e = 1; e < 8; ++e) v[j][e] = c + e < n ? v[j][e] : m;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float d = v[j][e] - mc;
-      if ((n & 7) && c + e >= n) d = 0.0f;
+      const float d = v[j][e] - mc;
       d2 = __builtin_fmaf(d, d, d2);
     }
   }
@@ -377,6 +388,7 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : T == 128 || (XT ==
 #pragma unroll
       for (int j = 0; j < C; ++j)
         if (in && col(j) < p.N) {
+          next[j].settle(col(j), p.N);
           next[j].get(v[j]);
         } else {
 #pragma unroll
@@ -393,12 +405,15 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : T == 128 || (XT ==
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] = __builtin_fmaf((v[j][e] - mean) * rstd, gamma[j][e], beta[j][e]);
         out[j].set(v[j]);
-        if (p.Y && in && col(j) < p.N) out[j].store(p.Y + row * p.ldy * Raw<OT>::EB, col(j), p.N, p.stream_y);
+        if (p.Y && in && col(j) < p.N) out[j].store(p.Y + row * p.ldy * Raw<OT>::EB, col(j), p.N);
         if ((p.N & 7) && col(j) < p.N && p.N - col(j) < 8) out[j].clear_from(p.N - col(j));
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < C; ++j) out[j] = next[j];
+      for (int j = 0; j < C; ++j) {
+        out[j] = next[j];
+        if (col(j) < p.N) out[j].settle(col(j), p.N);
+      }
       if (row + step < p.M) load(row + step);
     }
     if (p.scale) {
@@ -414,7 +429,7 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : T == 128 || (XT ==
         if (in && col(j) < p.N) {
           float v[8];
           out[j].get(v);
-          q.store(p.Q + row * p.ldq + col(j), p.N - col(j), v, p.stream_q);
+          q.store(p.Q + row * p.ldq + col(j), p.N - col(j), v);
         }
     }
   }
@@ -436,6 +451,7 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
         float v[8];
         Raw<XT> raw;
         raw.load(x, c, p.N);
+        raw.settle(c, p.N);
         raw.get(v);
         f(v, c, min(p.N - c, 8));
       }
@@ -481,7 +497,7 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
     if (!NORM || p.Y || p.scale) {
       chunks([&](float(&v)[8], int c, int n) {
         Raw<OT> out = normed(v, c, n);
-        if (p.Y) out.store(p.Y + row * p.ldy * Raw<OT>::EB, c, p.N, p.stream_y);
+        if (p.Y) out.store(p.Y + row * p.ldy * Raw<OT>::EB, c, p.N);
         if (n < 8) out.clear_from(n);
         top = max(top, out.top());
       });
@@ -492,7 +508,7 @@ __global__ void __launch_bounds__(T) long_row_kernel(const RowArgs p) {
       if (threadIdx.x == 0) p.scale[row] = Quantizer::scale<OT>(top);
       chunks([&](float(&v)[8], int c, int n) {
         normed(v, c, n);
-        q.store(p.Q + row * p.ldq + c, n, v, p.stream_q);
+        q.store(p.Q + row * p.ldq + c, n, v);
       });
     }
   }
@@ -514,7 +530,6 @@ struct NormBackArgs {
   float* sums;    // or NULL: dgamma and dbeta of each row block, [blocks][2][width]
   int width;      // N rounded up to a multiple of 64
   int rows, groups, blocks;  // rows of a block; workgroups across the columns and down the rows
-  int stream;                // dX is written past the caches
 };
 
 // Rows in registers: T threads a row, a chunk of 8 elements a thread, 1024 / T
@@ -559,9 +574,14 @@ __global__ void __launch_bounds__(1024) norm_back_rows_kernel(const NormBackArgs
     const float mean = in ? next_mean : 0.0f, rstd = in ? next_rstd : 0.0f;
     float d[8], v[8], a[8];
     if (in && have) {
+      dy.settle(c, p.N);
       dy.get(d);
+      x.settle(c, p.N);
       x.get(v);
-      if (p.R) r.get(a);
+      if (p.R) {
+        r.settle(c, p.N);
+        r.get(a);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] = v[e] = a[e] = 0.0f;
@@ -569,10 +589,13 @@ __global__ void __launch_bounds__(1024) norm_back_rows_kernel(const NormBackArgs
     if (row + step < p.M) load(row + step);
     float m[2] = {0.0f, 0.0f};
     const float from = have ? mean : 0.0f;  // (what lies past the row is 0, and 0 from there)
+    if ((p.N & 7) && have && c + 8 > p.N) {
+#pragma unroll
+      for (int e = 1; e < 8; ++e) v[e] = c + e < p.N ? v[e] : from;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] = (v[e] - from) * rstd;
-      if ((p.N & 7) && c + e >= p.N) v[e] = 0.0f;
       sg[e] = __builtin_fmaf(d[e], v[e], sg[e]);
       sb[e] += d[e];
       d[e] *= gamma[e];
@@ -591,7 +614,7 @@ __global__ void __launch_bounds__(1024) norm_back_rows_kernel(const NormBackArgs
       }
       Raw<XT> out;
       out.set(v);
-      out.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N, p.stream);
+      out.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N);
     }
   }
   if (!p.sums) return;
@@ -634,7 +657,9 @@ __global__ void __launch_bounds__(T) norm_back_stats_kernel(const NormBackArgs p
       dy.load(p.dY + row * p.lddy * Raw<OT>::EB, c, p.N);
       x.load(p.X + row * p.ldx * Raw<XT>::EB, c, p.N);
       float d[8], v[8], g[8];
+      dy.settle(c, p.N);
       dy.get(d);
+      x.settle(c, p.N);
       x.get(v);
       if (p.gamma) load_vector(p.gamma, c, p.N, g);
 #pragma unroll
@@ -672,7 +697,9 @@ __global__ void __launch_bounds__(256) norm_back_kernel(const NormBackArgs p) {
       dy.load(p.dY + row * p.lddy * Raw<OT>::EB, c, p.N);
       x.load(p.X + row * p.ldx * Raw<XT>::EB, c, p.N);
       float d[8], v[8], a[8];
+      dy.settle(c, p.N);
       dy.get(d);
+      x.settle(c, p.N);
       x.get(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -684,6 +711,7 @@ __global__ void __launch_bounds__(256) norm_back_kernel(const NormBackArgs p) {
         const float2 m = p.stats[row];
         if (p.R) {
           r.load(p.R + row * p.ldr * Raw<XT>::EB, c, p.N);
+          r.settle(c, p.N);
           r.get(a);
         }
 #pragma unroll
@@ -692,7 +720,7 @@ __global__ void __launch_bounds__(256) norm_back_kernel(const NormBackArgs p) {
           if (p.R) v[e] += a[e];
         }
         x.set(v);
-        x.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N, p.stream);
+        x.store(p.dX + row * p.lddx * Raw<XT>::EB, c, p.N);
       }
     }
   }

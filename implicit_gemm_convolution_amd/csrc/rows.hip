@@ -29,14 +29,6 @@ using igc_rows::RowArgs;
 
 int elem(int type) { return type == IGC_F32 ? 4 : 2; }
 
-// Whether an output is written past the caches: rows of whole 128-byte lines
-// (us, in the caches and past them: norm of 8192 x 4096 bf16 32.7 and 26.7, of
-// 1000 x 4096 9.1 and 7.8, to 8 bits 34.2 and 33.3; its backward pass 56.4 and 55.3;
-// dropout of 2048 x 4096 with a residual 10.7 and 9.9).
-bool past_caches(const void* p, long long cols, long long ld, int bytes) {
-  return reinterpret_cast<uintptr_t>(p) % 128 == 0 && ld * bytes % 128 == 0 && cols * bytes % 128 == 0;
-}
-
 // Sizes and types of a norm: `type` 16 bits wide, x_type the same or fp32.
 void check_rows(Checker& c, int M, int N, int type) {
   c.fail_if(M < 0 || N < 0, "negative size");
@@ -116,8 +108,6 @@ int layer_norm_forward_impl(const igc_layer_norm_forward* d, hipStream_t stream)
   a.Q = d->Q;
   a.ldq = d->ldq;
   a.scale = d->Q ? d->scale : nullptr;
-  a.stream_y = past_caches(d->Y, d->N, d->ldy, 2);
-  a.stream_q = past_caches(d->Q, d->N, d->ldq, 1);
   using namespace igc_ffn;
   const int cus = device_cus(dev);
   const bool wide = d->x_type == IGC_F32;
@@ -149,7 +139,6 @@ int quantize_rows_impl(const igc_quantize_rows* d, hipStream_t stream) {
   a.Q = d->Q;
   a.ldq = d->ldq;
   a.scale = d->scale;
-  a.stream_q = past_caches(d->Q, d->N, d->ldq, 1);
   using namespace igc_ffn;
   if (d->type == IGC_BF16)
     launch_rows<false, T_BF16, T_BF16>(a, device_cus(dev), stream);
@@ -268,7 +257,6 @@ int layer_norm_backward_impl(const igc_layer_norm_backward* d, size_t* query, hi
   a.rows = pl.rows;
   a.groups = pl.groups;
   a.blocks = pl.blocks;
-  a.stream = past_caches(d->dX, d->N, d->lddx, elem(d->x_type));
   if (d->M > 0) {
     using namespace igc_ffn;
     const bool wide = d->x_type == IGC_F32;
@@ -319,7 +307,6 @@ int dropout_impl(const igc_dropout* d, hipStream_t stream) {
   a.drops = border != 0;
   a.last = (uint32_t)(border - 1);
   a.scale = border >> 32 ? 0.0f : (float)(0x1p32 / (double)((1ULL << 32) - border));
-  a.stream = past_caches(d->Y, d->N, d->ldy, elem(d->y_type));
   a.seed0 = (uint32_t)d->seed;
   a.seed1 = (uint32_t)(d->seed >> 32);
   a.offset = d->offset;
