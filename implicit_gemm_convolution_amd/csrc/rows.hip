@@ -42,10 +42,17 @@ void check_rows(Checker& c, int M, int N, int type) {
 // (so more rows at once in a compute unit's registers than with more chunks a
 // thread: 8192 x 4096 bf16 32.6 us with 512 threads, 36.0 with 256 and two chunks;
 // 8192 x 1024 10.4, and 14.6 by a wave with two).  Longer rows are read again in
-// every pass (2000 x 20000 54 us: 2.9 TB/s).
+// every pass (2048 x 20000 bf16 34 us: 4.8 TB/s; 2048 x 65536 148: 3.6).
 template <bool NORM, int XT, int OT>
 void launch_rows(const RowArgs& a, int cus, hipStream_t stream) {
-  auto groups = [&](int threads, int rows) { return dim3((unsigned)std::min(ceil_div(a.M, rows), 2048LL / threads * cus)); };
+  // Rows that are read again are two to a compute unit, but one where two are more
+  // than its share of an L2 (128 KB) and one is not (us, two and one: 2048 x 20000
+  // bf16 35.5 and 40.5, 1024 x 32768 32.1 and 35.0, 1024 x 40000 42.4 and 37.9, 512 x 65536
+  // 38.8 and 34.2, 256 x 262144 81.5 and 81.3; of 300 x 65536, less than two each, 23.9
+  // and 27.8; to 8 bits without a norm, read twice, 2048 x 65536 99 and 118).
+  const long long row_bytes = (long long)a.N * igc_rows::Raw<XT>::EB;
+  const bool one = NORM && a.N > 16384 && row_bytes > 64 * 1024 && row_bytes <= 128 * 1024 && a.M >= 2LL * cus;
+  auto groups = [&](int threads, int rows) { return dim3((unsigned)std::min(ceil_div(a.M, rows), (one ? 1024LL : 2048LL) / threads * cus)); };
 #define IGC_ROWS(threads, rows, ...) \
   hipLaunchKernelGGL((igc_rows::__VA_ARGS__), groups(threads, rows), dim3(threads), 0, stream, a)
   if constexpr (NORM) {
@@ -150,7 +157,7 @@ int quantize_rows_impl(const igc_quantize_rows* d, hipStream_t stream) {
 // ---------------------------------------------------------------- backward
 // How a backward pass splits its rows: registers hold rows of up to 8192
 // elements, a chunk a thread; longer ones go by columns, after a launch for
-// their means (2048 x 16384 bf16 77 us; two chunks a thread, which do not fit
+// their means (2048 x 16384 bf16 76 us; two chunks a thread, which do not fit
 // the registers of 1024 threads, 105).
 struct BackPlan {
   bool in_registers;
@@ -190,7 +197,8 @@ int launch_back(const NormBackArgs& a, const BackPlan& pl, int cus, hipStream_t 
     return launch_status();
   }
   if (a.dX) {
-    hipLaunchKernelGGL((igc_rows::norm_back_stats_kernel<XT, OT, 1024>), dim3((unsigned)std::min<long long>(a.M, 2LL * cus)), dim3(1024), 0,
+    // (three workgroups of 512 threads a compute unit; of 1024 threads with these registers one fits: 8192 x 12288 bf16 94 us, so 69)
+    hipLaunchKernelGGL((igc_rows::norm_back_stats_kernel<XT, OT, 512>), dim3((unsigned)std::min<long long>(a.M, 3LL * cus)), dim3(512), 0,
                        stream, a);
     if (int s = launch_status()) return s;
   }

@@ -96,6 +96,11 @@ int main() {
       I(M); I(N); I(type); I(x_type); P(dY); I(lddy); P(X); I(ldx); P(mean); P(rstd); P(gamma); P(R); I(ldr); P(dX); I(lddx); P(dgamma);
       P(dbeta); P(workspace); d.ws_bytes = f("ws_bytes");
       both(d, layer_norm_backward, layer_norm_backward_workspace_size);
+    } else if (entry == "layer_norm_forward") {
+      igc_layer_norm_forward d{};
+      I(M); I(N); I(type); I(x_type); P(X); I(ldx); P(Y); I(ldy); P(Q); I(ldq); P(scale);
+      const int s = layer_norm_forward(&d, nullptr);
+      std::printf("status %d query 0 need 0 %s\n", s, s ? g_error : "");
     } else {
       std::printf("unknown entry %s\n", entry.c_str());
       return 1;

@@ -390,3 +390,17 @@ def test_rows_past_32_bit_offsets(torch, igc, ws):  # noqa: F811
     igc.dropout(M, N, flat, ld, out, ld, 0.3, 5, R=flat, ldr=ld)
     igc.dropout(M, N, x, N, dx, N, 0.3, 5, R=x, ldr=N)
     assert torch.equal(outs, dx)
+
+
+@pytest.mark.parametrize("kind,x_kind", TYPES, ids=str)
+@pytest.mark.parametrize("N", [20001, 33001])
+def test_layer_norm_forward_of_many_long_rows(torch, igc, N, kind, x_kind):  # noqa: F811
+    """Rows that are read again, several to a workgroup, one and two workgroups to a compute unit."""
+    test_layer_norm_forward_of_many_rows(torch, igc, N, kind, x_kind)
+
+
+@pytest.mark.parametrize("kind,x_kind", TYPES, ids=str)
+@pytest.mark.parametrize("size", [(900, 8193, 1, 1), (1700, 8207, 0, 0), (800, 12290, 3, 1)], ids=str)
+def test_layer_norm_backward_of_many_long_rows(torch, igc, ws, size, kind, x_kind):  # noqa: F811
+    """Rows by columns, the next row and the next chunk on their way, with a last chunk of 1 to 7 elements."""
+    test_layer_norm_backward(torch, igc, ws, size, kind, x_kind)

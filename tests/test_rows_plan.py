@@ -125,3 +125,19 @@ def test_norm_backward_sizes(host, M, N):
     assert status == 0 and less == (0 if in_registers else -(-8 * M // 256) * 256)
     status, _, sums, _, launches = host("layer_norm_backward", **_back(M, N, dX=0))
     assert status == 0 and len(launches) == 2 and sums == need - less
+
+
+def _norm(M, N, **more):
+    f = dict(M=M, N=N, type=1, x_type=1, X=P, ldx=N, Y=P, ldy=N)
+    f.update(more)
+    return f
+
+
+def test_long_rows_share_the_caches(host):
+    """Workgroups that read their rows again: two to each of 256 compute units, one where two rows are too much for its share of a cache."""
+    for N, x_type, groups in ((20000, 1, 512), (32768, 1, 512), (32769, 1, 256), (65536, 1, 256), (65537, 1, 512), (16385, 2, 256), (32769, 2, 512),
+                              (2 ** 31 - 4096, 2, 512)):
+        status, _, _, _, launches = host("layer_norm_forward", **_norm(100000, N, x_type=x_type))
+        assert status == 0 and [l[1:] for l in launches] == [(groups, 1024)]
+    for M, groups in ((1, 1), (300, 300), (511, 511), (512, 256)):
+        assert [l[1:] for l in host("layer_norm_forward", **_norm(M, 40000))[4]] == [(groups, 1024)]
