@@ -55,14 +55,13 @@ void launch_rows(const RowArgs& a, int cus, hipStream_t stream) {
   auto groups = [&](int threads, int rows) { return dim3((unsigned)std::min(ceil_div(a.M, rows), (one ? 1024LL : 2048LL) / threads * cus)); };
 #define IGC_ROWS(threads, rows, ...) \
   hipLaunchKernelGGL((igc_rows::__VA_ARGS__), groups(threads, rows), dim3(threads), 0, stream, a)
-  if constexpr (NORM) {
-    // Many rows of fp32, or to 8 bits, are bound by instructions, and what a row
-    // takes of them in every thread is shared by two chunks (us, one chunk and
-    // two: 8192 x 4096 fp32 to bf16 41.8 and 37.6, 8192 x 8192 to 8 bits 61 and 55; 8192 x 4096
-    // bf16 to bf16 22.5 and 22.7, 1000 x 5001 fp32 to fp16 10.6 and 12.4).
-    if (a.N > 2048 && a.N <= 8192 && a.M >= 8LL * cus && (a.scale || XT == igc_ffn::T_F32)) {
-      if (a.N <= 4096) IGC_ROWS(256, 1, row_kernel<NORM, XT, OT, 256, 2>);
-      else IGC_ROWS(512, 1, row_kernel<NORM, XT, OT, 512, 2>);
+  if constexpr (NORM && XT == igc_ffn::T_F32) {
+    // Many rows of fp32 are bound by instructions, and what a row takes of them in
+    // every thread is shared by two chunks (us, one chunk and two: fp32 to bf16 of 8192
+    // x 4096 40.0 and 36.9, of 4096 x 4096 17.3 and 16.5, of 2100 x 4096 10.0 and 11.5, of 4000 x
+    // 8192 36.0 and 36.4; bf16 to 8 bits of 4096 x 4096 16.7 and 17.6, of 8192 x 8192 60 and 64).
+    if (a.N > 2048 && a.N <= 4096 && a.M >= 16LL * cus) {
+      IGC_ROWS(256, 1, row_kernel<NORM, XT, OT, 256, 2>);
       return;
     }
   }

@@ -404,3 +404,27 @@ def test_layer_norm_forward_of_many_long_rows(torch, igc, N, kind, x_kind):  # n
 def test_layer_norm_backward_of_many_long_rows(torch, igc, ws, size, kind, x_kind):  # noqa: F811
     """Rows by columns, the next row and the next chunk on their way, with a last chunk of 1 to 7 elements."""
     test_layer_norm_backward(torch, igc, ws, size, kind, x_kind)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("N", [2049, 2500, 4095, 4096])
+def test_layer_norm_forward_of_thousands_of_rows(torch, igc, N, kind):  # noqa: F811
+    """fp32 rows enough for two chunks a thread, with statistics, in 8 bits, and the same rows a few at a time."""
+    M, few = 4200, 300
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(N)
+    X = Mat(torch, M, N, "f32", N + 1, values=_stream(torch, gen, M, N))
+    gamma, beta = 1 + 0.3 * torch.randn(N, generator=gen, device="cuda"), torch.randn(N, generator=gen, device="cuda")
+    Y, Q = Mat(torch, M, N, kind, N + 3), Bytes(torch, M, N)
+    mean, rstd, s = (torch.empty(M, device="cuda") for _ in range(3))
+    kw = dict(gamma=gamma, beta=beta, eps=EPS, type=_type(igc, kind), x_type=igc.IGC_F32)
+    igc.layer_norm_forward(M, N, X.ptr, X.ld, Y.ptr, Y.ld, mean=mean, rstd=rstd, Q=Q.ptr, ldq=N, scale=s, **kw)
+    y, m, r, ey, em, er = _norm_reference(X.double(), gamma.double(), beta.double())
+    _check("Y", Y.t, y, ey + _store(kind, y.abs() + ey))
+    _check("mean", mean, m, em + U * m.abs())
+    _check("rstd", rstd, r, er)
+    q, scale = _exact_rows(Y.double())
+    assert torch.equal(Q.t.double(), q) and torch.equal(s, scale) and Q.others_untouched() and Y.others_untouched()
+    V = Mat(torch, few, N, kind)
+    igc.layer_norm_forward(few, N, X.ptr, X.ld, V.ptr, V.ld, **kw)
+    _check("Y of few", V.t, y[:few], (ey + _store(kind, y.abs() + ey))[:few])
