@@ -337,7 +337,8 @@ __device__ __forceinline__ void row_stats(float (&v)[C][8], int t, int n, float 
     __syncthreads();
     const float2 a = parts[t % W];  // (a lane for each wave's part)
     mean = wave_combine<W>(a.x * w.lane, add) * inv_n;
-    var = wave_combine<W>(__builtin_fmaf((a.x - mean) * (a.x - mean), w.lane, a.y), add) * inv_n;
+    const float d = w.lane > 0.0f ? a.x - mean : 0.0f;  // (a wave past the row has no mean: 0 of its squares may be 0 times infinity)
+    var = wave_combine<W>(__builtin_fmaf(d * d, w.lane, a.y), add) * inv_n;
   }
 }
 
