@@ -254,12 +254,26 @@ struct Quantizer {
 // ---------------------------------------------------------------------------
 // Forward: the norm, and rows in 8 bits.
 // ---------------------------------------------------------------------------
+// Division by a whole number: with 1 / n in two parts the quotient is the nearest
+// number.  (By the first part alone it may be the one next to an exact quotient: a
+// row of 41 times 60000 has 59999.996 as its mean then, which eps = 1e-5 turns into
+// values of 0.7.)
+struct Divisor {
+  float inv, rest;
+  __host__ __device__ static Divisor by(int n) {
+    const float f = (float)n, inv = n > 0 ? 1.0f / f : 0.0f;
+    return Divisor{inv, n > 0 ? __builtin_fmaf(-inv, f, 1.0f) * inv : 0.0f};
+  }
+  __device__ __forceinline__ float of(float s) const { return __builtin_fmaf(s, inv, s * rest); }
+};
+
 struct RowArgs {
   long long M;
   int N;
   const uint8_t* X;
   long long ldx;  // elements, as all of them
-  float inv_n, eps;
+  Divisor n;
+  float eps;
   const float *gamma, *beta;  // or NULL: 1, 0
   uint8_t* Y;                 // or NULL
   long long ldy;
@@ -276,10 +290,11 @@ __device__ __forceinline__ float rsqrt_of(float v) {
   return v < 0x1p-100f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
 }
 
-// What does not change from row to row: one over the number of elements that this
-// thread's wave holds, and how many the wave holds whose part this lane takes.
+// What does not change from row to row: the number of elements that this thread's
+// wave holds, and how many the wave holds whose part this lane takes.
 struct WaveShare {
-  float inv_own = 0.0f, lane = 0.0f;
+  Divisor own{};
+  float lane = 0.0f;
   template <int T, int C>
   __device__ __forceinline__ static WaveShare of(int t, int n) {
     WaveShare r;
@@ -287,11 +302,11 @@ struct WaveShare {
       int k = 0;
 #pragma unroll
       for (int j = 0; j < C; ++j) k += min(max(n - (j * T + w * 64) * 8, 0), 512);
-      return (float)k;
+      return k;
     };
     if constexpr (T > 64) {
-      r.inv_own = 1.0f / fmaxf(held(t >> 6), 1.0f);
-      r.lane = held(t % (T / 64));
+      r.own = Divisor::by(__builtin_amdgcn_readfirstlane(held(t >> 6)));
+      r.lane = (float)held(t % (T / 64));
     }
     return r;
   }
@@ -299,10 +314,12 @@ struct WaveShare {
 // Mean and variance of a row in its threads' registers, with one barrier: every
 // wave takes the mean of its own elements and their squared distances from it,
 // and the waves' parts join as M2 = sum of M2_w + n_w (mean_w - mean)^2: no
-// difference of large squares anywhere.  (With a barrier for the mean and one for
-// the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
+// difference of large squares anywhere.  Rows of one 16-bit value have it as their
+// mean: sums of 11 bits over up to 8192 elements are exact, and of longer rows the
+// means' distances from the first one are summed.  (With a barrier for the mean and
+// one for the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
 template <int T, int C>
-__device__ __forceinline__ void row_stats(float (&v)[C][8], int t, int n, float inv_n, const WaveShare& w, float2* parts, float& mean,
+__device__ __forceinline__ void row_stats(float (&v)[C][8], int t, int n, const Divisor& by, const WaveShare& w, float2* parts, float& mean,
                                           float& var) {
   constexpr int WT = T < 64 ? T : 64, W = T / 64;
   auto add = [](float a, float b) { return a + b; };
@@ -312,7 +329,7 @@ __device__ __forceinline__ void row_stats(float (&v)[C][8], int t, int n, float 
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += v[j][e];  // (zeros past the row)
   s = wave_combine<WT>(s, add);
-  const float m = s * (T <= 64 ? inv_n : w.inv_own);
+  const float m = T <= 64 ? by.of(s) : w.own.of(s);
   float d2 = 0.0f;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
@@ -331,14 +348,20 @@ __device__ __forceinline__ void row_stats(float (&v)[C][8], int t, int n, float 
   d2 = wave_combine<WT>(d2, add);
   if constexpr (T <= 64) {
     mean = m;
-    var = d2 * inv_n;
+    var = d2 * by.inv;
   } else {
     if ((t & 63) == 0) parts[t >> 6] = make_float2(m, d2);
     __syncthreads();
     const float2 a = parts[t % W];  // (a lane for each wave's part)
-    mean = wave_combine<W>(a.x * w.lane, add) * inv_n;
-    const float d = w.lane > 0.0f ? a.x - mean : 0.0f;  // (a wave past the row has no mean: 0 of its squares may be 0 times infinity)
-    var = wave_combine<W>(__builtin_fmaf(d * d, w.lane, a.y), add) * inv_n;
+    if constexpr (C > 1) {
+      const float first = parts[0].x;
+      mean = first + wave_combine<W>((a.x - first) * w.lane, add) * by.inv;
+    } else {
+      mean = by.of(wave_combine<W>(a.x * w.lane, add));
+    }
+    // (a wave past the row has no mean: 0 of its squares may be 0 times infinity.  Rows by two waves, or by two chunks a thread, leave none.)
+    const float d = W > 2 && C == 1 && w.lane == 0.0f ? 0.0f : a.x - mean;
+    var = wave_combine<W>(__builtin_fmaf(d * d, w.lane, a.y), add) * by.inv;
   }
 }
 
@@ -397,7 +420,7 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : T == 128 || (XT ==
         }
       if (row + step < p.M) load(row + step);
       float mean, var;
-      row_stats<T, C>(v, t, p.N, p.inv_n, share, parts[turn][rg], mean, var);
+      row_stats<T, C>(v, t, p.N, p.n, share, parts[turn][rg], mean, var);
       const float rstd = rsqrt_of(var + p.eps);
       if (in && t == 0 && p.mean) p.mean[row] = mean;
       if (in && t == 0 && p.rstd) p.rstd[row] = rstd;
@@ -440,7 +463,7 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : T == 128 || (XT ==
 template <bool NORM, int XT, int OT, int T>
 __global__ void __launch_bounds__(T, 8) long_row_kernel(const RowArgs p) {
   constexpr int W = T / 64;
-  __shared__ float sums[2][W][1];
+  __shared__ float sums[W][1], squares[W][2];
   __shared__ uint32_t tops[2][W][1];
   int turn = 0;
   for (long long row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
@@ -464,16 +487,23 @@ __global__ void __launch_bounds__(T, 8) long_row_kernel(const RowArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v[e];  // (zeros past the row)
       });
-      mean = row_sum<T>(s, sums[0]) * p.inv_n;
-      s = 0.0f;
+      mean = p.n.of(row_sum<T>(s, sums));
+      // The mean is off by the rounding of so many additions: by the mean of the
+      // distances from it, which is added to it and whose square goes out of theirs.
+      float m[2] = {0.0f, 0.0f};
       chunks([&](const float(&v)[8], int, int n) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float d = e < n ? v[e] - mean : 0.0f;
-          s = __builtin_fmaf(d, d, s);
+          m[0] += d;
+          m[1] = __builtin_fmaf(d, d, m[1]);
         }
       });
-      rstd = rsqrt_of(row_sum<T>(s, sums[1]) * p.inv_n + p.eps);
+      row_combine<T, 2>(m, squares, [](float f, float g) { return f + g; });
+      const float off = m[0] * p.n.inv, around = m[1] * p.n.inv, least = around - off * off;
+      mean += off;
+      const float var = around < __builtin_inff() ? (least < 0.0f ? 0.0f : least) : around;
+      rstd = rsqrt_of(var + p.eps);
       if (threadIdx.x == 0 && p.mean) p.mean[row] = mean;
       if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
     }

@@ -103,7 +103,7 @@ int layer_norm_forward_impl(const igc_layer_norm_forward* d, hipStream_t stream)
   a.N = d->N;
   a.X = static_cast<const uint8_t*>(d->X);
   a.ldx = d->ldx;
-  a.inv_n = d->N ? 1.0f / (float)d->N : 0.0f;
+  a.n = igc_rows::Divisor::by(d->N);
   a.eps = d->eps;
   a.gamma = d->gamma;
   a.beta = d->beta;

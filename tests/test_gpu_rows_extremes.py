@@ -37,3 +37,29 @@ def test_layer_norm_forward_far_from_zero(torch, igc, N, x_kind):  # noqa: F811
     _check("Y", Y.t, y, ey + _store("bf16", y.abs() + ey))
     q, scale = _exact_rows(Y.double())
     assert torch.equal(Q.t.double(), q) and torch.equal(s, scale) and Y.others_untouched() and Q.others_untouched()
+
+
+@pytest.mark.parametrize("kind,x_kind", [("f16", "f16"), ("bf16", "bf16"), ("f16", "f32"), ("bf16", "f32")], ids=str)
+@pytest.mark.parametrize("N", [1, 7, 41, 47, 123, 500, 511, 513, 1001, 1025, 1100, 2049, 3000, 4095, 5003, 6144, 8191, 9001, 12345, 16383, 20001, 40000,
+                               70001])
+def test_layer_norm_of_rows_of_one_value(torch, igc, N, kind, x_kind):  # noqa: F811
+    """The value is the mean, and Y is beta: a last place of 60000 by eps^-1/2 would be more than 1."""
+    values = [60000.0, -65504.0, 3.0, 0.1, 1023.5, 2.0 ** -14, 5 * 2.0 ** -24] if kind == "f16" else \
+        [60000.0, 2.0 ** 65, 2.0 ** 66, -2.0 ** 100, 0.1, 1.0078125, 200.0, 3e33]
+    c = torch.tensor(values, device="cuda").to(getattr(torch, {"f16": "float16", "bf16": "bfloat16"}[kind])).float()
+    M = len(values)
+    X = Mat(torch, M, N, x_kind, values=c[:, None].expand(M, N))
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(N)
+    gamma, beta = 1 + 0.3 * torch.randn(N, generator=gen, device="cuda"), torch.randn(N, generator=gen, device="cuda")
+    Y = Mat(torch, M, N, kind)
+    mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    igc.layer_norm_forward(M, N, X.ptr, X.ld, Y.ptr, Y.ld, gamma=gamma, beta=beta, mean=mean, rstd=rstd,
+                           type=igc.IGC_F16 if kind == "f16" else igc.IGC_BF16, x_type={"f32": igc.IGC_F32, "f16": igc.IGC_F16, "bf16": igc.IGC_BF16}[x_kind])
+    assert torch.equal(mean, c), (mean - c).tolist()
+    assert torch.equal(Y.t, beta.to(Y.t.dtype).expand(M, N))
+    # sums of one 16-bit value (11 bits) over up to 8192 elements are exact, and the variance 0; past the registers the first
+    # mean is off by up to 4 last places, and (N / 8192 + 1) 8 + 12 additions, one after the other, leave 2^-24 each of their square
+    off = (4 * 2.0 ** -23 * c.double()) ** 2 * ((N // 8192 + 1) * 8 + 12) * 2.0 ** -24 if N > 16384 else 0.0 * c.double()
+    ref = (off * 0 + 1e-5) ** -0.5
+    assert bool(((rstd.double() / ref - 1).abs() <= 2.0 ** -22 + off / 1e-5).all()), (rstd / ref).tolist()
