@@ -459,6 +459,11 @@ __global__ void __launch_bounds__(row_threads<T>, C > 1 ? 4 : T == 128 || (XT ==
   }
 }
 
+// Elements that a thread adds one after the other in fp32: of longer rows these
+// sums are added in fp64 (2^18 additions of 40.1 in fp32 alone would be off by one
+// in a thousand, each of them rounded the same way).
+constexpr uint32_t SEGMENT = 512;
+
 // Rows that registers do not hold: read again in every pass.
 template <bool NORM, int XT, int OT, int T>
 __global__ void __launch_bounds__(T, 8) long_row_kernel(const RowArgs p) {
@@ -468,9 +473,10 @@ __global__ void __launch_bounds__(T, 8) long_row_kernel(const RowArgs p) {
   int turn = 0;
   for (long long row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
     const uint8_t* const x = p.X + row * p.ldx * Raw<XT>::EB;
-    // f(chunk of 8, its first column, how many of its columns are in the row)
-    auto chunks = [&](auto&& f) {
-      for (uint32_t u = threadIdx.x * 8; u < (uint32_t)p.N; u += T * 8) {  // (steps past 2^31 at most once)
+    // f(chunk of 8, its first column, how many of its columns are in the row) for this
+    // thread's chunks from column u to column `end`; the next one's column
+    auto chunks = [&](uint32_t u, uint32_t end, auto&& f) {
+      for (; u < end; u += T * 8) {  // (steps past 2^31 at most once)
         const int c = (int)u;
         float v[8];
         Raw<XT> raw;
@@ -479,22 +485,42 @@ __global__ void __launch_bounds__(T, 8) long_row_kernel(const RowArgs p) {
         raw.get(v);
         f(v, c, min(p.N - c, 8));
       }
+      return u;
     };
+    // K sums over the row: f as above adds to sums[K].
+    auto sum = [&](auto& sums, auto&& f) {
+      constexpr int K = sizeof(sums) / sizeof(float);
+      double total[K] = {};
+      for (uint32_t u = threadIdx.x * 8; u < (uint32_t)p.N;) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) sums[i] = 0.0f;
+        u = chunks(u, (uint32_t)min((long long)p.N, (long long)u + SEGMENT * T), f);
+#pragma unroll
+        for (int i = 0; i < K; ++i) total[i] += (double)sums[i];
+      }
+#pragma unroll
+      for (int i = 0; i < K; ++i) sums[i] = (float)total[i];
+    };
+    auto all = [&](auto&& f) { chunks(threadIdx.x * 8, (uint32_t)p.N, f); };
     float mean = 0.0f, rstd = 1.0f;
     if constexpr (NORM) {
-      float s = 0.0f;
-      chunks([&](const float(&v)[8], int, int) {
+      float s[1];
+      sum(s, [&](const float(&v)[8], int, int) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[e];  // (zeros past the row)
+        for (int e = 0; e < 8; ++e) s[0] += v[e];  // (zeros past the row)
       });
-      mean = p.n.of(row_sum<T>(s, sums));
+      mean = p.n.of(row_sum<T>(s[0], sums));
       // The mean is off by the rounding of so many additions: by the mean of the
       // distances from it, which is added to it and whose square goes out of theirs.
-      float m[2] = {0.0f, 0.0f};
-      chunks([&](const float(&v)[8], int, int n) {
+      float m[2];
+      sum(m, [&](float(&v)[8], int, int n) {
+        if (n < 8) {  // (nothing past the row)
+#pragma unroll
+          for (int e = 1; e < 8; ++e) v[e] = e < n ? v[e] : mean;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float d = e < n ? v[e] - mean : 0.0f;
+          const float d = v[e] - mean;
           m[0] += d;
           m[1] = __builtin_fmaf(d, d, m[1]);
         }
@@ -526,7 +552,7 @@ __global__ void __launch_bounds__(T, 8) long_row_kernel(const RowArgs p) {
     };
     uint32_t top = 0;
     if (!NORM || p.Y || p.scale) {
-      chunks([&](float(&v)[8], int c, int n) {
+      all([&](float(&v)[8], int c, int n) {
         Raw<OT> out = normed(v, c, n);
         if (p.Y) out.store(p.Y + row * p.ldy * Raw<OT>::EB, c, p.N);
         if (n < 8) out.clear_from(n);
@@ -537,7 +563,7 @@ __global__ void __launch_bounds__(T, 8) long_row_kernel(const RowArgs p) {
       top = row_max<T>(top, tops[turn]);
       const Quantizer q = Quantizer::of<OT>(top);
       if (threadIdx.x == 0) p.scale[row] = Quantizer::scale<OT>(top);
-      chunks([&](float(&v)[8], int c, int n) {
+      all([&](float(&v)[8], int c, int n) {
         normed(v, c, n);
         q.store(p.Q + row * p.ldq + c, n, v);
       });
@@ -694,8 +720,17 @@ __global__ void __launch_bounds__(T) norm_back_stats_kernel(const NormBackArgs p
   int turn = 0;
   for (long long row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
     float m[2] = {0.0f, 0.0f};
-    for (uint32_t u = t * 8; u < (uint32_t)p.N; u += T * 8) {
+    double total[2] = {0.0, 0.0};
+    for (uint32_t u = t * 8, turns = 0; u < (uint32_t)p.N; u += T * 8, ++turns) {
       const int c = (int)u, n = p.N - c;
+      if (turns == SEGMENT / 8) {
+        turns = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          total[i] += (double)m[i];
+          m[i] = 0.0f;
+        }
+      }
       const float mean = next_mean, rstd = next_rstd;
       float d[8], v[8], g[8];
       dy.settle(c, p.N);
@@ -724,6 +759,8 @@ __global__ void __launch_bounds__(T) norm_back_stats_kernel(const NormBackArgs p
         m[1] = __builtin_fmaf(d[e], (v[e] - mean) * rstd, m[1]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m[i] = (float)(total[i] + (double)m[i]);
     row_combine<T, 2>(m, sums[turn], [](float f, float g) { return f + g; });
     if (t == 0) p.stats[row] = make_float2(m[0] * p.inv_n, m[1] * p.inv_n);
   }

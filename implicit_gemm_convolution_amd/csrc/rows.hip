@@ -162,6 +162,10 @@ struct BackPlan {
   bool in_registers;
   int rows, groups, blocks;  // rows at a time (a block, by columns); workgroups
 };
+// Rows that a thread adds one after the other: more of them get more blocks, so that
+// no sum takes so many fp32 additions that their roundings show (2^17 rows to a
+// thread, of 0.1: off by two in a thousand).
+constexpr long long MOST_ROWS = 4096;
 BackPlan plan_back(long long M, int N, int cus) {
   BackPlan b;
   b.in_registers = N <= 8192;
@@ -170,11 +174,12 @@ BackPlan plan_back(long long M, int N, int cus) {
     while (threads * 8 < N) threads *= 2;
     b.rows = 1024 / threads;
     b.groups = 1;
-    b.blocks = (int)std::min(ceil_div(M, b.rows), (long long)cus);
+    b.blocks = (int)std::min(ceil_div(M, b.rows), std::max((long long)cus, ceil_div(M, b.rows * MOST_ROWS)));
   } else {
     // enough workgroups to fill the card, and few enough that their sums stay small beside the rows
     b.groups = (int)ceil_div(N, 512);
-    b.rows = (int)std::max(16LL, ceil_div(M, std::max(1LL, 4LL * cus / b.groups)));
+    b.rows = (int)std::min(std::max(16LL, ceil_div(M, std::max(1LL, 4LL * cus / b.groups))), 4 * MOST_ROWS);
+    b.rows = (int)std::max<long long>(b.rows, ceil_div(M, std::max(1LL, 0x7fffffLL / b.groups)));
     b.blocks = (int)ceil_div(M, b.rows);
   }
   return b;

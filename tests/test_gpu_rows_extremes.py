@@ -63,3 +63,59 @@ def test_layer_norm_of_rows_of_one_value(torch, igc, N, kind, x_kind):  # noqa: 
     off = (4 * 2.0 ** -23 * c.double()) ** 2 * ((N // 8192 + 1) * 8 + 12) * 2.0 ** -24 if N > 16384 else 0.0 * c.double()
     ref = (off * 0 + 1e-5) ** -0.5
     assert bool(((rstd.double() / ref - 1).abs() <= 2.0 ** -22 + off / 1e-5).all()), (rstd / ref).tolist()
+
+
+# Additions one after the other in a sum over a row past the registers: 512 of a thread, then fp64 sums of those, and
+# 12 across the threads
+DEPTH = 512 + 12
+
+
+@pytest.mark.parametrize("x_kind", ["f32", "f16"])
+@pytest.mark.parametrize("N", [2 ** 20 + 3, 2 ** 24 + 5])
+def test_norm_of_rows_of_millions(torch, igc, ws, N, x_kind):  # noqa: F811
+    """Distances far smaller than the mean, gradients of one value: what roundings of the same sign would hide."""
+    U, M = 2.0 ** -24, 2
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(N)
+    noise = torch.randn(M, N, generator=gen, device="cuda")
+    X = Mat(torch, M, N, x_kind, values=40.1 + (1e-3 if x_kind == "f32" else 0.1) * noise)
+    del noise
+    Y, mean, rstd = Mat(torch, M, N, "f16"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    kw = dict(type=igc.IGC_F16, x_type=igc.IGC_F32 if x_kind == "f32" else igc.IGC_F16)
+    igc.layer_norm_forward(M, N, X.ptr, N, Y.ptr, N, mean=mean, rstd=rstd, eps=0.0, **kw)
+    x = X.double()
+    m = x.mean(1, keepdim=True)
+    d = x - m
+    var = (d * d).mean(1, keepdim=True)
+    r = var ** -0.5
+    first = (DEPTH + 3) * U * x.abs().mean(1, keepdim=True)                            # the first mean
+    em = (DEPTH + 4) * U * (d.abs().mean(1, keepdim=True) + first) + 2 * U * m.abs()  # with that of the distances from it
+    # the squares of distances from the first mean less that of its own distance, and theirs by the last mean's error
+    evar = (DEPTH + 12) * U * (var + 2 * first * first) + 2 * first * em
+    er = r * (0.6 * evar / var + 4 * U)
+    ey = 1.1 * ((r + er) * (em + U * d.abs()) + d.abs() * er + 4 * U * d.abs() * r)
+    assert float((em * r).max()) < 0.02 and float((er / r).max()) < 0.02  # (x itself is within 2e-6 of 1e-3)
+    _check("mean", mean, m[:, 0], em[:, 0])
+    _check("rstd", rstd, r[:, 0], er[:, 0])
+    _check("Y", Y.t, d * r, ey + _store("f16", (d * r).abs() + ey))
+    # the backward pass from given statistics; every g the same number, whose sums' last places round one way
+    xh = x = None
+    mean, rstd = m[:, 0].float(), r[:, 0].float()
+    c = 1637 * 2.0 ** -14
+    dY, dX = torch.full((M, N), c, dtype=torch.float16, device="cuda"), Mat(torch, M, N, x_kind)
+    igc.layer_norm_backward(M, N, dY, N, X.ptr, N, mean, rstd, dX=dX.ptr, lddx=N, workspace=ws, **kw)
+    xh = (X.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    mgx = (c * xh).mean(1, keepdim=True)
+    want = rstd.double()[:, None] * (c - c - xh * mgx)
+    size = (c * xh.abs()).mean(1, keepdim=True)
+    ed = 1.1 * rstd.double()[:, None] * ((DEPTH + 3) * U * c + xh.abs() * (DEPTH + 6) * U * size + 6 * U * (2 * c + (xh * mgx).abs()))
+    _check("dX", dX.t, want, ed + _store(x_kind, want.abs() + ed))
+
+
+def test_column_sums_of_very_many_rows(torch, igc, ws):  # noqa: F811
+    """2^31 rows of one gradient: 4096 additions in a thread, 2048 of workgroups' sums and a few more."""
+    M, c = 2 ** 31 - 4096, 1637 * 2.0 ** -14
+    dY, zeros = torch.full((M,), c, dtype=torch.float16, device="cuda"), torch.zeros(M, device="cuda")
+    dgamma, dbeta = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    igc.layer_norm_backward(M, 1, dY, 1, dY, 1, zeros, zeros, dgamma=dgamma, dbeta=dbeta, type=igc.IGC_F16, workspace=ws)
+    assert abs(float(dbeta) / (M * c) - 1) <= (4096 + 2048 + 80) * 2.0 ** -24 and float(dgamma) == 0.0
