@@ -84,7 +84,7 @@ int layer_norm_forward_impl(const igc_layer_norm_forward* d, hipStream_t stream)
   check_rows(c, d->M, d->N, d->type);
   c.fail_if(d->x_type != d->type && d->x_type != IGC_F32, "x_type must be `type` or IGC_F32");
   c.fail_if(!(d->eps >= 0.0f) || std::isinf(d->eps), "eps must be a finite number, not negative");
-  c.fail_if(!d->Y && !d->Q && !d->mean && !d->rstd && d->M > 0, "no output requested");
+  c.fail_if(!d->Y && !d->Q && !d->mean && !d->rstd && d->M > 0 && d->N > 0, "no output requested");  // (matrices of nothing may be NULL)
   c.matrix("X", d->X, d->ldx, d->M, d->N, elem(d->x_type), false);
   c.matrix("Y", d->Y, d->ldy, d->M, d->N, 2, true);
   c.matrix("Q", d->Q, d->ldq, d->M, d->N, 1, true);
@@ -113,7 +113,7 @@ int layer_norm_forward_impl(const igc_layer_norm_forward* d, hipStream_t stream)
   a.rstd = d->rstd;
   a.Q = d->Q;
   a.ldq = d->ldq;
-  a.scale = d->Q ? d->scale : nullptr;
+  a.scale = d->Q || d->N == 0 ? d->scale : nullptr;
   using namespace igc_ffn;
   const int cus = device_cus(dev);
   const bool wide = d->x_type == IGC_F32;
@@ -216,7 +216,7 @@ int layer_norm_backward_impl(const igc_layer_norm_backward* d, size_t* query, hi
   if (!c.ok()) return c.status;
   check_rows(c, d->M, d->N, d->type);
   c.fail_if(d->x_type != d->type && d->x_type != IGC_F32, "x_type must be `type` or IGC_F32");
-  c.fail_if(!d->dX && !d->dgamma && !d->dbeta, "no output requested");
+  c.fail_if(!d->dX && !d->dgamma && !d->dbeta && d->M > 0 && d->N > 0, "no output requested");
   c.matrix("dY", d->dY, d->lddy, d->M, d->N, 2, false);
   c.matrix("X", d->X, d->ldx, d->M, d->N, elem(d->x_type), false);
   c.fail_if(d->M > 0 && d->N > 0 && (!d->mean || !d->rstd), "mean or rstd is NULL");

@@ -119,3 +119,24 @@ def test_column_sums_of_very_many_rows(torch, igc, ws):  # noqa: F811
     dgamma, dbeta = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
     igc.layer_norm_backward(M, 1, dY, 1, dY, 1, zeros, zeros, dgamma=dgamma, dbeta=dbeta, type=igc.IGC_F16, workspace=ws)
     assert abs(float(dbeta) / (M * c) - 1) <= (4096 + 2048 + 80) * 2.0 ** -24 and float(dgamma) == 0.0
+
+
+def test_rows_without_elements_as_torch_gives_them(torch, igc, ws):  # noqa: F811
+    """Empty tensors have no address: the vectors of the rows are set all the same."""
+    M = 5
+    x, q = torch.empty(M, 0, dtype=torch.bfloat16, device="cuda"), torch.empty(M, 0, dtype=torch.int8, device="cuda")
+    mean, rstd, scale = (torch.full((M,), float("nan"), device="cuda") for _ in range(3))
+    assert x.data_ptr() == 0
+    igc.layer_norm_forward(M, 0, x, 0, x, 0, eps=0.25)
+    igc.layer_norm_forward(M, 0, x, 0, x, 0, eps=0.25, mean=mean, rstd=rstd, Q=q, ldq=0, scale=scale)
+    assert mean.tolist() == [0.0] * M and rstd.tolist() == [2.0] * M and scale.tolist() == [0.0] * M
+    scale.fill_(float("nan"))
+    igc.quantize_rows(M, 0, x, 0, q, 0, scale)
+    assert scale.tolist() == [0.0] * M
+    igc.layer_norm_backward(M, 0, x, 0, x, 0, mean, rstd, dX=x, lddx=0, workspace=ws)
+    none = torch.empty(0, 7, dtype=torch.bfloat16, device="cuda")
+    igc.layer_norm_forward(0, 7, none, 7, none, 7)
+    igc.layer_norm_backward(0, 7, none, 7, none, 7, None, None, dX=none, lddx=7, workspace=ws)
+    dgamma = torch.full((7,), float("nan"), device="cuda")
+    igc.layer_norm_backward(0, 7, none, 7, none, 7, None, None, dX=none, lddx=7, dgamma=dgamma, workspace=ws)
+    assert not bool(dgamma.any())
