@@ -392,9 +392,10 @@ def conv2d_u8i8_zp(Nb, H, W, C, Kout, R, S, stride_h, stride_w, pad_h, pad_w, x,
 # arguments (but for workspace and stream) and returns the bytes that the
 # call needs.
 # ---------------------------------------------------------------------------
-_native = None   # the _marshal module; False without torch
-_entries = None  # (the library, addresses of its entry points)
-_bound = {}      # _marshal's calls of them
+_native = None     # the _marshal module; False without torch
+_entries = None    # (the library, addresses of its entry points)
+_bound = {}        # _marshal's calls of them
+_bound_lib = None  # the library that these are of
 
 
 def _marshal():
@@ -448,12 +449,23 @@ def _describe(name, fields, workspace, ws_bytes):
     return _DESCRIPTORS[name](*values)
 
 
+def _bind(native, name):
+    """_marshal's call of an entry point of the library that is loaded now."""
+    global _bound_lib
+    f = native.bind(_entry(name), _FORMATS[name])
+    if _bound_lib is not _lib:
+        _bound.clear()
+        _bound_lib = _lib
+    _bound[name] = f
+    return f
+
+
 def _call(name, check, stream, workspace, ws_bytes, *fields) -> int:
     native = _native if _native is not None else _marshal()
     if native:
-        f = _bound.get(name)
+        f = _bound.get(name) if _bound_lib is _lib else None
         if f is None:
-            f = _bound[name] = native.bind(_entry(name), _FORMATS[name])
+            f = _bind(native, name)
         st = f(_stream(stream), workspace, ws_bytes, *fields)
     else:
         st = getattr(load(), name)(_describe(name, fields, workspace, ws_bytes), _stream(stream))
