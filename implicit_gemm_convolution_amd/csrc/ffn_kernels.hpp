@@ -954,9 +954,9 @@ struct ByteOperand {
 // first: 64 x 64 sums (the gated block: of each product) a workgroup, K tiles
 // through registers, DEPTH of them on their way, into two LDS stages.  What is
 // left of the reduction past the last whole tile comes first, so the loop has
-// whole tiles alone; it turns a multiple of DEPTH times without a branch, which
-// keeps the compiler's waits at the oldest loads, and the turns past the last
-// tile multiply by zeros.
+// whole tiles alone; it turns a multiple of DEPTH times without a branch, so that
+// the compiler's waits are for older loads and leave the youngest tile's on their
+// way, and the turns past the last tile multiply by zeros.
 template <bool BF, int MODE, int DEPTH>
 __global__ void __launch_bounds__(256) i8_any_kernel(const I8Args p) {
   constexpr bool GLU = is_glu(MODE);
