@@ -89,6 +89,9 @@ int product_i8(I8Args& a, int type, void* ws, size_t ws_bytes, size_t* query, hi
   Pads pads;
   Plan pl;
   int ia = -1, ib = -1, ib2 = -1;
+  // (Plans of aligned operands go by the times of 16-bit products whose rows have as
+  // many bytes: over 175 shapes 1.3% slower than the best plan in the mean, but with M <= 24 and
+  // N = 11008 by 14 to 38%, weights partly in the memory-side cache.)
   if (align == 16) {
     pl = make_plan(AS, a.M, a.N, units, 16, cus, true);
   } else {

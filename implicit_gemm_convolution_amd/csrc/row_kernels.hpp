@@ -34,11 +34,12 @@ using igc_ffn::unpack8;
 // the load the shift would wait for the data, and the workgroup's other waves for
 // that one at the next barrier (backward of 8192 x 4095 bf16 73 us, so 54; rows in 8
 // bits of 8192 x 4097 25, so 22).
-// Whole chunks are written past the caches, wherever they lie (us, in the caches
-// and past them: norm of 8192 x 4096 bf16 32.7 and 26.7, of 1000 x 4096 9.1 and 7.8, and
-// in its form of now, 8192 x 4095 35 and 26.6, 2048 x 20001 63 and 52; rows in 8 bits of
-// 8192 x 4097 33 and 25; the backward pass of 8192 x 4095 75 and 73; dropout of 8192 x
-// 8191 from -3 to +3%).
+// Whole chunks are written past the caches, wherever they lie.  In the caches and
+// past them, us, each in the form that its kernel had when this was tried: norm of
+// 8192 x 4096 bf16 32.7 and 26.7 (22 now), of 1000 x 4096 9.1 and 7.8 (5.6 now), of 8192 x
+// 4095 35 and 26.6, of 2048 x 20001 63 and 52; rows in 8 bits of 8192 x 4097 33 and 25
+// (22 now); the backward pass of 8192 x 4095 75 and 73 (54 now); dropout of 8192 x 8191
+// from -3 to +3%.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -317,7 +318,8 @@ struct WaveShare {
 // difference of large squares anywhere.  Rows of one 16-bit value have it as their
 // mean: sums of 11 bits over up to 8192 elements are exact, and of longer rows the
 // means' distances from the first one are summed.  (With a barrier for the mean and
-// one for the distances from it 8192 x 4096 bf16 takes 26.7 us, so 24.2.)
+// one for the distances from it 8192 x 4096 bf16 took 26.7 us, so 24.2, and 22.3 with
+// what came after.)
 template <int T, int C>
 __device__ __forceinline__ void row_stats(float (&v)[C][8], int t, int n, const Divisor& by, const WaveShare& w, float2* parts, float& mean,
                                           float& var) {
@@ -593,8 +595,8 @@ struct NormBackArgs {
 // rows at a time, one reduction of two sums a row, and the sums down the rows
 // in the registers of the threads that hold their columns.  Each input is read
 // once.  The next row is on its way while this one is summed.  (8192 x 4096 bf16
-// with a residual 43 us, 6.2 TB/s, and 4.5 for the second launch; two launches that read dY
-// and X twice 75.)
+// with a residual 49 us, 5.4 TB/s, and 4.5 for the second launch; two launches that read
+// dY and X twice 75.)
 template <int XT, int OT, int T>
 __global__ void __launch_bounds__(1024) norm_back_rows_kernel(const NormBackArgs p) {
   constexpr int RG = 1024 / T, W = T < 64 ? 1 : T / 64, COLS = T * 8;

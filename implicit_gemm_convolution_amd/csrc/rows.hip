@@ -42,11 +42,11 @@ void check_rows(Checker& c, int M, int N, int type) {
 // (so more rows at once in a compute unit's registers than with more chunks a
 // thread: 8192 x 4096 bf16 32.6 us with 512 threads, 36.0 with 256 and two chunks;
 // 8192 x 1024 10.4, and 14.6 by a wave with two).  Longer rows are read again in
-// every pass (2048 x 20000 bf16 34 us: 4.8 TB/s; 2048 x 65536 148: 3.6).
+// every pass (2048 x 20000 bf16 39 to 41 us: 4.1 TB/s; 2048 x 65536 168: 3.2).
 template <bool NORM, int XT, int OT>
 void launch_rows(const RowArgs& a, int cus, hipStream_t stream) {
   // Rows that are read again are two to a compute unit, but one where two are more
-  // than its share of an L2 (128 KB) and one is not (us, two and one: 2048 x 20000
+  // than its share of an L2 (128 KB) and one is not (us, two and one, when it was chosen: 2048 x 20000
   // bf16 35.5 and 40.5, 1024 x 32768 32.1 and 35.0, 1024 x 40000 42.4 and 37.9, 512 x 65536
   // 38.8 and 34.2, 256 x 262144 81.5 and 81.3; of 300 x 65536, less than two each, 23.9
   // and 27.8; to 8 bits without a norm, read twice, 2048 x 65536 99 and 118).

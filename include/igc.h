@@ -543,7 +543,8 @@ int grad_clip_workspace_size(const igc_grad_clip* d, size_t* bytes);
  * and each channel.
  *
  * The conventions of the feed-forward operators hold, but for these:
- *  - Calls without a workspace in their descriptor need none.
+ *  - Calls without a workspace in their descriptor need none; the others need
+ *    theirs where its size is not 0, the products in 8 bits too.
  *  - M and N (and K) go up to 2^31 - 4096; the K of the 8-bit products up to 131071
  *    (128 * 128 * K has to fit in int32; IGC_EOVERFLOW beyond).
  *  - Any leading dimension and any alignment that the element type allows. 16-byte
@@ -560,10 +561,14 @@ int grad_clip_workspace_size(const igc_grad_clip* d, size_t* bytes);
  *   Y            M x N of `type` (IGC_F16 or IGC_BF16), or NULL
  *   mean, rstd   fp32 vectors of length M for the backward pass, or NULL
  *   Q, scale     int8 M x N and fp32 of length M: the rows of y, rounded to `type`,
- *                in 8 bits as quantize_rows leaves them; or NULL
- * The statistics are held in fp32 and the deviations taken from the row's own mean.
- * A row with an infinity or NaN has NaN in Y, zeros in Q and NaN as its scale.
- * N == 0 leaves mean = 0 and rstd = 1 / sqrt(eps).
+ *                in 8 bits as quantize_rows leaves them; or NULL (scale is set with Q alone)
+ * The statistics are held in fp32 and the deviations taken from the row's own mean;
+ * a row of one 16-bit value has it as its mean and beta as its Y.
+ * A row with an infinity or NaN, or one whose elements' sums pass fp32, has NaN in
+ * Y, zeros in Q and NaN as its scale (its mean and rstd say nothing).  Where the
+ * sums of the squared deviations alone pass fp32, rstd is 0.
+ * N == 0 leaves mean = 0, rstd = 1 / sqrt(eps) and scale = 0.  Matrices of no rows
+ * or no elements may be NULL.
  * Errors: IGC_EINVAL (NULL descriptor or X, no output, negative size, leading
  * dimension below the row length, unknown type, eps negative or not finite,
  * misaligned pointer, Q without scale), IGC_EUNSUPPORTED (too large),
@@ -700,8 +705,10 @@ int quantize_rows(const igc_quantize_rows* d, void* stream);
  *   bias     fp32 of length N, or NULL
  *   R, Y     M x N of y_type: IGC_F16, IGC_BF16 or IGC_F32; R or NULL
  * The workspace is required where its size is not 0: for reductions that are
- * split, and for rows that are not 16-byte aligned or no multiple of 16 long,
- * which are first copied into rows that are.
+ * split, and for operands whose rows are not 16-byte aligned or no multiple of 16
+ * long where these are copied into rows that are.  Such operands are copied or read
+ * where they lie, whichever is estimated to be faster; aligned rows of whole chunks
+ * are the fast ones.
  * Errors: as linear_forward, plus IGC_EINVAL (a scale is NULL, the workspace is
  * missing) and IGC_EOVERFLOW (K > 131071).
  */
